@@ -54,7 +54,9 @@ typedef enum {
   PGEMM_ERR_TIMEOUT = 7, /* a credit wait exceeded its poll limit            */
   PGEMM_ERR_DEVICE = 8,  /* the current device is not gfx950                 */
   PGEMM_ERR_WORKSPACE = 9 /* pgemm_f16_nt_ws_static: the plan's K-split
-                            partial sums exceed the static scratch          */
+                            partial sums exceed the static scratch; fused
+                            operators: the stream's registered workspace is
+                            missing or smaller than pgemm_fused_workspace   */
 } pgemm_status;
 
 /* Variant codes used by the query functions. */
@@ -287,6 +289,112 @@ typedef struct {
 
 pgemm_status pgemm_plan_arena(int32_t n, const pgemm_lds_block *blocks, int64_t *offsets,
                               int64_t *arena_bytes, int64_t *no_reuse_bytes);
+
+/*
+ * Fused operators: the products around a model's feed-forward block and its
+ * loss, with what surrounds them in the same kernels.
+ *
+ * Rules beyond the common ones above
+ *   - Matrices are row-major and contiguous, M rows of tokens; weights have
+ *     one row per output feature, as rhs in the NT calls.  Any sizes: odd
+ *     widths and tails cost a padded copy of an operand, or guarded loads.
+ *     D, 2 F (gated) at most 2^22, other sizes below 2^31; M rows of a q4 call
+ *     at most 2^20 - 16.
+ *   - All sums, statistics and activations are fp32; a result is rounded to
+ *     its type once.  The backward calls also round the derivative by the
+ *     projections or logits to the operand type, since they multiply by it.
+ *   - Pointers are 16-byte aligned and outputs do not overlap inputs.  An
+ *     empty matrix's pointer may be NULL.
+ *   - Some calls need a workspace: pgemm_fused_workspace gives its bytes, and
+ *     the stream's registered workspace (pgemm_set_workspace) has to have
+ *     them; otherwise PGEMM_ERR_WORKSPACE, with nothing enqueued.
+ */
+typedef enum {
+  PGEMM_ACT_SILU = 0, /* a(g) = g / (1 + e^-g)                                       */
+  PGEMM_ACT_GELU = 1  /* a(g) = g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2      */
+} pgemm_act;
+
+/* Operators that may need a workspace; (M, N, K) is (M, F, D) or (M, V, D). */
+typedef enum {
+  PGEMM_FUSED_GATED = 0,      /* pgemm_*_gated without saved */
+  PGEMM_FUSED_GATED_SAVE = 1, /* pgemm_*_gated with saved    */
+  PGEMM_FUSED_GATED_BWD = 2,
+  PGEMM_FUSED_XENT = 3,
+  PGEMM_FUSED_XENT_BWD = 4
+} pgemm_fused_op;
+
+pgemm_status pgemm_fused_workspace(pgemm_fused_op op, int64_t M, int64_t N, int64_t K, int64_t *bytes);
+
+/*
+ * Gated feed-forward block, both projections and the product in one kernel:
+ *     h = a(x Wg^T) * (x Wu^T)
+ *   x: [M, D]; w: [2 F, D], the F gate rows and then the F up rows;
+ *   h: [M, F]; act: a pgemm_act.  saved: NULL, or fp32 of 2 M (F rounded up
+ *   to 4) values that keep both projections for the backward call (their
+ *   layout is the library's).
+ */
+pgemm_status pgemm_f16_gated(const uint16_t *x, const uint16_t *w, uint16_t *h, float *saved, int64_t M, int64_t F,
+                             int64_t D, int act, void *stream);
+pgemm_status pgemm_bf16_gated(const uint16_t *x, const uint16_t *w, uint16_t *h, float *saved, int64_t M, int64_t F,
+                              int64_t D, int act, void *stream);
+
+/*
+ * Its gradients for dh [M, F]: dx [M, D], dw [2 F, D].  saved: what the
+ * forward call kept, or NULL to compute the projections again.
+ */
+pgemm_status pgemm_f16_gated_bwd(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const float *saved,
+                                 uint16_t *dx, uint16_t *dw, int64_t M, int64_t F, int64_t D, int act, void *stream);
+pgemm_status pgemm_bf16_gated_bwd(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const float *saved,
+                                  uint16_t *dx, uint16_t *dw, int64_t M, int64_t F, int64_t D, int act, void *stream);
+
+/*
+ * Softmax cross entropy of the logits z = x W^T, which are never stored:
+ *     lse[m] = log sum_v e^z[m, v],   loss[m] = lse[m] - z[m, target[m]]
+ *   x: [M, D]; w: [V, D], V >= 1; target: int64 [M]; loss, lse: fp32 [M].
+ *   A target equal to ignore_index does not count: its loss is 0 and it adds
+ *   nothing to the gradients.  Any other target outside 0 .. V-1 makes its
+ *   loss NaN, and every gradient that it reaches.
+ */
+pgemm_status pgemm_f16_xent(const uint16_t *x, const uint16_t *w, const int64_t *target, float *loss, float *lse,
+                            int64_t M, int64_t V, int64_t D, int64_t ignore_index, void *stream);
+pgemm_status pgemm_bf16_xent(const uint16_t *x, const uint16_t *w, const int64_t *target, float *loss, float *lse,
+                             int64_t M, int64_t V, int64_t D, int64_t ignore_index, void *stream);
+
+/*
+ * Its gradients: dx [M, D] and dw [V, D] for dloss, fp32 [M] (dloss_step 1)
+ * or one value that all rows share (dloss_step 0), 4-byte aligned.  lse: from
+ * the forward call.  The logits are computed again in pieces of the
+ * vocabulary.  dloss = 0 gives a row no gradient whatever its logits are.
+ */
+pgemm_status pgemm_f16_xent_bwd(const float *dloss, int dloss_step, const uint16_t *x, const uint16_t *w,
+                                const int64_t *target, const float *lse, uint16_t *dx, uint16_t *dw, int64_t M,
+                                int64_t V, int64_t D, int64_t ignore_index, void *stream);
+pgemm_status pgemm_bf16_xent_bwd(const float *dloss, int dloss_step, const uint16_t *x, const uint16_t *w,
+                                 const int64_t *target, const float *lse, uint16_t *dx, uint16_t *dw, int64_t M,
+                                 int64_t V, int64_t D, int64_t ignore_index, void *stream);
+
+/*
+ * Products of few tokens with 4-bit weights:
+ *     out[m, n] = sum over groups G of scale[n, G] * sum over k in G of x[m, k] (q[n, k] - zero[n, G])
+ *   x: [M, K]; q: [N, B] bytes, B = 16 ceil(K / 32), weight k of a row in the
+ *   low (even k) or high (odd k) four bits of byte k / 2, the row's last bytes
+ *   unused; scale: [N, ceil(K / group)] of x's type; zero: bytes of the same
+ *   shape, or NULL for 8 everywhere; group: a multiple of 32; out: [M, N].
+ *   Weights enter the products as exact integers; each group's fp32 sum is
+ *   scaled in fp32.  The call suits few rows: the weights are read once per
+ *   64 of them.
+ */
+pgemm_status pgemm_f16_q4(const uint16_t *x, const uint8_t *q, const uint16_t *scale, const uint8_t *zero,
+                          uint16_t *out, int64_t M, int64_t N, int64_t K, int64_t group, void *stream);
+pgemm_status pgemm_bf16_q4(const uint16_t *x, const uint8_t *q, const uint16_t *scale, const uint8_t *zero,
+                           uint16_t *out, int64_t M, int64_t N, int64_t K, int64_t group, void *stream);
+
+/* The gated block on 4-bit weights: q, scale and zero have 2 F rows, the gate
+ * rows first; out: [M, F]. */
+pgemm_status pgemm_f16_q4_gated(const uint16_t *x, const uint8_t *q, const uint16_t *scale, const uint8_t *zero,
+                                uint16_t *out, int64_t M, int64_t F, int64_t K, int64_t group, int act, void *stream);
+pgemm_status pgemm_bf16_q4_gated(const uint16_t *x, const uint8_t *q, const uint16_t *scale, const uint8_t *zero,
+                                 uint16_t *out, int64_t M, int64_t F, int64_t K, int64_t group, int act, void *stream);
 
 const char *pgemm_strerror(pgemm_status status);
 int pgemm_abi_version(void);

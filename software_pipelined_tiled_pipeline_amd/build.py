@@ -1,9 +1,10 @@
 """Builds libpgemm.so (HIP, gfx950 only) in-tree with hipcc.
 
-The library is five translation units: the C ABI (argument checks,
-planning, the int32 kernel) and four units of NT kernel instances (f16 and
-bf16, each with the direct-to-LDS and the register-staged loader).  They are
-compiled in parallel and linked into one shared library.
+The library is twelve translation units: the C ABI of the products (argument
+checks, planning, the int32 kernel), four units of NT kernel instances (f16
+and bf16, each with the direct-to-LDS and the register-staged loader), the C
+ABI of the fused operators, and their instances by operator and type.  They
+are compiled in parallel and linked into one shared library.
 """
 from __future__ import annotations
 
@@ -17,7 +18,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 UNITS = ["pgemm_api.hip", "inst_f16_direct.hip", "inst_f16_staged.hip", "inst_bf16_direct.hip",
-         "inst_bf16_staged.hip"]
+         "inst_bf16_staged.hip", "fused_api.hip", "fused_gated_f16.hip", "fused_gated_bf16.hip", "fused_xent_f16.hip",
+         "fused_xent_bf16.hip", "fused_q4_f16.hip", "fused_q4_bf16.hip"]
 LIB = os.path.join(HERE, "libpgemm.so")
 
 HIPCC_FLAGS = [

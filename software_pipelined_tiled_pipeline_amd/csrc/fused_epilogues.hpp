@@ -1,0 +1,356 @@
+// Epilogues of the fused products.  Each gets a wave's settled accumulators:
+// lane l, register r of acc[i][j] is row 16 i + l % 16 and column
+// 16 j + 4 (l / 16) + r of the wave's block; the ring is free for staging.
+#pragma once
+
+#include "fused_gemm.hpp"
+
+namespace pgemm {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// e^x through v_exp_f32 (2^x): the product's rounding costs |x| 2^-24.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// The gate's activation and its derivative in fp32.  act 0: silu, g s(g);
+// act 1: gelu in its tanh form, (1 + tanh y) / 2 = s(2 y).  The derivative's
+// polynomial is taken at |g| <= 64 so that its square does not overflow into
+// 0 * inf where s (1 - s) has long vanished.
+struct Activation {
+  float a, d;
+};
+__device__ __forceinline__ float gate_sigmoid(int act, float g) {
+  const float y = act == 0 ? g : 1.5957691216057308f * g * (1.0f + 0.044715f * g * g);
+  return __builtin_amdgcn_rcpf(1.0f + fast_exp(-y));
+}
+__device__ __forceinline__ float activate(int act, float g) { return g * gate_sigmoid(act, g); }
+__device__ __forceinline__ Activation activate_slope(int act, float g) {
+  const float s = gate_sigmoid(act, g);
+  float q = 1.0f;
+  if (act != 0) {
+    const float c = fminf(fmaxf(g, -64.0f), 64.0f);
+    q = 1.5957691216057308f * (1.0f + 0.134145f * c * c);
+  }
+  return Activation{g * s, s + g * (s * (1.0f - s)) * q};
+}
+
+// fp32 of a 16-bit value
+template <typename T>
+__device__ __forceinline__ float widen(uint16_t v) {
+  return (float)__builtin_bit_cast(T, v);
+}
+
+// Copies columns [c0, c0 + BN) of a staged tile to out[m0..][n0..], row pitch
+// `po`: whole 16-byte pieces wherever they start (an odd pitch leaves them
+// at even addresses), single elements at the right edge.
+template <int BM, int BN, int THREADS>
+__device__ __forceinline__ void store_tile(const char *st, int pitch, int c0, uint16_t *out, int64_t po, int M, int N,
+                                           int m0, int n0, int tid) {
+  constexpr int CH = BN / 8;
+  for (int idx = tid; idx < BM * CH; idx += THREADS) {
+    const int row = idx / CH, c = idx % CH;
+    const int gm = m0 + row, gn = n0 + 8 * c;
+    if (gm >= M || gn >= N) continue;
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(st + row * pitch + (c0 + 8 * c) * 2);
+    uint16_t *dst = out + (int64_t)gm * po + gn;
+    if (gn + 8 <= N) {
+      *reinterpret_cast<u32x4_any *>(dst) = v;
+    } else {
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (gn + x < N) dst[x] = (uint16_t)(v[x / 2] >> (16 * (x % 2)));
+    }
+  }
+}
+
+// out = round((sum + acc) * *scale): one product, or the last of several whose
+// running sum is kept in fp32 (SumEpi).
+struct StoreEpi {
+  struct Args {
+    uint16_t *out;
+    int64_t po;
+    const float *scale;  // one device float, or null
+  };
+  template <typename T, class G, class W>
+  struct Run {
+    // `sum`: null, or what to add, row pitch ps (a multiple of 4)
+    __device__ __forceinline__ static void finish(W &w, const Args &e, const FusedProduct &g, char *smem, int m0,
+                                                  int n0, int wm, int wn, int lane, int tid, const float *sum, int ps) {
+      constexpr int PITCH = Staging<G::BN>::PITCH;
+      const float k = e.scale ? *e.scale : 1.0f;
+      const int lr = wm * G::WM + (lane & 15), lc = wn * G::WN + 4 * (lane >> 4);
+#pragma unroll
+      for (int i = 0; i < W::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < W::TN; ++j) {
+          f32x4 v = w.acc[i][j];
+          const int row = m0 + lr + 16 * i, col = n0 + lc + 16 * j;
+          if (sum && row < g.M && col < g.N) v += *reinterpret_cast<const f32x4 *>(sum + (int64_t)row * ps + col);
+          *reinterpret_cast<u32x2 *>(smem + (lr + 16 * i) * PITCH + (lc + 16 * j) * 2) =
+              Mfma<T>::pack4(v[0] * k, v[1] * k, v[2] * k, v[3] * k);
+        }
+      __syncthreads();
+      store_tile<G::BM, G::BN, G::THREADS>(smem, PITCH, 0, e.out, e.po, g.M, g.N, m0, n0, tid);
+    }
+    __device__ __forceinline__ void operator()(W &w, const Args &e, const FusedProduct &g, char *smem, int m0, int n0,
+                                               int wm, int wn, int lane, int tid) const {
+      finish(w, e, g, smem, m0, n0, wm, wn, lane, tid, nullptr, 0);
+    }
+  };
+};
+
+// A sum over several products: the running fp32 sum lives in `sum` (row
+// pitch a multiple of 4).  first: nothing to add yet; last: rounds to out.
+struct SumEpi {
+  struct Args {
+    float *sum;
+    int ps;
+    int first, last;
+    StoreEpi::Args out;
+  };
+  template <typename T, class G, class W>
+  struct Run {
+    __device__ __forceinline__ void operator()(W &w, const Args &e, const FusedProduct &g, char *smem, int m0, int n0,
+                                               int wm, int wn, int lane, int tid) const {
+      if (e.last) {
+        StoreEpi::Run<T, G, W>::finish(w, e.out, g, smem, m0, n0, wm, wn, lane, tid, e.sum, e.ps);
+        return;
+      }
+#pragma unroll
+      for (int i = 0; i < W::TM; ++i) {
+        const int row = m0 + wm * G::WM + 16 * i + (lane & 15);
+        if (row >= g.M) continue;
+        float *rp = e.sum + (int64_t)row * e.ps;
+#pragma unroll
+        for (int j = 0; j < W::TN; ++j) {
+          const int col = n0 + wn * G::WN + 16 * j + 4 * (lane >> 4);
+          if (col >= g.N) continue;
+          f32x4 v = w.acc[i][j];
+          if (!e.first) v += *reinterpret_cast<const f32x4 *>(rp + col);
+          *reinterpret_cast<f32x4 *>(rp + col) = v;
+        }
+      }
+    }
+  };
+};
+
+// Gated block: even column blocks of a wave hold the gate, odd ones the up
+// projection of the same 16 hidden columns.  h = act(gate) * up; `saved`
+// (null: not kept) takes both projections in fp32, per row and group of four
+// hidden columns the four gates and then the four ups, for the backward pass.
+struct GatedEpi {
+  struct Args {
+    uint16_t *h;
+    float *saved;
+    int act;
+  };
+  template <typename T, class G, class W>
+  struct Run {
+    __device__ __forceinline__ void operator()(W &w, const Args &e, const FusedProduct &g, char *smem, int m0, int n0,
+                                               int wm, int wn, int lane, int tid) const {
+      constexpr int ON = G::BN / 2, PITCH = Staging<ON>::PITCH;
+      const int r = lane & 15, q = lane >> 4;
+      const int64_t ps = (int64_t)((g.N + 3) / 4) * 8;
+#pragma unroll
+      for (int i = 0; i < W::TM; ++i) {
+        const int lrow = wm * G::WM + 16 * i + r;
+#pragma unroll
+        for (int p = 0; p < W::TN / 2; ++p) {
+          const f32x4 ga = w.acc[i][2 * p], up = w.acc[i][2 * p + 1];
+          const int lcol = wn * (G::WN / 2) + 16 * p + 4 * q;
+          if (e.saved && m0 + lrow < g.M && n0 + lcol < g.N) {
+            float *sp = e.saved + (m0 + lrow) * ps + (int64_t)(n0 + lcol) * 2;
+            *reinterpret_cast<f32x4 *>(sp) = ga;
+            *reinterpret_cast<f32x4 *>(sp + 4) = up;
+          }
+          f32x4 h;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) h[x] = activate(e.act, ga[x]) * up[x];
+          *reinterpret_cast<u32x2 *>(smem + lrow * PITCH + lcol * 2) = Mfma<T>::pack4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      __syncthreads();
+      store_tile<G::BM, ON, G::THREADS>(smem, PITCH, 0, e.h, g.N, g.M, g.N, m0, n0, tid);
+    }
+  };
+};
+
+// The gated block's derivative from recomputed projections: with dh read
+// here, dy[m] = [dh up act'(gate) | dh act(gate)], one row of 2 N values.
+struct GatedSlopeEpi {
+  struct Args {
+    const uint16_t *dh;
+    uint16_t *dy;
+    int64_t py;
+    int act;
+  };
+  template <typename T, class G, class W>
+  struct Run {
+    __device__ __forceinline__ void operator()(W &w, const Args &e, const FusedProduct &g, char *smem, int m0, int n0,
+                                               int wm, int wn, int lane, int tid) const {
+      constexpr int ON = G::BN / 2, PITCH = Staging<G::BN>::PITCH;
+      const int r = lane & 15, q = lane >> 4;
+#pragma unroll
+      for (int i = 0; i < W::TM; ++i) {
+        const int lrow = wm * G::WM + 16 * i + r;
+#pragma unroll
+        for (int p = 0; p < W::TN / 2; ++p) {
+          const f32x4 ga = w.acc[i][2 * p], up = w.acc[i][2 * p + 1];
+          const int lcol = wn * (G::WN / 2) + 16 * p + 4 * q;
+          const int gm = m0 + lrow, gn = n0 + lcol;
+          f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (gm < g.M && gn < g.N) {
+            const uint16_t *src = e.dh + (int64_t)gm * g.N + gn;
+            if (gn + 4 <= g.N) {
+              const u32x2 v = *reinterpret_cast<const u32x2_any *>(src);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) d[x] = widen<T>((uint16_t)(v[x / 2] >> (16 * (x % 2))));
+            } else {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (gn + x < g.N) d[x] = widen<T>(src[x]);
+            }
+          }
+          f32x4 dg, du;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const Activation v = activate_slope(e.act, ga[x]);
+            dg[x] = d[x] * up[x] * v.d;
+            du[x] = d[x] * v.a;
+          }
+          char *st = smem + lrow * PITCH + lcol * 2;
+          *reinterpret_cast<u32x2 *>(st) = Mfma<T>::pack4(dg[0], dg[1], dg[2], dg[3]);
+          *reinterpret_cast<u32x2 *>(st + ON * 2) = Mfma<T>::pack4(du[0], du[1], du[2], du[3]);
+        }
+      }
+      __syncthreads();
+      store_tile<G::BM, ON, G::THREADS>(smem, PITCH, 0, e.dy, e.py, g.M, g.N, m0, n0, tid);
+      store_tile<G::BM, ON, G::THREADS>(smem, PITCH, ON, e.dy + g.N, e.py, g.M, g.N, m0, n0, tid);
+    }
+  };
+};
+
+// Softmax statistics of a tile of logits: per row and wave column the
+// largest logit and the sum of e^(z - largest), and the target's logit.
+struct LseEpi {
+  struct Args {
+    float2 *part;  // [tiles_n * WGN][M]
+    float *at;     // [M] the target's logit
+    const int64_t *target;
+  };
+  template <typename T, class G, class W>
+  struct Run {
+    __device__ __forceinline__ void operator()(W &w, const Args &e, const FusedProduct &g, char *smem, int m0, int n0,
+                                               int wm, int wn, int lane, int tid) const {
+      const int r = lane & 15, q = lane >> 4;
+      const int c0 = n0 + wn * G::WN + 4 * q;
+      const bool edge = n0 + G::BN > g.N;
+      float2 *part = e.part + (int64_t)((n0 / G::BN) * G::WGN + wn) * g.M;
+#pragma unroll
+      for (int i = 0; i < W::TM; ++i) {
+        const int row = m0 + wm * G::WM + 16 * i + r;
+        const bool in = row < g.M;
+        const int64_t t = in ? e.target[row] - c0 : -1;
+        const int tc = t >= 0 && t < G::WN ? (int)t : -1;  // column within the lane's blocks
+        float top = -INFINITY, z = 0.0f;
+        bool mine = false;
+#pragma unroll
+        for (int j = 0; j < W::TN; ++j)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float v = w.acc[i][j][x];
+            if (edge && c0 + 16 * j + x >= g.N) v = -INFINITY;
+            if (tc == 16 * j + x) {
+              z = v;
+              mine = true;
+            }
+            top = fmaxf(top, v);  // a NaN shows in the sum
+          }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float ref = top == -INFINITY ? 0.0f : top;  // no finite logit here: the sum is zero, not 0/0
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < W::TN; ++j)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float v = w.acc[i][j][x];
+            if (edge && c0 + 16 * j + x >= g.N) v = -INFINITY;
+            sum += fast_exp(v - ref);
+          }
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (in && q == 0) part[row] = make_float2(top, sum);
+        if (in && mine) e.at[row] = z;
+      }
+    }
+  };
+};
+
+// The loss's derivative by a tile of logits, dz = s (e^(z - lse) - [v = t])
+// with s = kDzUnit dloss / *top (0 for an ignored row, NaN for a target
+// outside the vocabulary), rounded to T; the products after it multiply by
+// *top / kDzUnit again.  *top is the largest |dloss|: with the usual dloss, the
+// same for all rows, s is a power of two and an improbable target's entry,
+// close to -s, rounds to next to nothing, where -dloss itself would give
+// every row the same rounding error (measured: 3.0e-3 off instead of 1.7e-3
+// over the whole gradient in bf16).  Columns from N up to 8 are zeros.
+//
+// kDzUnit: binary16 ends at 2^-24, and most entries of a large vocabulary are
+// far smaller than 1; bf16 has fp32's range.
+template <typename T>
+constexpr float kDzUnit = std::is_same_v<T, _Float16> ? 16384.0f : 1.0f;
+
+struct SlopeEpi {
+  struct Args {
+    uint16_t *dz;
+    int64_t pz;
+    const float *lse, *dloss;
+    int dstep;  // 1, or 0 for one dloss shared by all rows
+    const int64_t *target;
+    const float *top;
+    int64_t ignore, v0, V;  // the piece's first vocabulary row; the whole vocabulary
+  };
+  template <typename T, class G, class W>
+  struct Run {
+    __device__ __forceinline__ void operator()(W &w, const Args &e, const FusedProduct &g, char *smem, int m0, int n0,
+                                               int wm, int wn, int lane, int tid) const {
+      const int r = lane & 15, q = lane >> 4;
+      const int c0 = n0 + wn * G::WN + 4 * q;
+      const bool edge = n0 + G::BN > g.N;
+      const float top = *e.top;
+#pragma unroll
+      for (int i = 0; i < W::TM; ++i) {
+        const int row = m0 + wm * G::WM + 16 * i + r;
+        float s = 0.0f, lse = 0.0f;
+        int tc = -1;
+        if (row < g.M) {
+          const int64_t t = e.target[row];
+          lse = e.lse[row];
+          s = t == e.ignore ? 0.0f : (t < 0 || t >= e.V) ? NAN : e.dloss[(int64_t)row * e.dstep] / top * kDzUnit<T>;
+          const int64_t d = t - e.v0 - c0;
+          tc = d >= 0 && d < G::WN ? (int)d : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < W::TN; ++j) {
+          f32x4 v;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float p = fast_exp(w.acc[i][j][x] - lse);
+            if (tc == 16 * j + x) p -= 1.0f;
+            p = s == 0.0f ? 0.0f : p * s;  // an ignored row is zero whatever its logits are
+            if (edge && c0 + 16 * j + x >= g.N) p = 0.0f;
+            v[x] = p;
+          }
+          char *dst = smem + (wm * G::WM + 16 * i + r) * Staging<G::BN>::PITCH + (wn * G::WN + 16 * j + 4 * q) * 2;
+          *reinterpret_cast<u32x2 *>(dst) = Mfma<T>::pack4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      __syncthreads();
+      store_tile<G::BM, G::BN, G::THREADS>(smem, Staging<G::BN>::PITCH, 0, e.dz, e.pz, g.M, (g.N + 7) / 8 * 8, m0, n0,
+                                           tid);
+    }
+  };
+};
+
+}  // namespace pgemm

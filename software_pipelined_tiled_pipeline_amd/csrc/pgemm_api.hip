@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "pgemm.h"
+#include "fused.hpp"
 #include "instances.hpp"
 #include "launch.hpp"
 #include "planner.hpp"
@@ -372,6 +373,20 @@ pgemm_status nt_entry(Elem e, pgemm_op op, const uint16_t *lhs, const uint16_t *
 
 }  // namespace
 
+namespace pgemm {
+
+pgemm_status checked_device(int *dev) { return current_device(dev); }
+
+pgemm_status stream_workspace(int dev, void *stream, int64_t bytes, std::unique_lock<std::mutex> *lock, char **ws) {
+  *lock = std::unique_lock<std::mutex>(g_work_mutex);
+  const Workspace *w = find_workspace(dev, stream);
+  if (!w || w->bytes < bytes) return PGEMM_ERR_WORKSPACE;
+  *ws = reinterpret_cast<char *>(w->ptr);
+  return PGEMM_OK;
+}
+
+}  // namespace pgemm
+
 extern "C" {
 
 pgemm_status pgemm_s32_nn(const int32_t *lhs, const int32_t *rhs, int32_t *out, int64_t M, int64_t N, int64_t K,
@@ -529,14 +544,14 @@ const char *pgemm_strerror(pgemm_status status) {
   switch (status) {
     case PGEMM_OK: return "ok";
     case PGEMM_ERR_NULL: return "a required pointer is NULL";
-    case PGEMM_ERR_SHAPE: return "M, N or K out of range, or an unsupported tiling request";
+    case PGEMM_ERR_SHAPE: return "a size, group, activation or step out of range, or an unsupported tiling request";
     case PGEMM_ERR_STAGES: return "unsupported number of stages";
     case PGEMM_ERR_ALIGN: return "pointer not 16-byte aligned";
     case PGEMM_ERR_LDS: return "tile ring exceeds the LDS budget";
     case PGEMM_ERR_LAUNCH: return "HIP launch or query failed";
     case PGEMM_ERR_TIMEOUT: return "a credit wait exceeded its poll limit";
     case PGEMM_ERR_DEVICE: return "current device is not gfx950";
-    case PGEMM_ERR_WORKSPACE: return "the K-split partial sums exceed the static scratch (PGEMM_STATIC_SCRATCH_BYTES)";
+    case PGEMM_ERR_WORKSPACE: return "the workspace is too small: the static scratch for these K-split partial sums, or the stream's registered one for a fused operator";
   }
   return "unknown status";
 }

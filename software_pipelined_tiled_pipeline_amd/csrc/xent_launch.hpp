@@ -1,0 +1,159 @@
+// The cross entropy and its gradients: row kernels and launches.
+#pragma once
+
+#include "fused_rows.hpp"
+
+namespace pgemm {
+
+// Joins the tiles' softmax statistics of 64 rows per workgroup: each of its
+// 16 waves runs through every 16th part, then the waves' are joined.
+//   lse = log sum_v e^(z_v), loss = lse - z_target (0 for an ignored row, NaN
+// for a target outside the vocabulary).
+template <typename T>
+__global__ void __launch_bounds__(1024) lse_join_kernel(const float2 *__restrict__ part, const float *__restrict__ at,
+                                                        const int64_t *__restrict__ target, float *__restrict__ loss,
+                                                        float *__restrict__ lse, int64_t M, int64_t V, int parts,
+                                                        int64_t ignore) {
+  __shared__ float tops[16][64], sums[16][64];
+  const int r = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t row = (int64_t)blockIdx.x * 64 + r;
+  float top = -INFINITY, sum = 0.0f;
+  auto join = [&](float t, float s) {
+    const float m = fmaxf(top, t);
+    const float ref = m == -INFINITY ? 0.0f : m;
+    sum = sum * fast_exp(top - ref) + s * fast_exp(t - ref);
+    top = m;
+  };
+  if (row < M) {
+#pragma unroll 4
+    for (int p = w; p < parts; p += 16) {
+      const float2 v = part[(int64_t)p * M + row];
+      join(v.x, v.y);
+    }
+  }
+  tops[w][r] = top;
+  sums[w][r] = sum;
+  __syncthreads();
+  if (w == 0 && row < M) {
+#pragma unroll
+    for (int p = 1; p < 16; ++p) join(tops[p][r], sums[p][r]);
+    const float l = top + logf(sum);
+    const int64_t t = target[row];
+    lse[row] = l;
+    loss[row] = t == ignore ? 0.0f : (t < 0 || t >= V) ? NAN : l - at[row];
+  }
+}
+
+// scale[0] = the largest |dloss| of the rows that count (1 if there is none
+// or it is not finite), scale[1] = scale[0] / kDzUnit<T>: see SlopeEpi.
+template <typename T>
+__global__ void __launch_bounds__(1024) loss_scale_kernel(const float *__restrict__ dloss, int dstep,
+                                                          const int64_t *__restrict__ target, int64_t M, int64_t ignore,
+                                                          float *__restrict__ scale) {
+  __shared__ float tops[16];
+  float top = 0.0f;
+  for (int64_t i = threadIdx.x; i < M; i += 1024)
+    if (target[i] != ignore) top = fmaxf(top, fabsf(dloss[i * dstep]));
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, tops[i]);
+    if (!(top > 0.0f && top < INFINITY)) top = 1.0f;
+    scale[0] = top;
+    scale[1] = top / kDzUnit<T>;
+  }
+}
+
+namespace launch_detail {
+
+template <typename T>
+pgemm_status xent_operands(const XentCall &c, const XentPlan &p, const uint16_t **x, const uint16_t **w) {
+  *x = c.x;
+  *w = c.w;
+  if (!p.padded) return PGEMM_OK;
+  pgemm_status st = pad_rows(c.x, c.ws + p.x, c.M, c.D, p.d8, c.stream);
+  if (st == PGEMM_OK) st = pad_rows(c.w, c.ws + p.w, c.V, c.D, p.d8, c.stream);
+  *x = reinterpret_cast<const uint16_t *>(c.ws + p.x);
+  *w = reinterpret_cast<const uint16_t *>(c.ws + p.w);
+  return st;
+}
+
+template <typename T>
+pgemm_status xent_forward(const XentCall &c) {
+  const XentPlan p = plan_xent(c.M, c.V, c.D, false);
+  const uint16_t *x, *w;
+  pgemm_status st = xent_operands<T>(c, p, &x, &w);
+  if (st != PGEMM_OK) return st;
+  float2 *part = reinterpret_cast<float2 *>(c.ws + p.part);
+  float *at = reinterpret_cast<float *>(c.ws + p.at);
+  FusedProduct g{};
+  g.a = FusedOperand{x, nullptr, (int)p.d8, (int)c.M};
+  g.b = FusedOperand{w, nullptr, (int)p.d8, (int)c.V};
+  g.M = (int)c.M;
+  g.N = (int)c.V;
+  g.K = (int)p.d8;
+  st = launch_product<T, Lay::KC, Lay::KC, false, LseEpi>(g, LseEpi::Args{part, at, c.target}, c.stream, c.dev);
+  if (st != PGEMM_OK) return st;
+  hipLaunchKernelGGL(lse_join_kernel<T>, dim3((unsigned)per(c.M, 64)), dim3(1024), 0, c.stream, part, at, c.target, c.loss,
+                     c.lse, c.M, c.V, (int)p.parts, c.ignore);
+  return launched();
+}
+
+template <typename T>
+pgemm_status xent_backward(const XentCall &c) {
+  const XentPlan p = plan_xent(c.M, c.V, c.D, true);
+  const uint16_t *x, *w;
+  pgemm_status st = xent_operands<T>(c, p, &x, &w);
+  if (st != PGEMM_OK) return st;
+  uint16_t *dz = reinterpret_cast<uint16_t *>(c.ws + p.dz);
+  float *sum = reinterpret_cast<float *>(c.ws + p.sum);
+  float *scale = reinterpret_cast<float *>(c.ws + p.scale);
+  hipLaunchKernelGGL(loss_scale_kernel<T>, dim3(1), dim3(1024), 0, c.stream, c.dloss, c.dstep, c.target, c.M, c.ignore,
+                     scale);
+  st = launched();
+  if (st != PGEMM_OK) return st;
+  const float *unscale = scale + 1;
+  for (int64_t v0 = 0; v0 < c.V; v0 += p.piece) {
+    const int64_t n = c.V - v0 < p.piece ? c.V - v0 : p.piece;
+    const uint16_t *wp = w + v0 * p.d8;
+    FusedProduct g{};
+    // dz of this piece, from its recomputed logits
+    g.a = FusedOperand{x, nullptr, (int)p.d8, (int)c.M};
+    g.b = FusedOperand{wp, nullptr, (int)p.d8, (int)n};
+    g.M = (int)c.M;
+    g.N = (int)n;
+    g.K = (int)p.d8;
+    st = launch_product<T, Lay::KC, Lay::KC, false, SlopeEpi>(
+        g, SlopeEpi::Args{dz, p.pz, c.lse_in, c.dloss, c.dstep, c.target, scale, c.ignore, v0, c.V}, c.stream, c.dev);
+    if (st != PGEMM_OK) return st;
+    // dW rows of this piece = dz^T x
+    g.a = FusedOperand{dz, nullptr, (int)p.pz, (int)n};
+    g.b = FusedOperand{x, nullptr, (int)p.d8, (int)c.D};
+    g.M = (int)n;
+    g.N = (int)c.D;
+    g.K = (int)c.M;
+    st = launch_product<T, Lay::KR, Lay::KR, false, StoreEpi>(g, StoreEpi::Args{c.dw + v0 * c.D, c.D, unscale},
+                                                              c.stream, c.dev);
+    if (st != PGEMM_OK) return st;
+    // dx += dz W
+    g.a = FusedOperand{dz, nullptr, (int)p.pz, (int)c.M};
+    g.b = FusedOperand{wp, nullptr, (int)p.d8, (int)c.D};
+    g.M = (int)c.M;
+    g.N = (int)c.D;
+    g.K = (int)n;
+    const StoreEpi::Args out{c.dx, c.D, unscale};
+    const bool first = v0 == 0, last = v0 + n == c.V;
+    if (first && last)
+      st = launch_product<T, Lay::KC, Lay::KR, false, StoreEpi>(g, out, c.stream, c.dev);
+    else
+      st = launch_product<T, Lay::KC, Lay::KR, false, SumEpi>(g, SumEpi::Args{sum, (int)p.ps, first, last, out},
+                                                              c.stream, c.dev);
+    if (st != PGEMM_OK) return st;
+  }
+  return PGEMM_OK;
+}
+
+}  // namespace launch_detail
+}  // namespace pgemm

@@ -16,6 +16,9 @@ from __future__ import annotations
 import ctypes
 import os
 
+from . import fused
+from .fused import pack_q4  # noqa: F401
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpgemm.so")
 
@@ -57,6 +60,7 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.argtypes = [P, P, P, I64, I64, I64, I, P]
             f.restype = I
+        fused.declare(L)
         L.pgemm_query.argtypes = [I, I, I64, I64, I64, ctypes.POINTER(KernelInfo)]
         L.pgemm_query.restype = I
         L.pgemm_debug_status.argtypes = [P]
@@ -202,6 +206,10 @@ def pgemm_f16_nt_ws_static(lhs, rhs, out=None, stages: int = 0, stream=None):
 
 pgemm_bf16_nt = _nt("pgemm_bf16_nt", "bfloat16")
 pgemm_bf16_nt_ws = _nt("pgemm_bf16_nt_ws", "bfloat16")
+
+
+# the fused operators: pgemm_{f16,bf16}_{gated,gated_bwd,xent,xent_bwd,q4,q4_gated}
+globals().update(fused.FUNCTIONS)
 
 
 def pgemm_query(op: str, stages: int, M: int, N: int, K: int) -> dict:
