@@ -62,6 +62,13 @@ struct KRows {
   __device__ __forceinline__ static int f(int k) { return (k & 3) | (((k >> 3) & FMASK) << 2); }
 };
 
+__device__ __forceinline__ const char *wave_uniform(const char *p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+  return reinterpret_cast<const char *>((uint64_t)hi << 32 | lo);
+}
+
 // Fills ring slots with direct-to-LDS loads.  The first half of the waves
 // load the A tile, the second half the B tile, PER instructions each; what a
 // lane adds to the tile's start is worked out once per instruction.  The
@@ -137,6 +144,14 @@ struct FusedLoader {
       lay_out<LA, G::BM, false>(g.a, m0, wave * PER);
     else
       lay_out<LB, G::BN, DUAL>(g.b, n0, (wave - WAVES / 2) * PER);
+    // one operand per wave: the same in every lane, which the compiler cannot
+    // see through the choice above (it would loop over the lanes at each load)
+    base = wave_uniform(base);
+    base2 = DUAL ? wave_uniform(base2) : base;
+    step = (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)step);
+    span = (uint32_t)__builtin_amdgcn_readfirstlane((int)span);
+    cut = (uint32_t)__builtin_amdgcn_readfirstlane((int)cut);
+    kc = __builtin_amdgcn_readfirstlane((int)kc) != 0;
   }
 
   // The resource of K tile t (past the end: of no bytes, every lane reads zero).
