@@ -169,7 +169,7 @@ template <typename Launch>
 pgemm_status q4(Launch launch, const uint16_t *x, const uint8_t *q, const uint16_t *scale, const uint8_t *zero,
                 uint16_t *out, int64_t M, int64_t N, int64_t K, int64_t group, bool gated, int act, void *stream) {
   const int64_t rows = gated ? 2 * N : N;
-  if (!dim(M) || !dim(N) || !dim(rows) || !dim(K) || group <= 0 || group % 32 != 0 || !dim(group) || !act_ok(act))
+  if (!dim(M) || !dim(N) || !dim(rows) || !pitch(K) || group <= 0 || group % 32 != 0 || !dim(group) || !act_ok(act))
     return PGEMM_ERR_SHAPE;
   // tokens are the grid's second dimension, at least 16 a workgroup
   if (per(M, 16) > 65535 || per(N, 16) * 512 >= kMaxWorkItems) return PGEMM_ERR_SHAPE;

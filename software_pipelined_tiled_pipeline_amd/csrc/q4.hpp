@@ -1,0 +1,314 @@
+// Products with few rows (tokens) and 4-bit weights with a scale and a zero
+// point per group of a row: out = x W^T, or the gated block on such weights.
+//
+//   out[m][n] = sum over groups G of s[n][G] * sum over k in G of x[m][k] (q[n][k] - z[n][G])
+//
+// Bound by reading the weights once: two of them are a byte, so what a byte
+// costs elsewhere counts four times as much as with 16-bit weights.  A lane
+// that loaded its own weight row's bytes, as the 16-bit kernel does, would
+// make every lane of a load a request of its own, and the address unit, not
+// the memory, would set the pace.  So weights come in whole lines:
+//
+//  * weights: a wave's blocks of 32 weight rows and 128 k (2 KiB) go straight
+//    into a ring of D slots in LDS, four lanes to a row's 64 bytes, and are
+//    read from there as MFMA fragments, a dword of eight weights a lane;
+//  * x: 16 lanes load a token's 128 k; they are put in the fragments' order
+//    and written to LDS;
+//  * scales and zero points of the workgroup's rows are kept in LDS, a dword
+//    each, for CB blocks of K at a time.
+//
+// Waves: KW work on blocks of K in turn and join their sums in LDS at the end;
+// NW beside each other on different weight rows share their tokens in LDS
+// (worth it once reading x again for every 32 weight rows counts: more than
+// 16 tokens).  MT blocks of 16 tokens; XI loads of four tokens each hold them.
+#pragma once
+
+#include "few_rows.hpp"
+
+namespace pgemm {
+
+struct Q4Args {
+  const uint16_t *x;     // [M][K]
+  const uint8_t *q;      // [rows][wb]
+  const uint16_t *scale;  // [rows][groups]
+  const uint8_t *zero;   // [rows][groups], or null (8 everywhere)
+  uint16_t *out;         // [M][N]
+  int M, N, K;           // N output columns; the gated block has 2 N weight rows
+  int wb;                // bytes of a weight row
+  int group, groups;
+  uint64_t per32;        // u * per32 >> 40 is the group of k = 32 u (u up to 2^17)
+  int sp;                // dwords of a row's scales in LDS, odd
+  int act;
+};
+
+// waves a SIMD holds that LDS leaves room for
+constexpr int q4_per_simd(int xi, int nw) { return nw > 1 ? 2 : xi == 1 ? 4 : 3; }
+
+template <typename T, bool GATED, int MT, int GS, int XI, int NW, int KW, int D>
+struct Q4Geom {
+  static constexpr int NT = 2, WAVES = NW * KW, THREADS = WAVES * 64;
+  static constexpr int ROWS = NW * 32;                  // weight rows of a workgroup
+  static constexpr int COLS = GATED ? ROWS / 2 : ROWS;  // output columns
+  static constexpr int CB = NW == 1 ? 64 : 16;          // blocks of K whose scales are kept
+  static constexpr int XBUFS = NW == 1 ? 1 : 2;
+  static constexpr int RING = WAVES * D * 2048;
+  static constexpr int XBYTES = KW * XBUFS * XI * 1024;
+  static constexpr int XW = XI / NW;  // loads of x a wave does for a block
+  static constexpr int JOIN = WAVES * MT * NT * 4 * 256;
+  static_assert(XI % NW == 0 && CB % KW == 0 && (XI == 4 * MT || (MT == 1 && XI == 1)), "");
+};
+
+template <typename T, bool GATED, int MT, int GS, int XI, int NW, int KW, int D>
+__global__ void __launch_bounds__(NW *KW * 64, q4_per_simd(XI, NW)) q4_kernel(Q4Args a) {
+  using G = Q4Geom<T, GATED, MT, GS, XI, NW, KW, D>;
+  using F = Frag8<T>;
+  constexpr int NT = G::NT, SG = 4 / GS, XW = G::XW, CB = G::CB;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wk = wave / NW, wn = wave % NW;
+  const int c = lane & 15, q = lane >> 4;
+  const int n0 = blockIdx.x * G::COLS, m0 = blockIdx.y * MT * 16;
+
+  char *ring = smem + wave * (D * 2048);
+  char *xbuf = smem + G::RING + wk * (G::XBUFS * XI * 1024);
+  uint32_t *scales = reinterpret_cast<uint32_t *>(smem + G::RING + G::XBYTES);
+
+  // first matrix row and rows inside the matrix of this wave's block b
+  auto block_row = [&](int w, int b, int *have) __attribute__((always_inline)) {
+    const int n = n0 + (GATED ? w * 16 : w * 32 + b * 16);
+    *have = a.N - n < 0 ? 0 : a.N - n < 16 ? a.N - n : 16;
+    return (int64_t)n + (GATED && b ? a.N : 0);
+  };
+
+  // weights: lane l brings 16 bytes of row l / 4
+  __amdgpu_buffer_rsrc_t rw[NT];
+#pragma unroll
+  for (int b = 0; b < NT; ++b) {
+    int have;
+    const int64_t row = block_row(wn, b, &have);
+    rw[b] = make_rsrc(wave_uniform(reinterpret_cast<const char *>(a.q) + (have ? row : 0) * a.wb),
+                      (uint32_t)__builtin_amdgcn_readfirstlane(have * a.wb));
+  }
+  // the four 16-byte pieces of a row are kept in an order that spreads the
+  // rows that a fragment read meets over the banks
+  const uint32_t wvo = (uint32_t)(lane >> 2) * (uint32_t)a.wb + (uint32_t)(((lane & 3) ^ ((lane >> 4) & 3)) * 16);
+  auto load_w = [&](int slot, int kb, bool there) __attribute__((always_inline)) {
+    // bytes past the rows inside the matrix read zero, those past a row's end
+    // (the next row's) meet x = 0
+    const uint32_t off = there ? wvo + (uint32_t)kb * 64u : kOobOffset;
+    load_lds_x4<0>(rw[0], ring + slot * 2048, off, 0);
+    load_lds_x4<1>(rw[1], ring + slot * 2048, off, 0);
+  };
+
+  // x: lane l brings eight k of token l / 16 of each group of four
+  const char *xrow[XW];
+#pragma unroll
+  for (int i = 0; i < XW; ++i) {
+    const int m = m0 + 4 * (wn * XW + i) + (lane >> 4);
+    xrow[i] = reinterpret_cast<const char *>(a.x + (int64_t)(m < a.M ? m : a.M - 1) * a.K);
+  }
+  const int blocks = (a.K + 127) / 128;
+  // (K is at least eight: the row's last eight values are loaded where fewer
+  // are left, and put in place when they are stored)
+  auto load_x = [&](u32x4 (&to)[XW], int kb) __attribute__((always_inline)) {
+    const int k = kb * 128 + 8 * (lane & 15);
+    const uint32_t at = (uint32_t)(k < a.K - 8 ? k : a.K - 8) * 2u;
+#pragma unroll
+    for (int i = 0; i < XW; ++i) to[i] = load_at<u32x4_any>(xrow[i], at);
+  };
+  auto store_x = [&](char *to, u32x4 (&from)[XW], int kb) __attribute__((always_inline)) {
+    if (kb * 128 + 128 > a.K) {
+      const int k = kb * 128 + 8 * (lane & 15);
+#pragma unroll
+      for (int i = 0; i < XW; ++i) from[i] = drop_values(from[i], k > a.K - 8 ? k - (a.K - 8) : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < XW; ++i) {
+      const int row = 4 * (wn * XW + i) + (lane >> 4);
+      *reinterpret_cast<u32x4 *>(to + row * 256 + (((lane & 15) ^ (row & 15)) * 16)) = weight_order(from[i]);
+    }
+  };
+
+  f32x4 tot[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int b = 0; b < NT; ++b) tot[m][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const uint32_t wread = c * 64 + q * 4;
+  const int xr = XI < 4 ? c & (4 * XI - 1) : c;
+  const uint32_t *myscales = scales + (wn * 32 + c) * a.sp;
+
+  auto compute = [&](const char *slot, const char *xs_, int kb, int g0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int g = 0; g < SG; ++g) {
+      const int gi = (int)((uint64_t)(uint32_t)(kb * 4 + GS * g) * a.per32 >> 40) - g0;
+      f32x4 acc[MT][NT], xs[MT];
+      typename F::Zero z[NT];
+      float sc[NT];
+#pragma unroll
+      for (int b = 0; b < NT; ++b) {
+        const uint32_t v = myscales[b * 16 * a.sp + gi];
+        sc[b] = widen<T>((uint16_t)(v >> 16));
+        z[b].set(v);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        xs[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int b = 0; b < NT; ++b) acc[m][b] = xs[m];
+      }
+#pragma unroll
+      for (int s = g * GS; s < (g + 1) * GS; ++s) {
+        u32x4 xf[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          xf[m] = *reinterpret_cast<const u32x4 *>(xs_ + (16 * m + xr) * 256 + (((4 * s + q) ^ xr) * 16));
+          // the weights carry 16 + zero too much: the sum of x takes it out again
+          if constexpr (!F::kExactZero) xs[m] = F::mma(xf[m], F::ones(), xs[m]);
+        }
+#pragma unroll
+        for (int b = 0; b < NT; ++b) {
+          const uint32_t v = *reinterpret_cast<const uint32_t *>(slot + b * 1024 + wread + ((s ^ (c >> 2)) * 16));
+          const u32x4 f = F::weights(v, z[b]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[m][b] = F::mma(xf[m], f, acc[m][b]);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float v = acc[m][b][r];
+            if constexpr (!F::kExactZero) v -= z[b].off * xs[m][r];
+            tot[m][b][r] += sc[b] * v;
+          }
+    }
+  };
+
+  for (int c0 = 0; c0 < blocks; c0 += CB) {
+    const int nb = blocks - c0 < CB ? blocks - c0 : CB;
+    // Workgroups start at different blocks: rows are often a multiple of the
+    // memory channels' interleave apart, and all would meet on the same few.
+    const int turn = (int)((blockIdx.x * 0x9E3779B1u >> 12) % (unsigned)nb);
+    const int mine = wk < nb ? (nb - wk + KW - 1) / KW : 0;
+    const int rounds = NW == 1 ? mine : (nb + KW - 1) / KW;
+    auto block = [&](int i) {
+      const int p = wk + (i < mine ? i : mine - 1) * KW + turn;
+      return c0 + (p < nb ? p : p - nb);
+    };
+    // Loads are issued for every i, those past the last block with no bytes
+    // (weights) or once more (x): the counts that the waits below rely on.
+    u32x4 xreg[D - 1][XW];
+    if (mine > 0) {
+#pragma unroll
+      for (int i = 0; i < D - 1; ++i) {
+        load_x(xreg[i], block(i));
+        compiler_fence();
+        load_w(i, block(i), i < mine);
+        compiler_fence();
+      }
+    }
+    {
+      const int g0 = (int)((uint64_t)(uint32_t)(c0 * 4) * a.per32 >> 40);
+      const int ng = (int)((uint64_t)(uint32_t)((c0 + nb) * 4 - 1) * a.per32 >> 40) - g0 + 1;
+      const uint32_t by = 0xFFFFFFFFu / (uint32_t)ng + 1u;  // 0 for one group
+      const uint8_t *zp = a.zero ? a.zero : reinterpret_cast<const uint8_t *>(a.scale);
+      const int total = G::ROWS * ng;
+      auto stage = [&](auto at_once) __attribute__((always_inline)) {
+        constexpr int U = decltype(at_once)::value;
+        for (int base = tid; base < total; base += U * G::THREADS) {
+          uint32_t sv[U], zv[U];
+          int to[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int idx = base + u * G::THREADS;
+            const int r = ng == 1 ? idx : (int)__umulhi((uint32_t)idx, by);
+            const int g = idx - r * ng;
+            int have;
+            const int64_t row = block_row(r / 32, r / 16 % 2, &have) + (r & 15);
+            // a row or group past the end: its products are zeros or not stored
+            const bool in = idx < total && (r & 15) < have && g0 + g < a.groups;
+            const int64_t at = in ? row * a.groups + g0 + g : 0;
+            sv[u] = a.scale[at];
+            zv[u] = zp[at];
+            to[u] = idx >= total ? -1 : in ? r * a.sp + g : r * a.sp + g + (1 << 30);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (to[u] >= 0)
+              scales[to[u] & ~(1 << 30)] = F::pack(to[u] >> 30 ? 0 : (uint16_t)sv[u], a.zero ? zv[u] : 8u);
+        }
+      };
+      // several loads at once: one after the other would each wait for memory
+      if (total <= G::THREADS)
+        stage(std::integral_constant<int, 1>{});
+      else
+        stage(std::integral_constant<int, 2048 / G::THREADS>{});
+      lds_barrier();
+      auto round = [&](int i, u32x4(&x)[XW]) __attribute__((always_inline)) {
+        char *xs = xbuf + (NW == 1 ? 0 : (i & 1)) * (XI * 1024);
+        if (mine > 0) {
+          store_x(xs, x, block(i));
+          load_x(x, block(i + D - 1));
+          wait_lgkmcnt0();  // the slot's last reads are over
+          compiler_fence();
+          load_w((i + D - 1) % D, block(i + D - 1), i + D - 1 < mine);
+          wait_vmcnt<(D - 1) * (XW + 2)>();
+          compiler_fence();
+        }
+        if (NW > 1) lds_barrier();
+        if (NW == 1 || i < mine) compute(ring + (i % D) * 2048, xs, block(i), g0);
+      };
+      int i = 0;
+      if constexpr (D == 2) {
+        for (; i < rounds; ++i) round(i, xreg[0]);
+      } else {
+        for (; i + 1 < rounds; i += 2) {
+          round(i, xreg[0]);
+          round(i + 1, xreg[D - 2]);
+        }
+        if (i < rounds) round(i, xreg[0]);
+      }
+    }
+    wait_vmcnt<0>();
+    __syncthreads();  // the ring, the tokens and the scales are free
+  }
+
+  float *sums = reinterpret_cast<float *>(smem) + wn * (MT * NT * 4 * 64);
+  constexpr int PART = NW * MT * NT * 4 * 64;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int b = 0; b < NT; ++b)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sums[wk * PART + ((m * NT + b) * 4 + r) * 64 + lane] = tot[m][b][r];
+  __syncthreads();
+  join_and_store<T, GATED, MT, NT>(sums, KW, PART, wk, KW, lane, a.act, a.out, a.M, a.N, m0,
+                                   n0 + wn * (GATED ? 16 : 32));
+}
+
+// Rows shorter than eight values: one output a thread.
+template <typename T, bool GATED>
+__global__ void __launch_bounds__(256) q4_short_kernel(Q4Args a) {
+  const int64_t total = (int64_t)a.M * a.N;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / a.N, n = i % a.N;
+    auto dot = [&](int64_t row) {  // one group
+      float sum = 0.0f;
+      const float z = a.zero ? (float)a.zero[row] : 8.0f;
+      for (int k = 0; k < a.K; ++k) {
+        const float w = (float)(a.q[row * a.wb + k / 2] >> (4 * (k & 1)) & 15) - z;
+        sum += widen<T>(a.x[m * a.K + k]) * w;
+      }
+      return a.K > 0 ? sum * widen<T>(a.scale[row]) : 0.0f;
+    };
+    const float v = GATED ? activate(a.act, dot(n)) * dot(n + a.N) : dot(n);
+    a.out[i] = __builtin_bit_cast(uint16_t, (T)v);
+  }
+}
+
+}  // namespace pgemm

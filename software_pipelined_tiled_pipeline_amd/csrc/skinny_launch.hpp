@@ -7,11 +7,11 @@
 namespace pgemm {
 namespace launch_detail {
 
-template <typename T, bool W4, bool GATED, int MT, int NT, int GS, int WAVES>
+template <typename T, bool GATED, int MT, int NT, int WAVES>
 pgemm_status launch_skinny_one(const SkinnyArgs &a, hipStream_t stream, int dev) {
   static std::atomic<uint64_t> lds_set{0};
   constexpr int LDS = WAVES * MT * NT * 4 * 64 * 4;
-  auto kern = skinny_kernel<T, W4, GATED, MT, NT, GS, WAVES>;
+  auto kern = skinny_kernel<T, GATED, MT, NT, WAVES>;
   if (LDS > 65536) {
     pgemm_status st = allow_lds(kern, LDS, dev, lds_set);
     if (st != PGEMM_OK) return st;
@@ -22,12 +22,21 @@ pgemm_status launch_skinny_one(const SkinnyArgs &a, hipStream_t stream, int dev)
   return launched();
 }
 
+// Waves along K: so many that all workgroups together give each CU about
+// sixteen.
+template <typename T, bool GATED, int MT>
+pgemm_status launch_skinny_waves(const SkinnyArgs &a, hipStream_t stream, int dev) {
+  const int64_t groups = per(a.N, GATED ? 16 : 32) * per(a.M, 16 * MT);
+  if (groups <= 512) return launch_skinny_one<T, GATED, MT, 2, 8>(a, stream, dev);
+  return launch_skinny_one<T, GATED, MT, 2, 4>(a, stream, dev);
+}
+
 // Token blocks of 16 a workgroup takes: as many as there are, up to four.
-template <typename T, bool W4, bool GATED, int GS>
+template <typename T, bool GATED>
 pgemm_status launch_skinny(const SkinnyArgs &a, hipStream_t stream, int dev) {
-  if (a.M <= 16) return launch_skinny_one<T, W4, GATED, 1, 2, GS, 8>(a, stream, dev);
-  if (a.M <= 32) return launch_skinny_one<T, W4, GATED, 2, 2, GS, 8>(a, stream, dev);
-  return launch_skinny_one<T, W4, GATED, 4, 2, GS, 8>(a, stream, dev);
+  if (a.M <= 16) return launch_skinny_waves<T, GATED, 1>(a, stream, dev);
+  if (a.M <= 32) return launch_skinny_waves<T, GATED, 2>(a, stream, dev);
+  return launch_skinny_waves<T, GATED, 4>(a, stream, dev);
 }
 
 }  // namespace launch_detail

@@ -2,13 +2,14 @@
 
 The functions are reached through :mod:`pgemm`, next to the products:
 ``pgemm_{f16,bf16}_gated`` and ``_gated_bwd``, ``_xent`` and ``_xent_bwd``,
-``_q4`` and ``_q4_gated``.  Tensors live on the current GPU; what a call needs
-as workspace is a torch tensor on the call's stream, registered there and kept
-for later calls.  All arithmetic runs in the library's kernels.
+``_q4`` and ``_q4_gated``.  Tensors live on the current GPU; every function also
+takes a ``stream`` to run on.  What a call needs as workspace is a torch tensor
+on the call's stream, registered there and kept for later calls.  All arithmetic runs in the library's kernels.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 
 ACTS = {"silu": 0, "gelu": 1}
 FUSED_OPS = {"gated": 0, "gated_save": 1, "gated_bwd": 2, "xent": 3, "xent_bwd": 4}
@@ -35,6 +36,7 @@ def declare(L) -> None:
     L.pgemm_fused_workspace.restype = I
 
 
+@functools.lru_cache(maxsize=1024)
 def workspace_bytes(op: str, M: int, N: int, K: int) -> int:
     """Bytes of workspace of a call: (M, N, K) is (M, F, D) or (M, V, D)."""
     from . import pgemm
@@ -43,28 +45,49 @@ def workspace_bytes(op: str, M: int, N: int, K: int) -> int:
     return n.value
 
 
-def _here():
+def _refuse(name, t, dtype, shape, dev):
+    """Says what is wrong with one operand; a size of None in `shape` takes any size."""
     import torch
     if not torch.cuda.is_available():
         raise ValueError("pgemm needs a GPU")
-    return torch.device("cuda", torch.cuda.current_device())
-
-
-def _tensor(name, t, dtype, shape, here):
-    """Checks one operand; a size of None in `shape` takes any size."""
+    here = torch.device("cuda", torch.cuda.current_device() if dev is None else dev)
     if t.dtype != dtype or not t.is_cuda or t.device != here:
         raise ValueError(f"{name} must be a {dtype} tensor on the current device {here}, not {t.dtype} on {t.device}")
     if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
         want = "[" + ", ".join("any" if w is None else str(w) for w in shape) + "]"
         raise ValueError(f"{name} must have shape {want}, not {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _out(name, t, dtype, shape, here):
+def _first(name, t, dtype):
+    """Checks a call's first matrix; (rows, columns, current device)."""
     import torch
-    return torch.empty(shape, dtype=dtype, device=here) if t is None else _tensor(name, t, dtype, shape, here)
+    if not t.is_cuda or t.dim() != 2:
+        _refuse(name, t, dtype, (None, None), None)
+    dev = torch.cuda.current_device()
+    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, dtype, (None, None), dev)
+    rows, cols = t.shape
+    return rows, cols, dev
+
+
+def _want(name, t, dtype, shape, dev):
+    if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _refuse(name, t, dtype, shape, dev)
+
+
+def _rows(name, t, dtype, cols, dev):
+    """Checks a matrix of any number of rows; that number."""
+    if t.dim() != 2 or t.shape[1] != cols or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, dtype, (None, cols), dev)
+    return t.shape[0]
+
+
+def _out(name, t, dtype, shape, dev, like):
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    _want(name, t, dtype, shape, dev)
+    return t
 
 
 def _act(act):
@@ -77,13 +100,47 @@ def _ptr(t):
     return None if t is None else (t.data_ptr() or None)
 
 
-def _run(name, op, sizes, args, stream):
+_entries = {}  # library functions by name
+
+
+def _run(name, dev, args, need=0):
+    """Calls the library on the current stream, with a workspace of `need` bytes."""
+    import torch
     from . import pgemm
-    if op is not None:
-        need = workspace_bytes(op, *sizes)
-        if need:
-            pgemm.ensure_workspace(need, stream)
-    pgemm._check(getattr(pgemm.lib(), name)(*args, pgemm._stream(stream)), name)
+    f = _entries.get(name)
+    if f is None:
+        f = _entries[name] = getattr(pgemm.lib(), name)
+    handle = torch._C._cuda_getCurrentRawStream(dev)
+    if need:
+        if torch.cuda.is_current_stream_capturing():
+            # A graph replays with this buffer for as long as it lives, so it is
+            # the graph's own, from its memory pool, and not the stream's, which
+            # a later call may replace.
+            own = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
+            pgemm._register(handle, own)
+            try:
+                pgemm._check(f(*args, handle), name)
+            finally:
+                pgemm._register(handle, pgemm._workspaces.get((dev, handle)))
+            return
+        ws = pgemm._workspaces.get((dev, handle))
+        if ws is None or ws.numel() < need:
+            pgemm.ensure_workspace(need)
+    status = f(*args, handle)
+    if status != 0:
+        pgemm._check(status, name)
+
+
+def _on_stream(fn):
+    """`fn` with an argument `stream`: its outputs and kernels then belong to that stream instead of the current one."""
+    @functools.wraps(fn)
+    def run(*args, stream=None, **more):
+        if stream is None:
+            return fn(*args, **more)
+        import torch
+        with torch.cuda.stream(stream):
+            return fn(*args, **more)
+    return run
 
 
 def _saved_shape(M, F):
@@ -91,140 +148,134 @@ def _saved_shape(M, F):
 
 
 def _make(fmt, dtype_name):
-    def dtype():
-        import torch
-        return getattr(torch, dtype_name)
+    def name(op):
+        return f"pgemm_{fmt}_{op}"
 
-    def block(x, w, here):
-        _tensor("x", x, dtype(), (None, None), here)
-        M, D = x.shape
-        _tensor("w", w, dtype(), (None, D), here)
-        if w.shape[0] % 2:
+    GATED, GATED_BWD, XENT, XENT_BWD, Q4, Q4_GATED = map(
+        name, ("gated", "gated_bwd", "xent", "xent_bwd", "q4", "q4_gated"))
+
+    def block(x, w, dtype):
+        M, D, dev = _first("x", x, dtype)
+        rows = _rows("w", w, dtype, D, dev)
+        if rows % 2:
             raise ValueError("w must have 2 F rows, the gate rows and then the up rows")
-        return M, w.shape[0] // 2, D
+        return M, rows // 2, D, dev
 
-    def gated(x, w, act="silu", out=None, save=False, stream=None):
+    def gated(x, w, act="silu", out=None, save=False):
         import torch
-        here = _here()
-        M, F, D = block(x, w, here)
+        dtype = getattr(torch, dtype_name)
+        M, F, D, dev = block(x, w, dtype)
         code = _act(act)
-        h = _out("out", out, dtype(), (M, F), here)
-        saved = torch.empty(_saved_shape(M, F), dtype=torch.float32, device=here) if save else None
-        _run(f"pgemm_{fmt}_gated", "gated_save" if save else "gated", (M, F, D),
-             (_ptr(x), _ptr(w), _ptr(h), _ptr(saved), M, F, D, code), stream)
+        h = _out("out", out, dtype, (M, F), dev, x)
+        saved = x.new_empty(_saved_shape(M, F), dtype=torch.float32) if save else None
+        _run(GATED, dev, (_ptr(x), _ptr(w), _ptr(h), _ptr(saved), M, F, D, code),
+             workspace_bytes("gated_save" if save else "gated", M, F, D))
         return (h, saved) if save else h
 
     gated.__doc__ = (f"{dtype_name} h[M,F] = act(x Wg^T) * (x Wu^T) for x [M,D] and w [2F,D], the gate rows and then the up "
-                     f"rows (library call pgemm_{fmt}_gated); act is 'silu' or 'gelu' (tanh form).  With save=True also "
+                     f"rows (library call {GATED}); act is 'silu' or 'gelu' (tanh form).  With save=True also "
                      "returns the fp32 projections for the backward call, 8 bytes per value of h.")
 
-    def gated_bwd(dh, x, w, saved=None, act="silu", dx=None, dw=None, stream=None):
+    def gated_bwd(dh, x, w, saved=None, act="silu", dx=None, dw=None):
         import torch
-        here = _here()
-        M, F, D = block(x, w, here)
+        dtype = getattr(torch, dtype_name)
+        M, F, D, dev = block(x, w, dtype)
         code = _act(act)
-        _tensor("dh", dh, dtype(), (M, F), here)
+        _want("dh", dh, dtype, (M, F), dev)
         if saved is not None:
-            _tensor("saved", saved, torch.float32, _saved_shape(M, F), here)
-        dx = _out("dx", dx, dtype(), (M, D), here)
-        dw = _out("dw", dw, dtype(), (2 * F, D), here)
-        _run(f"pgemm_{fmt}_gated_bwd", "gated_bwd", (M, F, D),
-             (_ptr(dh), _ptr(x), _ptr(w), _ptr(saved), _ptr(dx), _ptr(dw), M, F, D, code), stream)
+            _want("saved", saved, torch.float32, _saved_shape(M, F), dev)
+        dx = _out("dx", dx, dtype, (M, D), dev, x)
+        dw = _out("dw", dw, dtype, (2 * F, D), dev, x)
+        _run(GATED_BWD, dev, (_ptr(dh), _ptr(x), _ptr(w), _ptr(saved), _ptr(dx), _ptr(dw), M, F, D, code),
+             workspace_bytes("gated_bwd", M, F, D))
         return dx, dw
 
-    gated_bwd.__doc__ = (f"(dx[M,D], dw[2F,D]) of pgemm_{fmt}_gated for dh [M,F].  saved: what the forward call kept "
+    gated_bwd.__doc__ = (f"(dx[M,D], dw[2F,D]) of {GATED} for dh [M,F].  saved: what the forward call kept "
                          "(faster: two products fewer); None computes the projections again.")
 
-    def xent(x, w, target, ignore_index=-100, loss=None, lse=None, stream=None):
+    def head(x, w, target, dtype, i64):
+        M, D, dev = _first("x", x, dtype)
+        V = _rows("w", w, dtype, D, dev)
+        _want("target", target, i64, (M,), dev)
+        return M, V, D, dev
+
+    def xent(x, w, target, ignore_index=-100, loss=None, lse=None):
         import torch
-        here = _here()
-        _tensor("x", x, dtype(), (None, None), here)
-        M, D = x.shape
-        _tensor("w", w, dtype(), (None, D), here)
-        V = w.shape[0]
-        _tensor("target", target, torch.int64, (M,), here)
-        loss = _out("loss", loss, torch.float32, (M,), here)
-        lse = _out("lse", lse, torch.float32, (M,), here)
-        _run(f"pgemm_{fmt}_xent", "xent", (M, V, D),
-             (_ptr(x), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse), M, V, D, int(ignore_index)), stream)
+        M, V, D, dev = head(x, w, target, getattr(torch, dtype_name), torch.int64)
+        loss = _out("loss", loss, torch.float32, (M,), dev, x)
+        lse = _out("lse", lse, torch.float32, (M,), dev, x)
+        _run(XENT, dev, (_ptr(x), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse), M, V, D, int(ignore_index)),
+             workspace_bytes("xent", M, V, D))
         return loss, lse
 
     xent.__doc__ = (f"(loss[M], lse[M]) in fp32: softmax cross entropy of the logits x w^T for {dtype_name} x [M,D] and w "
-                    f"[V,D], without storing them (library call pgemm_{fmt}_xent).  Rows whose target is ignore_index have "
+                    f"[V,D], without storing them (library call {XENT}).  Rows whose target is ignore_index have "
                     "loss 0; any other target outside the vocabulary makes its loss NaN.")
 
-    def xent_bwd(dloss, x, w, target, lse, ignore_index=-100, dx=None, dw=None, stream=None):
+    def xent_bwd(dloss, x, w, target, lse, ignore_index=-100, dx=None, dw=None):
         import torch
-        here = _here()
-        _tensor("x", x, dtype(), (None, None), here)
-        M, D = x.shape
-        _tensor("w", w, dtype(), (None, D), here)
-        V = w.shape[0]
-        _tensor("target", target, torch.int64, (M,), here)
-        _tensor("lse", lse, torch.float32, (M,), here)
-        if dloss.dtype != torch.float32 or not dloss.is_cuda or dloss.device != here:
-            raise ValueError(f"dloss must be a torch.float32 tensor on the current device {here}")
+        dtype = getattr(torch, dtype_name)
+        M, V, D, dev = head(x, w, target, dtype, torch.int64)
+        _want("lse", lse, torch.float32, (M,), dev)
+        if dloss.dtype != torch.float32 or dloss.get_device() != dev:
+            raise ValueError(f"dloss must be a torch.float32 tensor on the current device cuda:{dev}")
         if dloss.dim() == 0:
             step = 0
-        elif tuple(dloss.shape) == (M,) and (M <= 1 or dloss.stride(0) in (0, 1)):
+        elif dloss.shape == (M,) and (M <= 1 or dloss.stride(0) in (0, 1)):
             step = 0 if M > 1 and dloss.stride(0) == 0 else 1
         else:
             raise ValueError("dloss must be a scalar, or have shape [M] and be contiguous or expanded from a scalar")
-        dx = _out("dx", dx, dtype(), (M, D), here)
-        dw = _out("dw", dw, dtype(), (V, D), here)
-        _run(f"pgemm_{fmt}_xent_bwd", "xent_bwd", (M, V, D),
-             (_ptr(dloss), step, _ptr(x), _ptr(w), _ptr(target), _ptr(lse), _ptr(dx), _ptr(dw), M, V, D,
-              int(ignore_index)), stream)
+        dx = _out("dx", dx, dtype, (M, D), dev, x)
+        dw = _out("dw", dw, dtype, (V, D), dev, x)
+        _run(XENT_BWD, dev, (_ptr(dloss), step, _ptr(x), _ptr(w), _ptr(target), _ptr(lse), _ptr(dx), _ptr(dw), M, V, D,
+                             int(ignore_index)), workspace_bytes("xent_bwd", M, V, D))
         return dx, dw
 
-    xent_bwd.__doc__ = (f"(dx[M,D], dw[V,D]) of pgemm_{fmt}_xent for dloss, fp32 [M] or a scalar that all rows share, and "
+    xent_bwd.__doc__ = (f"(dx[M,D], dw[V,D]) of {XENT} for dloss, fp32 [M] or a scalar that all rows share, and "
                         "the forward call's lse.")
 
-    def q4_operands(x, q, scale, zero, group, here):
-        import torch
-        _tensor("x", x, dtype(), (None, None), here)
-        M, K = x.shape
+    def q4_operands(x, q, scale, zero, group, dtype, u8):
+        M, K, dev = _first("x", x, dtype)
         if group <= 0 or group % 32:
             raise ValueError("group must be a positive multiple of 32")
-        _tensor("q", q, torch.uint8, (None, -(-K // 32) * 16), here)
-        rows, groups = q.shape[0], -(-K // group)
-        _tensor("scale", scale, dtype(), (rows, groups), here)
+        rows, groups = _rows("q", q, u8, -(-K // 32) * 16, dev), -(-K // group)
+        _want("scale", scale, dtype, (rows, groups), dev)
         if zero is not None:
-            _tensor("zero", zero, torch.uint8, (rows, groups), here)
-        return M, rows, K
+            _want("zero", zero, u8, (rows, groups), dev)
+        return M, rows, K, dev
 
-    def q4(x, q, scale, zero=None, group=128, out=None, stream=None):
-        here = _here()
-        M, N, K = q4_operands(x, q, scale, zero, group, here)
-        out = _out("out", out, dtype(), (M, N), here)
-        _run(f"pgemm_{fmt}_q4", None, None,
-             (_ptr(x), _ptr(q), _ptr(scale), _ptr(zero), _ptr(out), M, N, K, int(group)), stream)
+    def q4(x, q, scale, zero=None, group=128, out=None):
+        import torch
+        dtype = getattr(torch, dtype_name)
+        M, N, K, dev = q4_operands(x, q, scale, zero, group, dtype, torch.uint8)
+        out = _out("out", out, dtype, (M, N), dev, x)
+        _run(Q4, dev, (_ptr(x), _ptr(q), _ptr(scale), _ptr(zero), _ptr(out), M, N, K, int(group)))
         return out
 
     q4.__doc__ = (f"{dtype_name} out[M,N] = x[M,K] w^T for few rows and 4-bit weights w[n,k] = scale[n,k/group] (q[n,k] - "
                   "zero[n,k/group]); q as pack_q4 gives it, zero None means 8 "
-                  f"(library call pgemm_{fmt}_q4).")
+                  f"(library call {Q4}).")
 
-    def q4_gated(x, q, scale, zero=None, group=128, act="silu", out=None, stream=None):
-        here = _here()
-        M, rows, K = q4_operands(x, q, scale, zero, group, here)
+    def q4_gated(x, q, scale, zero=None, group=128, act="silu", out=None):
+        import torch
+        dtype = getattr(torch, dtype_name)
+        M, rows, K, dev = q4_operands(x, q, scale, zero, group, dtype, torch.uint8)
         code = _act(act)
         if rows % 2:
             raise ValueError("q must have 2 F rows, the gate rows and then the up rows")
         F = rows // 2
-        out = _out("out", out, dtype(), (M, F), here)
-        _run(f"pgemm_{fmt}_q4_gated", None, None,
-             (_ptr(x), _ptr(q), _ptr(scale), _ptr(zero), _ptr(out), M, F, K, int(group), code), stream)
+        out = _out("out", out, dtype, (M, F), dev, x)
+        _run(Q4_GATED, dev, (_ptr(x), _ptr(q), _ptr(scale), _ptr(zero), _ptr(out), M, F, K, int(group), code))
         return out
 
     q4_gated.__doc__ = (f"{dtype_name} h[M,F] = act(x Wg^T) * (x Wu^T) for few rows and 4-bit weights of 2F rows, the gate rows "
-                        f"and then the up rows (library call pgemm_{fmt}_q4_gated).")
+                        f"and then the up rows (library call {Q4_GATED}).")
 
     made = {}
     for fn in (gated, gated_bwd, xent, xent_bwd, q4, q4_gated):
-        name = f"pgemm_{fmt}_{fn.__name__}"
-        fn.__name__ = fn.__qualname__ = name
-        made[name] = fn
+        full = name(fn.__name__)
+        fn.__name__ = fn.__qualname__ = full
+        made[full] = _on_stream(fn)
     return made
 
 

@@ -140,6 +140,12 @@ def _operands(lhs, rhs, out, dtype, nn: bool):
 _workspaces = {}
 
 
+def _register(handle: int, ws) -> None:
+    """Makes a tensor (None: nothing) the workspace of a stream on the current device."""
+    ptr, n = (None, 0) if ws is None else (ctypes.c_void_p(ws.data_ptr()), ws.numel())
+    _check(lib().pgemm_set_workspace(ctypes.c_void_p(handle), ptr, n), "pgemm_set_workspace")
+
+
 def ensure_workspace(nbytes: int, stream=None):
     """Registers a workspace of at least `nbytes` for `stream` (default: the
     current stream) on the current device, growing the registered one if it
@@ -152,8 +158,7 @@ def ensure_workspace(nbytes: int, stream=None):
     if ws is None or ws.numel() < nbytes:
         with torch.cuda.stream(s):
             ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device="cuda")
-        _check(lib().pgemm_set_workspace(ctypes.c_void_p(s.cuda_stream), ctypes.c_void_p(ws.data_ptr()),
-                                         ws.numel()), "pgemm_set_workspace")
+        _register(s.cuda_stream, ws)
         _workspaces[key] = ws
     return ws
 
@@ -163,7 +168,7 @@ def release_workspace(stream=None) -> None:
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
     key = (torch.cuda.current_device(), s.cuda_stream)
-    _check(lib().pgemm_set_workspace(ctypes.c_void_p(s.cuda_stream), None, 0), "pgemm_set_workspace")
+    _register(s.cuda_stream, None)
     _workspaces.pop(key, None)
 
 
