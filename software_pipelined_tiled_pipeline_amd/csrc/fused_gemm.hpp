@@ -62,6 +62,46 @@ struct KRows {
   __device__ __forceinline__ static int f(int k) { return (k & 3) | (((k >> 3) & FMASK) << 2); }
 };
 
+// Direct-to-LDS loads that the compiler does not see as such.
+//
+// It takes every LDS read that follows a direct-to-LDS load for a possible
+// reader of what that load brings.  Plain reads it can tell apart by their
+// type; the transposing reads have none, and each would wait for all loads in
+// flight (s_waitcnt vmcnt(0)), those of the next but one K tile included: that
+// took 2.0 us a K tile of 256 x 256 x 64 instead of 1.6.  So the loads of
+// kernels with transposing reads are inline assembly, which returns nothing in
+// registers, and their waits are explicit: UntrackedWait counts them.  M0, the
+// LDS address, is set by the first of four and read by the other three;
+// nothing between them writes it (tests/test_fused_asm.py).
+typedef int rsrc_words __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ rsrc_words make_rsrc_words(const char *base, uint32_t bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(base);
+  return rsrc_words{(int)(uint32_t)v, (int)(uint32_t)(v >> 32) & 0xffff, (int)bytes, kRsrcWord3};
+}
+
+template <int G>
+__device__ __forceinline__ void load_lds_x4_untracked(rsrc_words rsrc, const char *lds_base, uint32_t voffset) {
+  if constexpr (G == 0) {
+    const uint32_t lds = (uint32_t)(uintptr_t)(lds_void *)lds_base;
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :
+                 : "v"(voffset), "s"(rsrc), "s"(lds)
+                 : "memory");
+  } else {
+    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen offset:%c2 lds"
+                 :
+                 : "v"(voffset - 1024u * G), "s"(rsrc), "n"(1024 * G)
+                 : "memory");
+  }
+}
+
+// s_waitcnt vmcnt(N) that the compiler keeps though it knows of no load.
+template <int N>
+__device__ __forceinline__ void wait_vmcnt_untracked() {
+  asm volatile("s_waitcnt vmcnt(%c0)" : : "n"(N) : "memory");
+}
+
 __device__ __forceinline__ const char *wave_uniform(const char *p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
   const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
@@ -94,10 +134,34 @@ struct FusedLoader {
   int K;
   bool kc;
 
+  static constexpr bool UNTRACKED = LA == Lay::KR || LB == Lay::KR;
+  static_assert(!(UNTRACKED && DUAL), "two matrices have K contiguous");
+  using Rsrc = std::conditional_t<UNTRACKED, rsrc_words, __amdgpu_buffer_rsrc_t>;
   struct Tile {
-    __amdgpu_buffer_rsrc_t r, r2;
+    Rsrc r, r2;
     int rem;  // K left from the tile's first k
   };
+
+  __device__ __forceinline__ static Rsrc resource(const char *p, uint32_t bytes) {
+    if constexpr (UNTRACKED)
+      return make_rsrc_words(p, bytes);
+    else
+      return make_rsrc(p, bytes);
+  }
+  template <int N>
+  __device__ __forceinline__ static void wait() {
+    if constexpr (UNTRACKED)
+      wait_vmcnt_untracked<N>();
+    else
+      wait_vmcnt<N>();
+  }
+  template <int I>
+  __device__ __forceinline__ static void load(const Rsrc &r, char *dst, uint32_t v) {
+    if constexpr (UNTRACKED)
+      load_lds_x4_untracked<I>(r, dst, v);
+    else
+      load_lds_x4<I>(r, dst, v, 0);
+  }
 
   template <Lay L, int R, bool TWO>
   __device__ __forceinline__ void lay_out(const FusedOperand &o, int r0, int first) {
@@ -152,6 +216,9 @@ struct FusedLoader {
     span = (uint32_t)__builtin_amdgcn_readfirstlane((int)span);
     cut = (uint32_t)__builtin_amdgcn_readfirstlane((int)cut);
     kc = __builtin_amdgcn_readfirstlane((int)kc) != 0;
+    // five wait states between these and a load that reads them: the compiler
+    // does not look into the untracked ones
+    if constexpr (UNTRACKED) asm volatile("s_nop 4");
   }
 
   // The resource of K tile t (past the end: of no bytes, every lane reads zero).
@@ -167,8 +234,8 @@ struct FusedLoader {
     else
       bytes = (uint32_t)(s.rem < BK ? s.rem : BK) * span - cut;
     if (s.rem == 0) bytes = 0;
-    s.r = make_rsrc(base + off, bytes);
-    s.r2 = DUAL ? make_rsrc(base2 + off, bytes) : s.r;
+    s.r = resource(base + off, bytes);
+    s.r2 = DUAL ? resource(base2 + off, bytes) : s.r;
     return s;
   }
 
@@ -177,12 +244,12 @@ struct FusedLoader {
     uint32_t v = vo[i];
     if (lk[i & 1] >= s.rem) v = kOobOffset;
     char *dst = slot + (wave * PER + (i & ~3)) * (kWave * 16);
-    const __amdgpu_buffer_rsrc_t r = DUAL && ((i >> 1) & 1) ? s.r2 : s.r;
+    const Rsrc r = DUAL && ((i >> 1) & 1) ? s.r2 : s.r;
     switch (i & 3) {
-      case 0: load_lds_x4<0>(r, dst, v, 0); break;
-      case 1: load_lds_x4<1>(r, dst, v, 0); break;
-      case 2: load_lds_x4<2>(r, dst, v, 0); break;
-      default: load_lds_x4<3>(r, dst, v, 0); break;
+      case 0: load<0>(r, dst, v); break;
+      case 1: load<1>(r, dst, v); break;
+      case 2: load<2>(r, dst, v); break;
+      default: load<3>(r, dst, v); break;
     }
   }
 };
@@ -279,7 +346,7 @@ __global__ void __launch_bounds__(G::THREADS, G::OCC) fused_kernel(FusedProduct 
 #pragma unroll
     for (int i = 0; i < PER; ++i) ld.load_one(slot_ptr(j), wave, s, i);
   }
-  wait_vmcnt<PER>();
+  Loader::template wait<PER>();
   lds_barrier();
   if (n_k > 0) {
 #pragma unroll
@@ -295,7 +362,7 @@ __global__ void __launch_bounds__(G::THREADS, G::OCC) fused_kernel(FusedProduct 
       static_assert(PER == Pl::NLA + Pl::NLB, "every load of the wave's share is placed");
       auto war = []() __attribute__((always_inline)) { lds_barrier(); };
       auto raw = []() __attribute__((always_inline)) {
-        wait_vmcnt<PER>();
+        Loader::template wait<PER>();
         __builtin_amdgcn_s_barrier();
       };
       w.template sched_step<Pl::RA0, Pl::REA, NR, Pl::LA0, Pl::LEA, Pl::NLA, Pl::WAR>(
@@ -308,13 +375,13 @@ __global__ void __launch_bounds__(G::THREADS, G::OCC) fused_kernel(FusedProduct 
       NoLoads none;
       auto no_sync = []() __attribute__((always_inline)) {};
       w.template sched_step<0, 1, NR, 0, 1, 0, -1>(f[0], rd1, none, no_sync);
-      wait_vmcnt<0>();  // tile t + 1 landed
+      Loader::template wait<0>();  // tile t + 1 landed
       lds_barrier();    // and slot s is free
       w.template sched_step<0, 1, NR, NM / PER - 1, NM / PER, PER, -1>(
           f[1], rd0, FusedRefill<Loader>{ld, slot_ptr(s), wave, nt, 0}, no_sync);
     }
   }
-  wait_vmcnt<0>();  // loads past the end (zeros) land before the ring is reused
+  Loader::template wait<0>();  // loads past the end (zeros) land before the ring is reused
   w.settle();
   __syncthreads();
   typename Epi::template Run<T, G, W>{}(w, ea, g, smem, m0, n0, wm, wn, lane, tid);

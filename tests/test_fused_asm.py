@@ -1,0 +1,111 @@
+"""Hazards in the fused kernels that the compiler does not check for (CPU
+only: hipcc cross-compiles).
+
+The tiled kernels write their MFMAs, and those with transposing reads their
+direct-to-LDS loads too, as inline assembly: wait states around the MFMAs, the
+LDS address in M0 and scalar registers that a vector instruction wrote are
+theirs to mind.  These tests read the assembly that the library's own flags
+give for every unit of fused kernels.
+"""
+import os
+import re
+import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
+
+import pytest
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+import mfma_hazards  # noqa: E402
+from test_mfma_hazards import device_asm, hipcc_available  # noqa: E402
+
+from software_pipelined_tiled_pipeline_amd import build  # noqa: E402
+
+UNITS = [u for u in build.UNITS if u.startswith(("fused_gated", "fused_xent"))]
+SGPR_WAIT = 5  # wait states from a vector instruction's scalar result to a load that reads it
+
+
+@pytest.fixture(scope="module")
+def unit_asm():
+    if not hipcc_available():
+        pytest.skip("hipcc not available")
+    with tempfile.TemporaryDirectory() as tmp:
+        def one(u):
+            return u, device_asm(os.path.join(build.CSRC, u), os.path.join(tmp, u + ".s"))
+        with ThreadPoolExecutor(len(UNITS)) as pool:
+            return dict(pool.map(one, UNITS))
+
+
+@pytest.mark.parametrize("unit", UNITS)
+def test_no_mfma_hazards(unit_asm, unit):
+    hazards, mfmas = mfma_hazards.check_asm(unit_asm[unit])
+    assert mfmas > 500
+    hazards = [h for h in hazards if "fused_kernel" in h.function]  # the others' MFMAs are the compiler's
+    assert not hazards, "\n".join(f"{h.kind} line {h.line}: {h.text} ({h.detail})" for h in hazards[:20])
+
+
+def kernels(asm):
+    for m in re.finditer(r"^(_ZN5pgemm\S*fused_kernel\S*):.*?\n(.*?)s_endpgm", asm, re.S | re.M):
+        yield m.group(1), m.group(2)
+
+
+def scalars(text):
+    """Scalar registers that an operand string names."""
+    found = set()
+    for a, b in re.findall(r"\bs\[(\d+):(\d+)\]", text):
+        found.update(range(int(a), int(b) + 1))
+    found.update(int(n) for n in re.findall(r"\bs(\d+)\b", text))
+    return found
+
+
+def lds_load_faults(body):
+    """Loads into LDS whose M0 was not set for them, or that read a scalar too
+    soon after a vector instruction wrote it."""
+    faults, base, since, since_vector, loads = [], None, {}, 0, 0
+    for line in body.splitlines():
+        line = line.split(";")[0].strip()
+        if not line or line.startswith(".") and not line.endswith(":"):
+            continue
+        if line.endswith(":") or line.startswith(("s_branch", "s_cbranch")):
+            base = None  # M0 is set again in every block
+            if line.endswith(":"):
+                continue
+        op = line.split()[0]
+        states = int(line.split()[1]) + 1 if op == "s_nop" else 1
+        for r in list(since):
+            since[r] += states
+        if re.search(r"\bm0\b", line) and op.startswith(("s_", "v_")) and re.match(r"\S+\s+m0\b", line):
+            base = line
+        if op.startswith("buffer_load") and line.endswith(" lds"):
+            loads += 1
+            if base is None:
+                faults.append("M0 not set in this block: " + line)
+            soon = [r for r in scalars(line) if since.get(r, SGPR_WAIT + 1) <= SGPR_WAIT]
+            if soon:
+                faults.append(f"s{soon} written by a vector instruction just before: {line}")
+        if op.startswith("v_") and not op.startswith("v_mfma"):
+            for r in scalars(line.split(",")[0]):
+                since[r] = 0
+        elif op.startswith("s_") and len(line.split()) > 1:
+            for r in scalars(line.split(",")[0]):
+                since.pop(r, None)
+    return faults, loads
+
+
+@pytest.mark.parametrize("unit", UNITS)
+def test_loads_into_lds(unit_asm, unit):
+    seen = 0
+    for name, body in kernels(unit_asm[unit]):
+        faults, loads = lds_load_faults(body)
+        assert not faults, name + "\n" + "\n".join(faults[:10])
+        assert loads >= 8, name
+        seen += 1
+    assert seen >= 8
+
+
+def test_the_check_finds_planted_faults():
+    good = "\ts_mov_b32 m0, s3\n\ts_nop 0\n\tbuffer_load_dwordx4 v1, s[4:7], 0 offen lds\n"
+    assert lds_load_faults(good) == ([], 1)
+    assert lds_load_faults(good + ".LBB0_1:\n\tbuffer_load_dwordx4 v1, s[4:7], 0 offen offset:1024 lds\n")[0]
+    assert lds_load_faults("\tv_readfirstlane_b32 s5, v0\n" + good)[0]
+    assert not lds_load_faults("\tv_readfirstlane_b32 s5, v0\n\ts_nop 4\n" + good)[0]
