@@ -25,9 +25,62 @@ struct Carver {
   }
 };
 
-// 256 x 256 tiles when they alone nearly fill the 256 CUs, else 128 x 128
-// (the same rule as the NT calls).
-inline bool large_tile(int64_t M, int64_t N, bool dual) { return per(M, 256) * per(N, dual ? 128 : 256) >= 192; }
+// How a tiled product is cut: output tiles of 256 x 256 or 128 x 128, and
+// pieces of K whose fp32 partial sums a second kernel adds up in order.
+//
+// The cut that takes least by these times, in microseconds, which the kernels
+// were measured to need on the tiles of one CU (K tiles of 64):
+//   large, one to a CU:   1.6 a K tile and 7 to fill and store
+//   small, one to a CU:   0.72 and 7;   two to a CU: 1.0 and 9
+// so a large tile has the work of four small ones for the time of three, but
+// leaves CUs idle when there are fewer than 256, or few more than a multiple.
+// Pieces cost a second launch (4) and their sums' way to memory and back
+// (measured on 8 pieces of 1024 x 1024: 4 MB a microsecond).  Examples:
+// 2048 x 2048 x 8192 takes 90 us in 256 small tiles and 164 in 64 large ones;
+// 8192 x 2048 x 2048 takes 58 in 256 large ones and 80 in 1024 small ones.
+struct Tiling {
+  bool large;
+  int split;
+  int64_t k_chunk;  // a multiple of 64 when split
+};
+
+constexpr int kMaxPieces = 16;
+constexpr int64_t kMaxWorkItems = (int64_t)1 << 32;  // of a dispatch
+
+inline Tiling plan_tiles(int64_t M, int64_t N, int64_t K, bool dual, bool can_split) {
+  Tiling best{false, 1, K};
+  double least = -1.0;
+  for (int large = 0; large < 2; ++large) {
+    const int64_t t = large ? 256 : 128;
+    const int64_t tiles = per(M, t) * per(N, dual ? t / 2 : t);
+    for (int want = 1; want <= (can_split ? kMaxPieces : 1); ++want) {
+      const int64_t chunk = want == 1 ? K : up_to(per(K, want), 64);
+      const int split = chunk > 0 ? (int)per(K, chunk) : 1;
+      if (split != want || (want > 1 && chunk < 256)) continue;
+      const double steps = (double)per(chunk, 64);
+      const int64_t blocks = tiles * split;
+      if (!large && blocks * 512 >= kMaxWorkItems) continue;
+      double us;
+      if (large) {
+        us = (double)per(blocks, 256) * (1.6 * steps + 7.0);
+      } else {
+        const int64_t rest = blocks % 512;
+        us = (double)(blocks / 512 + (rest > 256)) * (steps + 9.0) + (rest > 0 && rest <= 256 ? 0.72 * steps + 7.0 : 0.0);
+      }
+      if (split > 1) us += 4.0 + (double)M * (double)N * (8.0 * split + 2.0) / 4e6;
+      if (least < 0.0 || us < least) {
+        least = us;
+        best = Tiling{large != 0, split, chunk};
+      }
+    }
+  }
+  return best;
+}
+
+// Bytes of a product's partial sums (rows of a multiple of 4).
+inline int64_t piece_bytes(const Tiling &t, int64_t M, int64_t N) {
+  return t.split > 1 ? t.split * M * up_to(N, 4) * 4 : 0;
+}
 
 // Rows up to which the gated block's forward call runs as a product of few
 // rows (skinny.hpp) instead of tiles.
@@ -38,7 +91,8 @@ struct GatedPlan {
   bool skinny, padded;
   int64_t d8;        // row pitch of x and W in the products
   int64_t py;        // row pitch of dy
-  int64_t x, w, dy;  // workspace offsets
+  int64_t x, w, dy, part;  // workspace offsets
+  Tiling forward, dx, dw;
   int64_t bytes;
 };
 
@@ -53,7 +107,14 @@ inline GatedPlan plan_gated(int64_t M, int64_t F, int64_t D, bool backward, bool
     p.x = c.take(M * p.d8 * 2);
     p.w = c.take(2 * F * p.d8 * 2);
   }
-  if (backward) p.dy = c.take(M * p.py * 2);
+  p.forward = plan_tiles(M, F, p.d8, true, false);
+  if (backward) {
+    p.dy = c.take(M * p.py * 2);
+    p.dx = plan_tiles(M, D, 2 * F, false, true);
+    p.dw = plan_tiles(2 * F, D, M, false, true);
+    const int64_t a = piece_bytes(p.dx, M, D), b = piece_bytes(p.dw, 2 * F, D);
+    p.part = c.take(a > b ? a : b);
+  }
   p.bytes = c.bytes;
   return p;
 }
@@ -70,6 +131,7 @@ struct XentPlan {
   int64_t pz;     // row pitch of a piece of dz
   int64_t ps;     // row pitch of the running sum of dx
   int64_t x, w, part, at, dz, sum, scale;
+  Tiling logits, dx, dw;  // of a whole piece
   int64_t bytes;
 };
 
@@ -83,8 +145,9 @@ inline XentPlan plan_xent(int64_t M, int64_t V, int64_t D, bool backward) {
     p.w = c.take(V * p.d8 * 2);
   }
   if (!backward) {
+    p.logits = plan_tiles(M, V, p.d8, false, false);
     // wave columns: 128 on the large tile, 32 on the small one
-    p.parts = large_tile(M, V, false) ? per(V, 256) * 2 : per(V, 128) * 4;
+    p.parts = p.logits.large ? per(V, 256) * 2 : per(V, 128) * 4;
     p.part = c.take(p.parts * M * 8);
     p.at = c.take(M * 4);
   } else {
@@ -93,6 +156,11 @@ inline XentPlan plan_xent(int64_t M, int64_t V, int64_t D, bool backward) {
     if (p.piece > V) p.piece = V;
     p.pz = up_to(p.piece, 8);
     p.ps = up_to(D, 4);
+    p.logits = plan_tiles(M, p.piece, p.d8, false, false);
+    p.dx = plan_tiles(M, D, p.piece, false, true);
+    p.dw = plan_tiles(p.piece, D, M, false, true);
+    const int64_t a = piece_bytes(p.dx, M, D), b = piece_bytes(p.dw, p.piece, D);
+    p.part = c.take(a > b ? a : b);
     p.dz = c.take(M * p.pz * 2);
     if (p.piece < V) p.sum = c.take(M * p.ps * 4);
     p.scale = c.take(8);

@@ -12,14 +12,13 @@ constexpr int64_t kMaxDim = (int64_t)1 << 31;
 // Widths that are a row pitch inside a product (D, 2 F, K): a tile's rows or
 // its 64 K rows then stay below 2^31 bytes, the reach of a buffer offset.
 constexpr int64_t kMaxPitch = (int64_t)1 << 22;
-constexpr int64_t kMaxWorkItems = (int64_t)1 << 32;
 
 bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 bool missing(const void *p, int64_t n) { return n > 0 && !p; }
 bool dim(int64_t n) { return n >= 0 && n < kMaxDim; }
 bool pitch(int64_t n) { return n >= 0 && n <= kMaxPitch; }
-// a product's grid, in work-items, fits a dispatch (512 threads a small tile,
-// which an output of 192 large tiles or more does not take; 256 a large one)
+// a product's grid, in work-items, fits a dispatch in large tiles of 256 x 128
+// columns or more (plan_tiles takes no cut that does not)
 bool grid_fits(int64_t M, int64_t N) { return per(M, 256) * per(N, 128) * 256 < kMaxWorkItems; }
 bool act_ok(int act) { return act == PGEMM_ACT_SILU || act == PGEMM_ACT_GELU; }
 

@@ -134,6 +134,31 @@ struct SumEpi {
   };
 };
 
+// A piece of K: the sums as they are, fp32, for join_pieces_kernel.
+struct PieceEpi {
+  struct Args {
+    float *part;  // [pieces][M][pp]
+    int pp;       // a multiple of 4
+  };
+  template <typename T, class G, class W>
+  struct Run {
+    __device__ __forceinline__ void operator()(W &w, const Args &e, const FusedProduct &g, char *smem, int m0, int n0,
+                                               int wm, int wn, int lane, int tid) const {
+      float *part = e.part + (int64_t)g.piece * g.M * e.pp;
+#pragma unroll
+      for (int i = 0; i < W::TM; ++i) {
+        const int row = m0 + wm * G::WM + 16 * i + (lane & 15);
+        if (row >= g.M) continue;
+#pragma unroll
+        for (int j = 0; j < W::TN; ++j) {
+          const int col = n0 + wn * G::WN + 16 * j + 4 * (lane >> 4);
+          if (col < g.N) *reinterpret_cast<f32x4 *>(part + (int64_t)row * e.pp + col) = w.acc[i][j];
+        }
+      }
+    }
+  };
+};
+
 // Gated block: even column blocks of a wave hold the gate, odd ones the up
 // projection of the same 16 hidden columns.  h = act(gate) * up; `saved`
 // (null: not kept) takes both projections in fp32, per row and group of four

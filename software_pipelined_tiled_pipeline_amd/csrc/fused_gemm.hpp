@@ -48,6 +48,8 @@ struct FusedProduct {
   FusedOperand a, b;
   int M, N, K;  // N counts output columns (of one matrix when DUAL)
   int tiles_m, tiles_n, group_m;
+  int k_chunk;  // K of a piece (a multiple of 64), or K
+  int piece;    // set in the kernel: which piece this workgroup does
 };
 
 // Granules of a KR tile: 16 bytes of a k row; the row's 32-byte pairs are
@@ -202,8 +204,8 @@ struct FusedLoader {
     }
   }
 
-  __device__ __forceinline__ void init(const FusedProduct &g, int m0, int n0, int wave) {
-    K = g.K;
+  __device__ __forceinline__ void init(const FusedProduct &g, int m0, int n0, int wave, int k_end) {
+    K = k_end;
     if (wave < WAVES / 2)
       lay_out<LA, G::BM, false>(g.a, m0, wave * PER);
     else
@@ -322,10 +324,14 @@ __global__ void __launch_bounds__(G::THREADS, G::OCC) fused_kernel(FusedProduct 
   constexpr int ON = DUAL ? G::BN / 2 : G::BN;  // output columns of a tile
   const int m0 = bm * G::BM, n0 = bn * ON;
   const int wm = wave / G::WGN, wn = wave % G::WGN;
-  const int n_k = (int)(((int64_t)g.K + G::BK - 1) / G::BK);
+  g.piece = split;
+  const int64_t k_end = ((int64_t)split + 1) * g.k_chunk;
+  const int k_last = k_end < g.K ? (int)k_end : g.K;
+  const int t0 = split * (g.k_chunk / G::BK);  // first K tile
+  const int n_k = (int)(((int64_t)k_last + G::BK - 1) / G::BK) - t0;
 
   Loader ld;
-  ld.init(g, m0, n0, wave);
+  ld.init(g, m0, n0, wave, k_last);
   FragSource<LA, G::BM> fa;
   FragSource<LB, G::BN> fb;
   fa.init(wm * G::WM, lane);
@@ -342,7 +348,7 @@ __global__ void __launch_bounds__(G::THREADS, G::OCC) fused_kernel(FusedProduct 
   W w;
   w.zero();
   for (int j = 0; j < 2; ++j) {
-    const typename Loader::Tile s = ld.tile(j);
+    const typename Loader::Tile s = ld.tile(t0 + j);
 #pragma unroll
     for (int i = 0; i < PER; ++i) ld.load_one(slot_ptr(j), wave, s, i);
   }
@@ -354,7 +360,7 @@ __global__ void __launch_bounds__(G::THREADS, G::OCC) fused_kernel(FusedProduct 
   }
   for (int t = 0; t < n_k; ++t) {
     const int s = t & 1;
-    const typename Loader::Tile nt = ld.tile(t + 2);
+    const typename Loader::Tile nt = ld.tile(t0 + t + 2);
     auto rd1 = [&](int r) __attribute__((always_inline)) { read(f[1], s, 1, r); };
     auto rd0 = [&](int r) __attribute__((always_inline)) { read(f[0], s ^ 1, 0, r); };
     if constexpr (W::TM * W::TN == 64) {

@@ -7,6 +7,39 @@
 #include "launch_impl.hpp"
 
 namespace pgemm {
+
+// Adds the pieces' partial sums up in the order of K, four columns a thread,
+// and does with the sum what SumEpi does with a product's.
+template <typename T>
+__global__ void __launch_bounds__(256) join_pieces_kernel(const float *__restrict__ part, int pieces, int M, int N, int pp,
+                                                          SumEpi::Args e) {
+  const int per_row = pp / 4;
+  const int64_t total = (int64_t)M * per_row, stride = (int64_t)M * pp;
+  const float k = e.last && e.out.scale ? *e.out.scale : 1.0f;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per_row;
+    const int col = (int)(i % per_row) * 4;
+    const float *p = part + i * 4;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int s = 0; s < pieces; ++s) v += *reinterpret_cast<const f32x4 *>(p + s * stride);
+    if (!e.first) v += *reinterpret_cast<const f32x4 *>(e.sum + row * e.ps + col);
+    if (!e.last) {
+      *reinterpret_cast<f32x4 *>(e.sum + row * e.ps + col) = v;
+      continue;
+    }
+    const u32x2 r = Mfma<T>::pack4(v[0] * k, v[1] * k, v[2] * k, v[3] * k);
+    uint16_t *dst = e.out.out + row * e.out.po + col;
+    if (col + 4 <= N) {
+      *reinterpret_cast<u32x2_any *>(dst) = r;
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (col + x < N) dst[x] = (uint16_t)(r[x / 2] >> (16 * (x % 2)));
+    }
+  }
+}
+
 namespace launch_detail {
 
 inline unsigned row_grid(int64_t items) {
@@ -15,7 +48,7 @@ inline unsigned row_grid(int64_t items) {
 }
 
 template <typename T, class G, Lay LA, Lay LB, bool DUAL, class Epi>
-pgemm_status launch_tiles(FusedProduct g, const typename Epi::Args &e, hipStream_t stream, int dev) {
+pgemm_status launch_tiles(FusedProduct g, const Tiling &t, const typename Epi::Args &e, hipStream_t stream, int dev) {
   static std::atomic<uint64_t> lds_set{0};
   auto kern = fused_kernel<T, G, LA, LB, DUAL, Epi>;
   pgemm_status st = allow_lds(kern, G::LDS_BYTES, dev, lds_set);
@@ -23,16 +56,37 @@ pgemm_status launch_tiles(FusedProduct g, const typename Epi::Args &e, hipStream
   g.tiles_m = cdiv_i(g.M, G::BM);
   g.tiles_n = cdiv_i(g.N, DUAL ? G::BN / 2 : G::BN);
   g.group_m = kGroupM;
-  hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n)), dim3(G::THREADS), G::LDS_BYTES, stream, g,
-                     e);
+  g.k_chunk = (int)t.k_chunk;
+  hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n * t.split)), dim3(G::THREADS), G::LDS_BYTES,
+                     stream, g, e);
   return launched();
 }
 
 template <typename T, Lay LA, Lay LB, bool DUAL, class Epi>
-pgemm_status launch_product(const FusedProduct &g, const typename Epi::Args &e, hipStream_t stream, int dev) {
+pgemm_status launch_product(const FusedProduct &g, const Tiling &t, const typename Epi::Args &e, hipStream_t stream,
+                            int dev) {
   if (g.M == 0 || g.N == 0) return PGEMM_OK;
-  if (large_tile(g.M, g.N, DUAL)) return launch_tiles<T, SwapGeom<2>, LA, LB, DUAL, Epi>(g, e, stream, dev);
-  return launch_tiles<T, SwapGeomSmall<2>, LA, LB, DUAL, Epi>(g, e, stream, dev);
+  if (t.large) return launch_tiles<T, SwapGeom<2>, LA, LB, DUAL, Epi>(g, t, e, stream, dev);
+  return launch_tiles<T, SwapGeomSmall<2>, LA, LB, DUAL, Epi>(g, t, e, stream, dev);
+}
+
+// out = round(scale * (A B + what is in sum)): one product, or one of a series
+// (SumEpi), in pieces of K as `t` says; `part` holds their partial sums.
+template <typename T, Lay LA, Lay LB>
+pgemm_status launch_sum(const FusedProduct &g, const Tiling &t, const SumEpi::Args &e, char *part, hipStream_t stream,
+                        int dev) {
+  if (g.M == 0 || g.N == 0) return PGEMM_OK;
+  if (t.split > 1) {
+    const int pp = (int)up_to(g.N, 4);
+    float *sums = reinterpret_cast<float *>(part);
+    pgemm_status st = launch_product<T, LA, LB, false, PieceEpi>(g, t, PieceEpi::Args{sums, pp}, stream, dev);
+    if (st != PGEMM_OK) return st;
+    hipLaunchKernelGGL(join_pieces_kernel<T>, dim3(row_grid((int64_t)g.M * (pp / 4))), dim3(256), 0, stream, sums, t.split,
+                       g.M, g.N, pp, e);
+    return launched();
+  }
+  if (e.first && e.last) return launch_product<T, LA, LB, false, StoreEpi>(g, t, e.out, stream, dev);
+  return launch_product<T, LA, LB, false, SumEpi>(g, t, e, stream, dev);
 }
 
 }  // namespace launch_detail

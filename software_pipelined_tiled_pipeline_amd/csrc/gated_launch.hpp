@@ -103,7 +103,7 @@ pgemm_status gated_forward(const GatedCall &c) {
   const uint16_t *x, *w;
   pgemm_status st = gated_operands<T>(c, p, &x, &w);
   if (st != PGEMM_OK) return st;
-  return launch_product<T, Lay::KC, Lay::KC, true, GatedEpi>(projections(c, p, x, w),
+  return launch_product<T, Lay::KC, Lay::KC, true, GatedEpi>(projections(c, p, x, w), p.forward,
                                                              GatedEpi::Args{c.h, c.saved, c.act}, c.stream, c.dev);
 }
 
@@ -124,7 +124,7 @@ pgemm_status gated_backward(const GatedCall &c) {
       st = launched();
     } else {
       st = launch_product<T, Lay::KC, Lay::KC, true, GatedSlopeEpi>(
-          projections(c, p, x, w), GatedSlopeEpi::Args{c.dh, dy, p.py, c.act}, c.stream, c.dev);
+          projections(c, p, x, w), p.forward, GatedSlopeEpi::Args{c.dh, dy, p.py, c.act}, c.stream, c.dev);
     }
     if (st == PGEMM_OK && p.py != F2) {  // the pad meets W rows that read zero, and must be finite
       hipLaunchKernelGGL(zero_tail_kernel, dim3(row_grid(c.M * (p.py - F2))), dim3(256), 0, c.stream, dy, c.M, (int)F2,
@@ -140,7 +140,8 @@ pgemm_status gated_backward(const GatedCall &c) {
   g.M = (int)c.M;
   g.N = (int)c.D;
   g.K = (int)F2;
-  st = launch_product<T, Lay::KC, Lay::KR, false, StoreEpi>(g, StoreEpi::Args{c.dx, c.D, nullptr}, c.stream, c.dev);
+  st = launch_sum<T, Lay::KC, Lay::KR>(g, p.dx, SumEpi::Args{nullptr, 0, 1, 1, {c.dx, c.D, nullptr}}, c.ws + p.part,
+                                       c.stream, c.dev);
   if (st != PGEMM_OK) return st;
   // dW = dy^T x
   g.a = FusedOperand{dy, nullptr, (int)p.py, (int)F2};
@@ -148,7 +149,8 @@ pgemm_status gated_backward(const GatedCall &c) {
   g.M = (int)F2;
   g.N = (int)c.D;
   g.K = (int)c.M;
-  return launch_product<T, Lay::KR, Lay::KR, false, StoreEpi>(g, StoreEpi::Args{c.dw, c.D, nullptr}, c.stream, c.dev);
+  return launch_sum<T, Lay::KR, Lay::KR>(g, p.dw, SumEpi::Args{nullptr, 0, 1, 1, {c.dw, c.D, nullptr}}, c.ws + p.part,
+                                         c.stream, c.dev);
 }
 
 }  // namespace launch_detail

@@ -94,7 +94,8 @@ pgemm_status xent_forward(const XentCall &c) {
   g.M = (int)c.M;
   g.N = (int)c.V;
   g.K = (int)p.d8;
-  st = launch_product<T, Lay::KC, Lay::KC, false, LseEpi>(g, LseEpi::Args{part, at, c.target}, c.stream, c.dev);
+  st = launch_product<T, Lay::KC, Lay::KC, false, LseEpi>(g, p.logits, LseEpi::Args{part, at, c.target}, c.stream,
+                                                          c.dev);
   if (st != PGEMM_OK) return st;
   hipLaunchKernelGGL(lse_join_kernel<T>, dim3((unsigned)per(c.M, 64)), dim3(1024), 0, c.stream, part, at, c.target, c.loss,
                      c.lse, c.M, c.V, (int)p.parts, c.ignore);
@@ -126,7 +127,8 @@ pgemm_status xent_backward(const XentCall &c) {
     g.N = (int)n;
     g.K = (int)p.d8;
     st = launch_product<T, Lay::KC, Lay::KC, false, SlopeEpi>(
-        g, SlopeEpi::Args{dz, p.pz, c.lse_in, c.dloss, c.dstep, c.target, scale, c.ignore, v0, c.V}, c.stream, c.dev);
+        g, n == p.piece ? p.logits : plan_tiles(c.M, n, p.d8, false, false),
+        SlopeEpi::Args{dz, p.pz, c.lse_in, c.dloss, c.dstep, c.target, scale, c.ignore, v0, c.V}, c.stream, c.dev);
     if (st != PGEMM_OK) return st;
     // dW rows of this piece = dz^T x
     g.a = FusedOperand{dz, nullptr, (int)p.pz, (int)n};
@@ -134,8 +136,9 @@ pgemm_status xent_backward(const XentCall &c) {
     g.M = (int)n;
     g.N = (int)c.D;
     g.K = (int)c.M;
-    st = launch_product<T, Lay::KR, Lay::KR, false, StoreEpi>(g, StoreEpi::Args{c.dw + v0 * c.D, c.D, unscale},
-                                                              c.stream, c.dev);
+    st = launch_sum<T, Lay::KR, Lay::KR>(g, n == p.piece ? p.dw : plan_tiles(n, c.D, c.M, false, false),
+                                         SumEpi::Args{nullptr, 0, 1, 1, {c.dw + v0 * c.D, c.D, unscale}}, c.ws + p.part,
+                                         c.stream, c.dev);
     if (st != PGEMM_OK) return st;
     // dx += dz W
     g.a = FusedOperand{dz, nullptr, (int)p.pz, (int)c.M};
@@ -143,13 +146,9 @@ pgemm_status xent_backward(const XentCall &c) {
     g.M = (int)c.M;
     g.N = (int)c.D;
     g.K = (int)n;
-    const StoreEpi::Args out{c.dx, c.D, unscale};
-    const bool first = v0 == 0, last = v0 + n == c.V;
-    if (first && last)
-      st = launch_product<T, Lay::KC, Lay::KR, false, StoreEpi>(g, out, c.stream, c.dev);
-    else
-      st = launch_product<T, Lay::KC, Lay::KR, false, SumEpi>(g, SumEpi::Args{sum, (int)p.ps, first, last, out},
-                                                              c.stream, c.dev);
+    st = launch_sum<T, Lay::KC, Lay::KR>(
+        g, n == p.piece ? p.dx : plan_tiles(c.M, c.D, n, false, false),
+        SumEpi::Args{sum, (int)p.ps, v0 == 0, v0 + n == c.V, {c.dx, c.D, unscale}}, c.ws + p.part, c.stream, c.dev);
     if (st != PGEMM_OK) return st;
   }
   return PGEMM_OK;
