@@ -12,6 +12,17 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // e^x through v_exp_f32 (2^x): the product's rounding costs |x| 2^-24.
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
+// 2^(x log2 e - off), the exponential of a logit from its row's log2 e * reference
+__device__ __forceinline__ float exp_from(float x, float off) {
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2e, -off));
+}
+// The larger of three in one instruction (a NaN may get lost).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
 // The gate's activation and its derivative in fp32.  act 0: silu, g s(g);
 // act 1: gelu in its tanh form, (1 + tanh y) / 2 = s(2 y).  The derivative's
 // polynomial is taken at |g| <= 64 so that its square does not overflow into
@@ -255,8 +266,29 @@ struct GatedSlopeEpi {
   };
 };
 
+// A lane's logits of one row, columns c0 + 16 j + x: those past N, at the
+// vocabulary's end, are minus infinity.  (A copy: the accumulators themselves,
+// written here, would be spilled all through the K loop.)
+template <class G, class W>
+struct RowLogits {
+  f32x4 v[W::TN];
+  __device__ __forceinline__ RowLogits(const W &w, int i, bool edge, int c0, int N) {
+#pragma unroll
+    for (int j = 0; j < W::TN; ++j) v[j] = w.acc[i][j];
+    if (edge) {
+#pragma unroll
+      for (int j = 0; j < W::TN; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (c0 + 16 * j + x >= N) v[j][x] = -INFINITY;
+    }
+  }
+};
+
 // Softmax statistics of a tile of logits: per row and wave column the
-// largest logit and the sum of e^(z - largest), and the target's logit.
+// largest logit and the sum of e^(z - largest), and the target's logit.  A
+// tile's 256 values a lane cost 1.5 plain operations and an exponential each;
+// what few rows need, the vocabulary's end and the targets, is branched around.
 struct LseEpi {
   struct Args {
     float2 *part;  // [tiles_n * WGN][M]
@@ -269,44 +301,45 @@ struct LseEpi {
                                                int wm, int wn, int lane, int tid) const {
       const int r = lane & 15, q = lane >> 4;
       const int c0 = n0 + wn * G::WN + 4 * q;
-      const bool edge = n0 + G::BN > g.N;
+      const int row0 = m0 + wm * G::WM + r;
       float2 *part = e.part + (int64_t)((n0 / G::BN) * G::WGN + wn) * g.M;
+      int64_t target[W::TM];
+#pragma unroll
+      for (int i = 0; i < W::TM; ++i) target[i] = e.target[row0 + 16 * i < g.M ? row0 + 16 * i : g.M - 1];
+      const bool edge = n0 + G::BN > g.N;
 #pragma unroll
       for (int i = 0; i < W::TM; ++i) {
-        const int row = m0 + wm * G::WM + 16 * i + r;
+        const int row = row0 + 16 * i;
         const bool in = row < g.M;
-        const int64_t t = in ? e.target[row] - c0 : -1;
-        const int tc = t >= 0 && t < G::WN ? (int)t : -1;  // column within the lane's blocks
-        float top = -INFINITY, z = 0.0f;
-        bool mine = false;
+        const RowLogits<G, W> z(w, i, edge, c0, g.N);
+        float top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < W::TN; ++j)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            float v = w.acc[i][j][x];
-            if (edge && c0 + 16 * j + x >= g.N) v = -INFINITY;
-            if (tc == 16 * j + x) {
-              z = v;
-              mine = true;
-            }
-            top = fmaxf(top, v);  // a NaN shows in the sum
-          }
+        for (int j = 0; j < W::TN; ++j) {
+          top = max3(top, z.v[j][0], z.v[j][1]);  // a NaN shows in the sum
+          top = max3(top, z.v[j][2], z.v[j][3]);
+        }
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float ref = top == -INFINITY ? 0.0f : top;  // no finite logit here: the sum is zero, not 0/0
+        const float off = top == -INFINITY ? 0.0f : top * kLog2e;  // no finite logit here: the sum is zero, not 0/0
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < W::TN; ++j)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            float v = w.acc[i][j][x];
-            if (edge && c0 + 16 * j + x >= g.N) v = -INFINITY;
-            sum += fast_exp(v - ref);
-          }
+          for (int x = 0; x < 4; ++x) sum += exp_from(z.v[j][x], off);
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
         if (in && q == 0) part[row] = make_float2(top, sum);
-        if (in && mine) e.at[row] = z;
+        const int64_t t = target[i] - c0;  // column within the lane's blocks
+        const bool mine = in && t >= 0 && t < G::WN && (t & 15) < 4;
+        if (__any(mine)) {
+          float at = 0.0f;
+#pragma unroll
+          for (int j = 0; j < W::TN; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (t == 16 * j + x) at = z.v[j][x];
+          if (mine) e.at[row] = at;
+        }
       }
     }
   };
@@ -342,33 +375,45 @@ struct SlopeEpi {
                                                int wm, int wn, int lane, int tid) const {
       const int r = lane & 15, q = lane >> 4;
       const int c0 = n0 + wn * G::WN + 4 * q;
-      const bool edge = n0 + G::BN > g.N;
-      const float top = *e.top;
+      const int row0 = m0 + wm * G::WM + r;
+      int64_t target[W::TM];
+      float lse[W::TM], dloss[W::TM];
 #pragma unroll
       for (int i = 0; i < W::TM; ++i) {
-        const int row = m0 + wm * G::WM + 16 * i + r;
-        float s = 0.0f, lse = 0.0f;
-        int tc = -1;
-        if (row < g.M) {
-          const int64_t t = e.target[row];
-          lse = e.lse[row];
-          s = t == e.ignore ? 0.0f : (t < 0 || t >= e.V) ? NAN : e.dloss[(int64_t)row * e.dstep] / top * kDzUnit<T>;
-          const int64_t d = t - e.v0 - c0;
-          tc = d >= 0 && d < G::WN ? (int)d : -1;
+        const int row = row0 + 16 * i < g.M ? row0 + 16 * i : g.M - 1;
+        target[i] = e.target[row];
+        lse[i] = e.lse[row];
+        dloss[i] = e.dloss[(int64_t)row * e.dstep];
+      }
+      const float top = *e.top;
+      const bool edge = n0 + G::BN > g.N;
+#pragma unroll
+      for (int i = 0; i < W::TM; ++i) {
+        const int64_t t = target[i];
+        const float s = t == e.ignore ? 0.0f : (t < 0 || t >= e.V) ? NAN : dloss[i] / top * kDzUnit<T>;
+        const uint32_t keep = s == 0.0f ? 0u : ~0u;  // an ignored row is zero whatever its logits are
+        const float off = lse[i] * kLog2e;
+        RowLogits<G, W> z(w, i, edge, c0, g.N);
+#pragma unroll
+        for (int j = 0; j < W::TN; ++j)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) z.v[j][x] = exp_from(z.v[j][x], off);
+        const int64_t d = t - e.v0 - c0;  // column within the lane's blocks
+        if (__any(d >= 0 && d < G::WN && (d & 15) < 4)) {
+#pragma unroll
+          for (int j = 0; j < W::TN; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (d == 16 * j + x) z.v[j][x] -= 1.0f;
         }
 #pragma unroll
         for (int j = 0; j < W::TN; ++j) {
-          f32x4 v;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            float p = fast_exp(w.acc[i][j][x] - lse);
-            if (tc == 16 * j + x) p -= 1.0f;
-            p = s == 0.0f ? 0.0f : p * s;  // an ignored row is zero whatever its logits are
-            if (edge && c0 + 16 * j + x >= g.N) p = 0.0f;
-            v[x] = p;
-          }
+          const f32x4 v = z.v[j];
+          u32x2 p = Mfma<T>::pack4(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
+          p[0] &= keep;
+          p[1] &= keep;
           char *dst = smem + (wm * G::WM + 16 * i + r) * Staging<G::BN>::PITCH + (wn * G::WN + 16 * j + 4 * q) * 2;
-          *reinterpret_cast<u32x2 *>(dst) = Mfma<T>::pack4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<u32x2 *>(dst) = p;
         }
       }
       __syncthreads();

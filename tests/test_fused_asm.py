@@ -103,6 +103,16 @@ def test_loads_into_lds(unit_asm, unit):
     assert seen >= 8
 
 
+@pytest.mark.parametrize("unit", UNITS)
+def test_no_spills_among_mfmas(unit_asm, unit):
+    # a spilled accumulator would be read without an MFMA's wait states, and
+    # the memory it goes to counts among the loads that the kernel waits for
+    for name, body in kernels(unit_asm[unit]):
+        for block in re.split(r"\n(?=\.LBB)", body):
+            if block.count("v_mfma") >= 8:
+                assert "scratch_" not in block, name
+
+
 def test_the_check_finds_planted_faults():
     good = "\ts_mov_b32 m0, s3\n\ts_nop 0\n\tbuffer_load_dwordx4 v1, s[4:7], 0 offen lds\n"
     assert lds_load_faults(good) == ([], 1)
