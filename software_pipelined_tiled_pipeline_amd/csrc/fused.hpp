@@ -26,20 +26,24 @@ struct Carver {
 };
 
 // How a tiled product is cut: output tiles of 256 x 256 or 128 x 128, and
-// pieces of K whose fp32 partial sums a second kernel adds up in order.
+// pieces of K whose fp32 partial sums a second kernel adds up in order.  Small
+// tiles that are at most one to a CU run with four ring slots (`deep`): alone
+// on a CU a tile waits for its loads most of the time, and with two slots it
+// took 0.72 us a K tile.
 //
 // The cut that takes least by these times, in microseconds, which the kernels
-// were measured to need on the tiles of one CU (K tiles of 64):
-//   large, one to a CU:   1.6 a K tile and 7 to fill and store
-//   small, one to a CU:   0.72 and 7;   two to a CU: 1.0 and 9
-// so a large tile has the work of four small ones for the time of three, but
-// leaves CUs idle when there are fewer than 256, or few more than a multiple.
-// Pieces cost a second launch (4) and their sums' way to memory and back
-// (measured on 8 pieces of 1024 x 1024: 4 MB a microsecond).  Examples:
-// 2048 x 2048 x 8192 takes 90 us in 256 small tiles and 164 in 64 large ones;
-// 8192 x 2048 x 2048 takes 58 in 256 large ones and 80 in 1024 small ones.
+// were measured to need for the tiles of one CU (K tiles of 64):
+//   large, one to a CU:         1.6 a K tile and 7 to fill and store
+//   small, deep, one to a CU:   0.45 and 6
+//   small, two to a CU:         1.0 and 9 (0.72 and 7 for one left over)
+// so a large tile has the work of four small ones for less than the time of
+// four, but leaves CUs idle when there are fewer than 256, or few more than a
+// multiple.  Pieces cost a second launch (4) and their sums' way to memory and
+// back (4 MB a microsecond).  Examples: 2048 x 2048 x 4096 takes 39 us in 256
+// small deep tiles, 52 with two slots; 8192 x 2048 x 2048 takes 58 in 256 large
+// ones and 80 in 1024 small ones.
 struct Tiling {
-  bool large;
+  bool large, deep;
   int split;
   int64_t k_chunk;  // a multiple of 64 when split
 };
@@ -48,7 +52,7 @@ constexpr int kMaxPieces = 16;
 constexpr int64_t kMaxWorkItems = (int64_t)1 << 32;  // of a dispatch
 
 inline Tiling plan_tiles(int64_t M, int64_t N, int64_t K, bool dual, bool can_split) {
-  Tiling best{false, 1, K};
+  Tiling best{false, false, 1, K};
   double least = -1.0;
   for (int large = 0; large < 2; ++large) {
     const int64_t t = large ? 256 : 128;
@@ -66,15 +70,26 @@ inline Tiling plan_tiles(int64_t M, int64_t N, int64_t K, bool dual, bool can_sp
       } else {
         const int64_t rest = blocks % 512;
         us = (double)(blocks / 512 + (rest > 256)) * (steps + 9.0) + (rest > 0 && rest <= 256 ? 0.72 * steps + 7.0 : 0.0);
+        if (blocks <= 256) us = 0.45 * steps + 6.0;
       }
       if (split > 1) us += 4.0 + (double)M * (double)N * (8.0 * split + 2.0) / 4e6;
       if (least < 0.0 || us < least) {
         least = us;
-        best = Tiling{large != 0, split, chunk};
+        best = Tiling{large != 0, !large && blocks <= 256, split, chunk};
       }
     }
   }
   return best;
+}
+
+// The same cut for a product with fewer rows, columns or less K.
+inline Tiling shortened(Tiling t, int64_t K) {
+  if (t.split > 1) {
+    t.split = (int)per(K, t.k_chunk);
+    if (t.split < 1) t.split = 1;
+  }
+  if (t.split == 1) t.k_chunk = K;
+  return t;
 }
 
 // Bytes of a product's partial sums (rows of a multiple of 4).
@@ -127,7 +142,7 @@ struct XentPlan {
   bool padded;
   int64_t d8;
   int64_t parts;  // softmax statistics per row
-  int64_t piece;  // vocabulary rows per piece
+  int64_t piece;  // vocabulary rows per piece, the last one's may be fewer
   int64_t pz;     // row pitch of a piece of dz
   int64_t ps;     // row pitch of the running sum of dx
   int64_t x, w, part, at, dz, sum, scale;
@@ -153,7 +168,11 @@ inline XentPlan plan_xent(int64_t M, int64_t V, int64_t D, bool backward) {
   } else {
     p.piece = kPieceBytes / (2 * (M > 0 ? M : 1)) / 256 * 256;
     if (p.piece < 256) p.piece = 256;
-    if (p.piece > V) p.piece = V;
+    // pieces alike, so that the last one is no short one
+    if (p.piece < V)
+      p.piece = up_to(per(V, per(V, p.piece)), 256);
+    else
+      p.piece = V;
     p.pz = up_to(p.piece, 8);
     p.ps = up_to(D, 4);
     p.logits = plan_tiles(M, p.piece, p.d8, false, false);

@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(G::THREADS, G::OCC) fused_kernel(FusedProduct 
   using Loader = FusedLoader<G, LA, LB, DUAL>;
   using W = WaveTile<T, G::WM, G::WN, G::BK>;
   constexpr int S = G::S, PER = Loader::PER, NR = W::TM + W::TN;
-  static_assert(G::P == 0 && S == 2 && W::NK == 2, "two slots of two k32 steps");
+  static_assert(G::P == 0 && W::NK == 2, "slots of two k32 steps");
   extern __shared__ __attribute__((aligned(16))) char smem[];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -347,23 +347,24 @@ __global__ void __launch_bounds__(G::THREADS, G::OCC) fused_kernel(FusedProduct 
 
   W w;
   w.zero();
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < S; ++j) {
     const typename Loader::Tile s = ld.tile(t0 + j);
 #pragma unroll
     for (int i = 0; i < PER; ++i) ld.load_one(slot_ptr(j), wave, s, i);
   }
-  Loader::template wait<PER>();
+  Loader::template wait<(S - 1) * PER>();
   lds_barrier();
   if (n_k > 0) {
 #pragma unroll
     for (int r = 0; r < NR; ++r) read(f[0], 0, 0, r);
   }
   for (int t = 0; t < n_k; ++t) {
-    const int s = t & 1;
-    const typename Loader::Tile nt = ld.tile(t0 + t + 2);
+    const int s = t % S;
+    const typename Loader::Tile nt = ld.tile(t0 + t + S);
     auto rd1 = [&](int r) __attribute__((always_inline)) { read(f[1], s, 1, r); };
-    auto rd0 = [&](int r) __attribute__((always_inline)) { read(f[0], s ^ 1, 0, r); };
+    auto rd0 = [&](int r) __attribute__((always_inline)) { read(f[0], (t + 1) % S, 0, r); };
     if constexpr (W::TM * W::TN == 64) {
+      static_assert(S == 2, "the placement refills the slot of this tile");
       using Pl = SplitSyncPlacement<64>;
       static_assert(PER == Pl::NLA + Pl::NLB, "every load of the wave's share is placed");
       auto war = []() __attribute__((always_inline)) { lds_barrier(); };
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(G::THREADS, G::OCC) fused_kernel(FusedProduct 
       NoLoads none;
       auto no_sync = []() __attribute__((always_inline)) {};
       w.template sched_step<0, 1, NR, 0, 1, 0, -1>(f[0], rd1, none, no_sync);
-      Loader::template wait<0>();  // tile t + 1 landed
+      Loader::template wait<(S - 2) * PER>();  // tile t + 1 landed
       lds_barrier();    // and slot s is free
       w.template sched_step<0, 1, NR, NM / PER - 1, NM / PER, PER, -1>(
           f[1], rd0, FusedRefill<Loader>{ld, slot_ptr(s), wave, nt, 0}, no_sync);

@@ -67,6 +67,7 @@ pgemm_status launch_product(const FusedProduct &g, const Tiling &t, const typena
                             int dev) {
   if (g.M == 0 || g.N == 0) return PGEMM_OK;
   if (t.large) return launch_tiles<T, SwapGeom<2>, LA, LB, DUAL, Epi>(g, t, e, stream, dev);
+  if (t.deep) return launch_tiles<T, SwapGeomSmall<4>, LA, LB, DUAL, Epi>(g, t, e, stream, dev);
   return launch_tiles<T, SwapGeomSmall<2>, LA, LB, DUAL, Epi>(g, t, e, stream, dev);
 }
 

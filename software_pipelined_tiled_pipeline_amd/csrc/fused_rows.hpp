@@ -5,15 +5,19 @@
 
 namespace pgemm {
 
-// dst[rows][pitch] = src[rows][cols], zeros from cols on (pitch a multiple of 8).
-static __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t *__restrict__ src, uint16_t *__restrict__ dst,
-                                                       int64_t rows, int cols, int pitch) {
+// dst[rows][pitch] = src[rows][cols], zeros from cols on (pitch a multiple of
+// 8), for two matrices of the same width.
+static __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t *__restrict__ a, uint16_t *__restrict__ pa,
+                                                       int64_t rows_a, const uint16_t *__restrict__ b,
+                                                       uint16_t *__restrict__ pb, int64_t rows_b, int cols, int pitch) {
   const int per = pitch / 8;
-  const int64_t total = rows * per;
+  const int64_t total = (rows_a + rows_b) * per;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / per;
+    const int64_t at = i / per;
+    const bool first = at < rows_a;
+    const int64_t row = first ? at : at - rows_a;
     const int c = (int)(i % per) * 8;
-    const uint16_t *s = src + row * cols + c;
+    const uint16_t *s = (first ? a : b) + row * cols + c;
     u32x4 v = {0u, 0u, 0u, 0u};
     if (c + 8 <= cols) {
       v = *reinterpret_cast<const u32x4_any *>(s);
@@ -22,17 +26,23 @@ static __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t *__
       for (int x = 0; x < 8; ++x)
         if (c + x < cols) v[x / 2] |= (uint32_t)s[x] << (16 * (x % 2));
     }
-    *reinterpret_cast<u32x4 *>(dst + row * pitch + c) = v;
+    *reinterpret_cast<u32x4 *>((first ? pa : pb) + row * pitch + c) = v;
   }
 }
 
 namespace launch_detail {
 
-inline pgemm_status pad_rows(const uint16_t *src, char *dst, int64_t rows, int64_t cols, int64_t pitch,
-                             hipStream_t stream) {
-  if (rows == 0) return PGEMM_OK;
-  hipLaunchKernelGGL(pad_rows_kernel, dim3(row_grid(rows * (pitch / 8))), dim3(256), 0, stream, src,
-                     reinterpret_cast<uint16_t *>(dst), rows, (int)cols, (int)pitch);
+// *x [rows_x][cols] and *w [rows_w][cols] as the products read them: copied into
+// rows that start on 16 bytes.
+inline pgemm_status pad_operands(const uint16_t **x, char *px, int64_t rows_x, const uint16_t **w, char *pw, int64_t rows_w,
+                                 int64_t cols, int64_t pitch, hipStream_t stream) {
+  const uint16_t *a = *x, *b = *w;
+  uint16_t *pa = reinterpret_cast<uint16_t *>(px), *pb = reinterpret_cast<uint16_t *>(pw);
+  *x = pa;
+  *w = pb;
+  if (rows_x + rows_w == 0 || cols == 0) return PGEMM_OK;
+  hipLaunchKernelGGL(pad_rows_kernel, dim3(row_grid((rows_x + rows_w) * (pitch / 8))), dim3(256), 0, stream, a, pa, rows_x,
+                     b, pb, rows_w, (int)cols, (int)pitch);
   return launched();
 }
 

@@ -6,7 +6,8 @@
 
 namespace pgemm {
 
-// dst[row][from .. pitch) = 0
+// dst[row][from .. pitch) = 0: the ends of dy's rows meet W rows that read zero,
+// and must be finite.
 static __global__ void __launch_bounds__(256) zero_tail_kernel(uint16_t *dst, int64_t rows, int from, int pitch) {
   const int n = pitch - from;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * n; i += (int64_t)gridDim.x * 256)
@@ -28,6 +29,9 @@ __global__ void __launch_bounds__(256) gated_slope_kernel(const float *__restric
     const f32x4 up = *reinterpret_cast<const f32x4 *>(saved + i * 8 + 4);
     const uint16_t *s = dh + m * F + c;
     const bool whole = c + 4 <= F;
+    if (c == 0) {  // a row's end meets W rows that read zero, and must be finite
+      for (int64_t x = 2 * (int64_t)F; x < py; ++x) dy[m * py + x] = 0;
+    }
     u32x2 v = {0u, 0u};
     if (whole) {
       v = *reinterpret_cast<const u32x2_any *>(s);
@@ -69,11 +73,7 @@ pgemm_status gated_operands(const GatedCall &c, const GatedPlan &p, const uint16
   *x = c.x;
   *w = c.w;
   if (!p.padded) return PGEMM_OK;
-  pgemm_status st = pad_rows(c.x, c.ws + p.x, c.M, c.D, p.d8, c.stream);
-  if (st == PGEMM_OK) st = pad_rows(c.w, c.ws + p.w, 2 * c.F, c.D, p.d8, c.stream);
-  *x = reinterpret_cast<const uint16_t *>(c.ws + p.x);
-  *w = reinterpret_cast<const uint16_t *>(c.ws + p.w);
-  return st;
+  return pad_operands(x, c.ws + p.x, c.M, w, c.ws + p.w, 2 * c.F, c.D, p.d8, c.stream);
 }
 
 inline FusedProduct projections(const GatedCall &c, const GatedPlan &p, const uint16_t *x, const uint16_t *w) {
@@ -125,11 +125,11 @@ pgemm_status gated_backward(const GatedCall &c) {
     } else {
       st = launch_product<T, Lay::KC, Lay::KC, true, GatedSlopeEpi>(
           projections(c, p, x, w), p.forward, GatedSlopeEpi::Args{c.dh, dy, p.py, c.act}, c.stream, c.dev);
-    }
-    if (st == PGEMM_OK && p.py != F2) {  // the pad meets W rows that read zero, and must be finite
-      hipLaunchKernelGGL(zero_tail_kernel, dim3(row_grid(c.M * (p.py - F2))), dim3(256), 0, c.stream, dy, c.M, (int)F2,
-                         (int)p.py);
-      st = launched();
+      if (st == PGEMM_OK && p.py != F2) {
+        hipLaunchKernelGGL(zero_tail_kernel, dim3(row_grid(c.M * (p.py - F2))), dim3(256), 0, c.stream, dy, c.M, (int)F2,
+                           (int)p.py);
+        st = launched();
+      }
     }
     if (st != PGEMM_OK) return st;
   }

@@ -73,11 +73,7 @@ pgemm_status xent_operands(const XentCall &c, const XentPlan &p, const uint16_t 
   *x = c.x;
   *w = c.w;
   if (!p.padded) return PGEMM_OK;
-  pgemm_status st = pad_rows(c.x, c.ws + p.x, c.M, c.D, p.d8, c.stream);
-  if (st == PGEMM_OK) st = pad_rows(c.w, c.ws + p.w, c.V, c.D, p.d8, c.stream);
-  *x = reinterpret_cast<const uint16_t *>(c.ws + p.x);
-  *w = reinterpret_cast<const uint16_t *>(c.ws + p.w);
-  return st;
+  return pad_operands(x, c.ws + p.x, c.M, w, c.ws + p.w, c.V, c.D, p.d8, c.stream);
 }
 
 template <typename T>
@@ -127,7 +123,7 @@ pgemm_status xent_backward(const XentCall &c) {
     g.N = (int)n;
     g.K = (int)p.d8;
     st = launch_product<T, Lay::KC, Lay::KC, false, SlopeEpi>(
-        g, n == p.piece ? p.logits : plan_tiles(c.M, n, p.d8, false, false),
+        g, p.logits,
         SlopeEpi::Args{dz, p.pz, c.lse_in, c.dloss, c.dstep, c.target, scale, c.ignore, v0, c.V}, c.stream, c.dev);
     if (st != PGEMM_OK) return st;
     // dW rows of this piece = dz^T x
@@ -136,7 +132,7 @@ pgemm_status xent_backward(const XentCall &c) {
     g.M = (int)n;
     g.N = (int)c.D;
     g.K = (int)c.M;
-    st = launch_sum<T, Lay::KR, Lay::KR>(g, n == p.piece ? p.dw : plan_tiles(n, c.D, c.M, false, false),
+    st = launch_sum<T, Lay::KR, Lay::KR>(g, p.dw,
                                          SumEpi::Args{nullptr, 0, 1, 1, {c.dw + v0 * c.D, c.D, unscale}}, c.ws + p.part,
                                          c.stream, c.dev);
     if (st != PGEMM_OK) return st;
@@ -147,7 +143,7 @@ pgemm_status xent_backward(const XentCall &c) {
     g.N = (int)c.D;
     g.K = (int)n;
     st = launch_sum<T, Lay::KC, Lay::KR>(
-        g, n == p.piece ? p.dx : plan_tiles(c.M, c.D, n, false, false),
+        g, shortened(p.dx, n),
         SumEpi::Args{sum, (int)p.ps, v0 == 0, v0 + n == c.V, {c.dx, c.D, unscale}}, c.ws + p.part, c.stream, c.dev);
     if (st != PGEMM_OK) return st;
   }
