@@ -20,7 +20,8 @@
 // Waves: KW work on blocks of K in turn and join their sums in LDS at the end;
 // NW beside each other on different weight rows share their tokens in LDS
 // (worth it once reading x again for every 32 weight rows counts: more than
-// 16 tokens).  MT blocks of 16 tokens; XI loads of four tokens each hold them.
+// 16 tokens).  Two beside each other, and four along K, where four beside each
+// other would leave most CUs without a workgroup.  MT blocks of 16 tokens; XI loads of four tokens each hold them.
 #pragma once
 
 #include "few_rows.hpp"
@@ -50,7 +51,7 @@ struct Q4Geom {
   static constexpr int ROWS = NW * 32;                  // weight rows of a workgroup
   static constexpr int COLS = GATED ? ROWS / 2 : ROWS;  // output columns
   static constexpr int CB = NW == 1 ? 64 : 16;          // blocks of K whose scales are kept
-  static constexpr int XBUFS = NW == 1 ? 1 : 2;
+  static constexpr int XBUFS = NW == 4 ? 2 : 1;
   static constexpr int RING = WAVES * D * 2048;
   static constexpr int XBYTES = KW * XBUFS * XI * 1024;
   static constexpr int XW = XI / NW;  // loads of x a wave does for a block
@@ -250,7 +251,8 @@ __global__ void __launch_bounds__(NW *KW * 64, q4_per_simd(XI, NW)) q4_kernel(Q4
         stage(std::integral_constant<int, 2048 / G::THREADS>{});
       lds_barrier();
       auto round = [&](int i, u32x4(&x)[XW]) __attribute__((always_inline)) {
-        char *xs = xbuf + (NW == 1 ? 0 : (i & 1)) * (XI * 1024);
+        char *xs = xbuf + (G::XBUFS == 1 ? 0 : (i & 1)) * (XI * 1024);
+        if (NW > 1 && G::XBUFS == 1) lds_barrier();  // the last block's tokens are no longer read
         if (mine > 0) {
           store_x(xs, x, block(i));
           load_x(x, block(i + D - 1));
