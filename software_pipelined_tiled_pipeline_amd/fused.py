@@ -39,18 +39,29 @@ def declare(L) -> None:
 @functools.lru_cache(maxsize=1024)
 def workspace_bytes(op: str, M: int, N: int, K: int) -> int:
     """Bytes of workspace of a call: (M, N, K) is (M, F, D) or (M, V, D)."""
-    from . import pgemm
+    _load()
     n = ctypes.c_int64()
     pgemm._check(pgemm.lib().pgemm_fused_workspace(FUSED_OPS[op], M, N, K, ctypes.byref(n)), "pgemm_fused_workspace")
     return n.value
 
 
-def _refuse(name, t, dtype, shape, dev):
+# torch and the products' binding, found by the first call: the package loads
+# without torch, and the binding imports this module
+torch = pgemm = None
+
+
+def _load():
+    global torch, pgemm
+    if pgemm is None:
+        import torch
+        from . import pgemm
+
+
+def _refuse(name, t, dtype, shape):
     """Says what is wrong with one operand; a size of None in `shape` takes any size."""
-    import torch
     if not torch.cuda.is_available():
         raise ValueError("pgemm needs a GPU")
-    here = torch.device("cuda", torch.cuda.current_device() if dev is None else dev)
+    here = torch.device("cuda", torch.cuda.current_device())
     if t.dtype != dtype or not t.is_cuda or t.device != here:
         raise ValueError(f"{name} must be a {dtype} tensor on the current device {here}, not {t.dtype} on {t.device}")
     if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
@@ -59,27 +70,27 @@ def _refuse(name, t, dtype, shape, dev):
     raise ValueError(f"{name} must be contiguous")
 
 
+# The checks below are a large part of what a call of a few microseconds costs:
+# they compare first and look for the reason only where something differs.
+
 def _first(name, t, dtype):
     """Checks a call's first matrix; (rows, columns, current device)."""
-    import torch
-    if not t.is_cuda or t.dim() != 2:
-        _refuse(name, t, dtype, (None, None), None)
-    dev = torch.cuda.current_device()
-    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
-        _refuse(name, t, dtype, (None, None), dev)
+    dev = t.get_device()
+    if dev < 0 or t.dim() != 2 or t.dtype is not dtype or dev != torch._C._cuda_getDevice() or not t.is_contiguous():
+        _refuse(name, t, dtype, (None, None))
     rows, cols = t.shape
     return rows, cols, dev
 
 
 def _want(name, t, dtype, shape, dev):
-    if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
-        _refuse(name, t, dtype, shape, dev)
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _refuse(name, t, dtype, shape)
 
 
 def _rows(name, t, dtype, cols, dev):
     """Checks a matrix of any number of rows; that number."""
-    if t.dim() != 2 or t.shape[1] != cols or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
-        _refuse(name, t, dtype, (None, cols), dev)
+    if t.dim() != 2 or t.shape[1] != cols or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, dtype, (None, cols))
     return t.shape[0]
 
 
@@ -96,20 +107,21 @@ def _act(act):
     return ACTS[act]
 
 
-def _ptr(t):
-    return None if t is None else (t.data_ptr() or None)
-
-
 _entries = {}  # library functions by name
 
 
-def _run(name, dev, args, need=0):
+def _entry(name):
+    f = _entries[name] = getattr(pgemm.lib(), name)
+    return f
+
+
+def _failed(name, status):
+    raise pgemm.PgemmError(status, name)
+
+
+def _run(name, dev, args, need):
     """Calls the library on the current stream, with a workspace of `need` bytes."""
-    import torch
-    from . import pgemm
-    f = _entries.get(name)
-    if f is None:
-        f = _entries[name] = getattr(pgemm.lib(), name)
+    f = _entries.get(name) or _entry(name)
     handle = torch._C._cuda_getCurrentRawStream(dev)
     if need:
         if torch.cuda.is_current_stream_capturing():
@@ -119,25 +131,28 @@ def _run(name, dev, args, need=0):
             own = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
             pgemm._register(handle, own)
             try:
-                pgemm._check(f(*args, handle), name)
+                status = f(*args, handle)
             finally:
                 pgemm._register(handle, pgemm._workspaces.get((dev, handle)))
+            if status != 0:
+                _failed(name, status)
             return
         ws = pgemm._workspaces.get((dev, handle))
         if ws is None or ws.numel() < need:
             pgemm.ensure_workspace(need)
     status = f(*args, handle)
     if status != 0:
-        pgemm._check(status, name)
+        _failed(name, status)
 
 
 def _on_stream(fn):
     """`fn` with an argument `stream`: its outputs and kernels then belong to that stream instead of the current one."""
     @functools.wraps(fn)
     def run(*args, stream=None, **more):
+        if torch is None:
+            _load()
         if stream is None:
             return fn(*args, **more)
-        import torch
         with torch.cuda.stream(stream):
             return fn(*args, **more)
     return run
@@ -162,14 +177,13 @@ def _make(fmt, dtype_name):
         return M, rows // 2, D, dev
 
     def gated(x, w, act="silu", out=None, save=False):
-        import torch
         dtype = getattr(torch, dtype_name)
         M, F, D, dev = block(x, w, dtype)
         code = _act(act)
         h = _out("out", out, dtype, (M, F), dev, x)
         saved = x.new_empty(_saved_shape(M, F), dtype=torch.float32) if save else None
-        _run(GATED, dev, (_ptr(x), _ptr(w), _ptr(h), _ptr(saved), M, F, D, code),
-             workspace_bytes("gated_save" if save else "gated", M, F, D))
+        _run(GATED, dev, (x.data_ptr(), w.data_ptr(), h.data_ptr(), 0 if saved is None else saved.data_ptr(), M, F, D,
+                          code), workspace_bytes("gated_save" if save else "gated", M, F, D))
         return (h, saved) if save else h
 
     gated.__doc__ = (f"{dtype_name} h[M,F] = act(x Wg^T) * (x Wu^T) for x [M,D] and w [2F,D], the gate rows and then the up "
@@ -177,7 +191,6 @@ def _make(fmt, dtype_name):
                      "returns the fp32 projections for the backward call, 8 bytes per value of h.")
 
     def gated_bwd(dh, x, w, saved=None, act="silu", dx=None, dw=None):
-        import torch
         dtype = getattr(torch, dtype_name)
         M, F, D, dev = block(x, w, dtype)
         code = _act(act)
@@ -186,26 +199,25 @@ def _make(fmt, dtype_name):
             _want("saved", saved, torch.float32, _saved_shape(M, F), dev)
         dx = _out("dx", dx, dtype, (M, D), dev, x)
         dw = _out("dw", dw, dtype, (2 * F, D), dev, x)
-        _run(GATED_BWD, dev, (_ptr(dh), _ptr(x), _ptr(w), _ptr(saved), _ptr(dx), _ptr(dw), M, F, D, code),
-             workspace_bytes("gated_bwd", M, F, D))
+        _run(GATED_BWD, dev, (dh.data_ptr(), x.data_ptr(), w.data_ptr(), 0 if saved is None else saved.data_ptr(),
+                              dx.data_ptr(), dw.data_ptr(), M, F, D, code), workspace_bytes("gated_bwd", M, F, D))
         return dx, dw
 
     gated_bwd.__doc__ = (f"(dx[M,D], dw[2F,D]) of {GATED} for dh [M,F].  saved: what the forward call kept "
                          "(faster: two products fewer); None computes the projections again.")
 
-    def head(x, w, target, dtype, i64):
+    def head(x, w, target, dtype):
         M, D, dev = _first("x", x, dtype)
         V = _rows("w", w, dtype, D, dev)
-        _want("target", target, i64, (M,), dev)
+        _want("target", target, torch.int64, (M,), dev)
         return M, V, D, dev
 
     def xent(x, w, target, ignore_index=-100, loss=None, lse=None):
-        import torch
-        M, V, D, dev = head(x, w, target, getattr(torch, dtype_name), torch.int64)
+        M, V, D, dev = head(x, w, target, getattr(torch, dtype_name))
         loss = _out("loss", loss, torch.float32, (M,), dev, x)
         lse = _out("lse", lse, torch.float32, (M,), dev, x)
-        _run(XENT, dev, (_ptr(x), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse), M, V, D, int(ignore_index)),
-             workspace_bytes("xent", M, V, D))
+        _run(XENT, dev, (x.data_ptr(), w.data_ptr(), target.data_ptr(), loss.data_ptr(), lse.data_ptr(), M, V, D,
+                         int(ignore_index)), workspace_bytes("xent", M, V, D))
         return loss, lse
 
     xent.__doc__ = (f"(loss[M], lse[M]) in fp32: softmax cross entropy of the logits x w^T for {dtype_name} x [M,D] and w "
@@ -213,9 +225,8 @@ def _make(fmt, dtype_name):
                     "loss 0; any other target outside the vocabulary makes its loss NaN.")
 
     def xent_bwd(dloss, x, w, target, lse, ignore_index=-100, dx=None, dw=None):
-        import torch
         dtype = getattr(torch, dtype_name)
-        M, V, D, dev = head(x, w, target, dtype, torch.int64)
+        M, V, D, dev = head(x, w, target, dtype)
         _want("lse", lse, torch.float32, (M,), dev)
         if dloss.dtype != torch.float32 or dloss.get_device() != dev:
             raise ValueError(f"dloss must be a torch.float32 tensor on the current device cuda:{dev}")
@@ -227,29 +238,36 @@ def _make(fmt, dtype_name):
             raise ValueError("dloss must be a scalar, or have shape [M] and be contiguous or expanded from a scalar")
         dx = _out("dx", dx, dtype, (M, D), dev, x)
         dw = _out("dw", dw, dtype, (V, D), dev, x)
-        _run(XENT_BWD, dev, (_ptr(dloss), step, _ptr(x), _ptr(w), _ptr(target), _ptr(lse), _ptr(dx), _ptr(dw), M, V, D,
-                             int(ignore_index)), workspace_bytes("xent_bwd", M, V, D))
+        _run(XENT_BWD, dev, (dloss.data_ptr(), step, x.data_ptr(), w.data_ptr(), target.data_ptr(), lse.data_ptr(),
+                             dx.data_ptr(), dw.data_ptr(), M, V, D, int(ignore_index)),
+             workspace_bytes("xent_bwd", M, V, D))
         return dx, dw
 
     xent_bwd.__doc__ = (f"(dx[M,D], dw[V,D]) of {XENT} for dloss, fp32 [M] or a scalar that all rows share, and "
                         "the forward call's lse.")
 
-    def q4_operands(x, q, scale, zero, group, dtype, u8):
+    def q4_operands(x, q, scale, zero, group, dtype):
         M, K, dev = _first("x", x, dtype)
         if group <= 0 or group % 32:
             raise ValueError("group must be a positive multiple of 32")
-        rows, groups = _rows("q", q, u8, -(-K // 32) * 16, dev), -(-K // group)
+        rows, groups = _rows("q", q, torch.uint8, -(-K // 32) * 16, dev), -(-K // group)
         _want("scale", scale, dtype, (rows, groups), dev)
         if zero is not None:
-            _want("zero", zero, u8, (rows, groups), dev)
+            _want("zero", zero, torch.uint8, (rows, groups), dev)
         return M, rows, K, dev
 
     def q4(x, q, scale, zero=None, group=128, out=None):
-        import torch
         dtype = getattr(torch, dtype_name)
-        M, N, K, dev = q4_operands(x, q, scale, zero, group, dtype, torch.uint8)
-        out = _out("out", out, dtype, (M, N), dev, x)
-        _run(Q4, dev, (_ptr(x), _ptr(q), _ptr(scale), _ptr(zero), _ptr(out), M, N, K, int(group)))
+        M, N, K, dev = q4_operands(x, q, scale, zero, group, dtype)
+        if out is None:
+            out = x.new_empty((M, N))
+        else:
+            _want("out", out, dtype, (M, N), dev)
+        f = _entries.get(Q4) or _entry(Q4)
+        status = f(x.data_ptr(), q.data_ptr(), scale.data_ptr(), 0 if zero is None else zero.data_ptr(), out.data_ptr(),
+                   M, N, K, int(group), torch._C._cuda_getCurrentRawStream(dev))
+        if status != 0:
+            _failed(Q4, status)
         return out
 
     q4.__doc__ = (f"{dtype_name} out[M,N] = x[M,K] w^T for few rows and 4-bit weights w[n,k] = scale[n,k/group] (q[n,k] - "
@@ -257,15 +275,21 @@ def _make(fmt, dtype_name):
                   f"(library call {Q4}).")
 
     def q4_gated(x, q, scale, zero=None, group=128, act="silu", out=None):
-        import torch
         dtype = getattr(torch, dtype_name)
-        M, rows, K, dev = q4_operands(x, q, scale, zero, group, dtype, torch.uint8)
+        M, rows, K, dev = q4_operands(x, q, scale, zero, group, dtype)
         code = _act(act)
         if rows % 2:
             raise ValueError("q must have 2 F rows, the gate rows and then the up rows")
         F = rows // 2
-        out = _out("out", out, dtype, (M, F), dev, x)
-        _run(Q4_GATED, dev, (_ptr(x), _ptr(q), _ptr(scale), _ptr(zero), _ptr(out), M, F, K, int(group), code))
+        if out is None:
+            out = x.new_empty((M, F))
+        else:
+            _want("out", out, dtype, (M, F), dev)
+        f = _entries.get(Q4_GATED) or _entry(Q4_GATED)
+        status = f(x.data_ptr(), q.data_ptr(), scale.data_ptr(), 0 if zero is None else zero.data_ptr(), out.data_ptr(),
+                   M, F, K, int(group), code, torch._C._cuda_getCurrentRawStream(dev))
+        if status != 0:
+            _failed(Q4_GATED, status)
         return out
 
     q4_gated.__doc__ = (f"{dtype_name} h[M,F] = act(x Wg^T) * (x Wu^T) for few rows and 4-bit weights of 2F rows, the gate rows "
@@ -284,7 +308,7 @@ FUNCTIONS = {**_make("f16", "float16"), **_make("bf16", "bfloat16")}
 
 def pack_q4(values):
     """The packed rows [N, 16 ceil(K/32)] of 4-bit weights given as a uint8 tensor [N, K] of values 0..15, on any device."""
-    import torch
+    _load()
     if values.dtype != torch.uint8 or values.dim() != 2:
         raise ValueError("values must be a 2-D uint8 tensor of weights 0..15")
     if values.numel() and int(values.max()) > 15:
