@@ -6,11 +6,15 @@
 
 namespace pgemm {
 
-// (v & mask) | bits in one instruction
-__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
-  uint32_t r;
-  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(v), "s"(mask), "v"(bits));
-  return r;
+// A constant the compiler knows nothing of, in a scalar or a vector register:
+// (v & mask) | bits with one of each is one instruction, with two literals two.
+__device__ __forceinline__ uint32_t scalar_constant(uint32_t v) {
+  asm("" : "+s"(v));
+  return v;
+}
+__device__ __forceinline__ uint32_t vector_constant(uint32_t v) {
+  asm("" : "+v"(v));
+  return v;
 }
 
 // MFMA fragments of eight values, and how eight 4-bit weights (a dword, the
@@ -40,14 +44,16 @@ struct Frag8<_Float16> {
       high = f16x2{h, h};
     }
   };
-  __device__ __forceinline__ static u32x4 weights(uint32_t v, const Zero &z) {
-    constexpr uint32_t one = 0x64006400u;
+  struct Bits {
+    uint32_t low = scalar_constant(0x000F000Fu), high = scalar_constant(0x00F000F0u), one = vector_constant(0x64006400u);
+  };
+  __device__ __forceinline__ static u32x4 weights(uint32_t v, const Zero &z, const Bits &k) {
     const f16x2 part = {(_Float16)0.0625f, (_Float16)0.0625f};
     const uint32_t u = v >> 8;
-    const f16x2 a = __builtin_bit_cast(f16x2, and_or(v, 0x000F000Fu, one)) + z.low;
-    const f16x2 b = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, and_or(v, 0x00F000F0u, one)), part, z.high);
-    const f16x2 c = __builtin_bit_cast(f16x2, and_or(u, 0x000F000Fu, one)) + z.low;
-    const f16x2 d = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, and_or(u, 0x00F000F0u, one)), part, z.high);
+    const f16x2 a = __builtin_bit_cast(f16x2, (v & k.low) | k.one) + z.low;
+    const f16x2 b = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (v & k.high) | k.one), part, z.high);
+    const f16x2 c = __builtin_bit_cast(f16x2, (u & k.low) | k.one) + z.low;
+    const f16x2 d = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (u & k.high) | k.one), part, z.high);
     return u32x4{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
                  __builtin_bit_cast(uint32_t, d)};
   }
@@ -67,9 +73,12 @@ struct Frag8<__bf16> {
     float off;
     __device__ __forceinline__ void set(uint32_t packed) { off = 16.0f + (float)(packed & 0xffu); }
   };
-  __device__ __forceinline__ static u32x4 weights(uint32_t v, const Zero &) {
-    constexpr uint32_t m = 0x00780078u, one = 0x41804180u;
-    return u32x4{and_or(v << 3, m, one), and_or(v >> 1, m, one), and_or(v >> 5, m, one), and_or(v >> 9, m, one)};
+  struct Bits {
+    uint32_t mask = scalar_constant(0x00780078u), one = vector_constant(0x41804180u);
+  };
+  __device__ __forceinline__ static u32x4 weights(uint32_t v, const Zero &, const Bits &k) {
+    return u32x4{((v << 3) & k.mask) | k.one, ((v >> 1) & k.mask) | k.one, ((v >> 5) & k.mask) | k.one,
+                 ((v >> 9) & k.mask) | k.one};
   }
 };
 

@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(NW *KW * 64, q4_per_simd(XI, NW)) q4_kernel(Q4
 #pragma unroll
     for (int b = 0; b < NT; ++b) tot[m][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+  const typename F::Bits bits;
   const uint32_t wread = c * 64 + q * 4;
   const int xr = XI < 4 ? c & (4 * XI - 1) : c;
   const uint32_t *myscales = scales + (wn * 32 + c) * a.sp;
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(NW *KW * 64, q4_per_simd(XI, NW)) q4_kernel(Q4
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
           const uint32_t v = *reinterpret_cast<const uint32_t *>(slot + b * 1024 + wread + ((s ^ (c >> 2)) * 16));
-          const u32x4 f = F::weights(v, z[b]);
+          const u32x4 f = F::weights(v, z[b], bits);
 #pragma unroll
           for (int m = 0; m < MT; ++m) acc[m][b] = F::mma(xf[m], f, acc[m][b]);
         }

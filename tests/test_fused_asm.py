@@ -22,6 +22,7 @@ from test_mfma_hazards import device_asm, hipcc_available  # noqa: E402
 from software_pipelined_tiled_pipeline_amd import build  # noqa: E402
 
 UNITS = [u for u in build.UNITS if u.startswith(("fused_gated", "fused_xent"))]
+ALL = UNITS + [u for u in build.UNITS if u.startswith("fused_q4")]
 SGPR_WAIT = 5  # wait states from a vector instruction's scalar result to a load that reads it
 
 
@@ -32,8 +33,18 @@ def unit_asm():
     with tempfile.TemporaryDirectory() as tmp:
         def one(u):
             return u, device_asm(os.path.join(build.CSRC, u), os.path.join(tmp, u + ".s"))
-        with ThreadPoolExecutor(len(UNITS)) as pool:
-            return dict(pool.map(one, UNITS))
+        with ThreadPoolExecutor(len(ALL)) as pool:
+            return dict(pool.map(one, ALL))
+
+
+@pytest.mark.parametrize("unit", ALL)
+def test_operands_of_mfmas(unit_asm, unit):
+    # the products with few rows leave their MFMAs to the compiler, which does
+    # not know what an inline-assembly instruction before one writes
+    hazards, mfmas = mfma_hazards.check_asm(unit_asm[unit])
+    assert mfmas > 500
+    hazards = [h for h in hazards if h.kind in ("VALU_TO_MFMA", "LOAD_TO_MFMA")]
+    assert not hazards, "\n".join(f"{h.kind} line {h.line}: {h.text} ({h.detail})" for h in hazards[:20])
 
 
 @pytest.mark.parametrize("unit", UNITS)
