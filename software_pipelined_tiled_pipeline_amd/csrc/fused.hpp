@@ -33,7 +33,7 @@ struct Carver {
 //
 // The cut that takes least by these times, in microseconds, which the kernels
 // were measured to need for the tiles of one CU (K tiles of 64):
-//   large, one to a CU:         1.6 a K tile and 7 to fill and store
+//   large, one to a CU:         1.5 a K tile and 12 to fill and store
 //   small, deep, one to a CU:   0.45 and 6
 //   small, two to a CU:         1.0 and 9 (0.72 and 7 for one left over)
 // so a large tile has the work of four small ones for less than the time of
@@ -66,7 +66,7 @@ inline Tiling plan_tiles(int64_t M, int64_t N, int64_t K, bool dual, bool can_sp
       if (!large && blocks * 512 >= kMaxWorkItems) continue;
       double us;
       if (large) {
-        us = (double)per(blocks, 256) * (1.6 * steps + 7.0);
+        us = (double)per(blocks, 256) * (1.5 * steps + 12.0);
       } else {
         const int64_t rest = blocks % 512;
         us = (double)(blocks / 512 + (rest > 256)) * (steps + 9.0) + (rest > 0 && rest <= 256 ? 0.72 * steps + 7.0 : 0.0);

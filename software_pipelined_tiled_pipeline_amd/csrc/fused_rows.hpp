@@ -6,27 +6,28 @@
 namespace pgemm {
 
 // dst[rows][pitch] = src[rows][cols], zeros from cols on (pitch a multiple of
-// 8), for two matrices of the same width.
+// 8), for two matrices of the same width; a wave a row.
 static __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t *__restrict__ a, uint16_t *__restrict__ pa,
                                                        int64_t rows_a, const uint16_t *__restrict__ b,
                                                        uint16_t *__restrict__ pb, int64_t rows_b, int cols, int pitch) {
-  const int per = pitch / 8;
-  const int64_t total = (rows_a + rows_b) * per;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t at = i / per;
+  const int lane = threadIdx.x & 63;
+  const int64_t step = (int64_t)gridDim.x * 4;
+  for (int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); at < rows_a + rows_b; at += step) {
     const bool first = at < rows_a;
     const int64_t row = first ? at : at - rows_a;
-    const int c = (int)(i % per) * 8;
-    const uint16_t *s = (first ? a : b) + row * cols + c;
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (c + 8 <= cols) {
-      v = *reinterpret_cast<const u32x4_any *>(s);
-    } else {
+    const uint16_t *src = (first ? a : b) + row * cols;
+    uint16_t *dst = (first ? pa : pb) + row * pitch;
+    for (int c = lane * 8; c < pitch; c += 512) {
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (c + 8 <= cols) {
+        v = *reinterpret_cast<const u32x4_any *>(src + c);
+      } else {
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (c + x < cols) v[x / 2] |= (uint32_t)s[x] << (16 * (x % 2));
+        for (int x = 0; x < 8; ++x)
+          if (c + x < cols) v[x / 2] |= (uint32_t)src[c + x] << (16 * (x % 2));
+      }
+      *reinterpret_cast<u32x4 *>(dst + c) = v;
     }
-    *reinterpret_cast<u32x4 *>((first ? pa : pb) + row * pitch + c) = v;
   }
 }
 
@@ -41,7 +42,7 @@ inline pgemm_status pad_operands(const uint16_t **x, char *px, int64_t rows_x, c
   *x = pa;
   *w = pb;
   if (rows_x + rows_w == 0 || cols == 0) return PGEMM_OK;
-  hipLaunchKernelGGL(pad_rows_kernel, dim3(row_grid((rows_x + rows_w) * (pitch / 8))), dim3(256), 0, stream, a, pa, rows_x,
+  hipLaunchKernelGGL(pad_rows_kernel, dim3(row_grid((rows_x + rows_w) * 64)), dim3(256), 0, stream, a, pa, rows_x,
                      b, pb, rows_w, (int)cols, (int)pitch);
   return launched();
 }

@@ -5,8 +5,8 @@
 
 namespace pgemm {
 
-// Joins the tiles' softmax statistics of 64 rows per workgroup: each of its
-// 16 waves runs through every 16th part, then the waves' are joined.
+// Joins the tiles' softmax statistics of 16 rows per workgroup: 64 threads a
+// row run through every 64th part, then theirs are joined.
 //   lse = log sum_v e^(z_v), loss = lse - z_target (0 for an ignored row, NaN
 // for a target outside the vocabulary).
 template <typename T>
@@ -14,9 +14,9 @@ __global__ void __launch_bounds__(1024) lse_join_kernel(const float2 *__restrict
                                                         const int64_t *__restrict__ target, float *__restrict__ loss,
                                                         float *__restrict__ lse, int64_t M, int64_t V, int parts,
                                                         int64_t ignore) {
-  __shared__ float tops[16][64], sums[16][64];
-  const int r = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t row = (int64_t)blockIdx.x * 64 + r;
+  __shared__ float tops[16][16], sums[16][16];
+  const int r = threadIdx.x & 15, w = threadIdx.x >> 6;
+  const int64_t row = (int64_t)blockIdx.x * 16 + r;
   float top = -INFINITY, sum = 0.0f;
   auto join = [&](float t, float s) {
     const float m = fmaxf(top, t);
@@ -26,15 +26,22 @@ __global__ void __launch_bounds__(1024) lse_join_kernel(const float2 *__restrict
   };
   if (row < M) {
 #pragma unroll 4
-    for (int p = w; p < parts; p += 16) {
+    for (int p = threadIdx.x >> 4; p < parts; p += 64) {
       const float2 v = part[(int64_t)p * M + row];
       join(v.x, v.y);
     }
   }
-  tops[w][r] = top;
-  sums[w][r] = sum;
+#pragma unroll
+  for (int d = 16; d <= 32; d *= 2) {
+    const float t = __shfl_xor(top, d), s = __shfl_xor(sum, d);
+    join(t, s);
+  }
+  if ((threadIdx.x & 63) < 16) {
+    tops[w][r] = top;
+    sums[w][r] = sum;
+  }
   __syncthreads();
-  if (w == 0 && row < M) {
+  if (threadIdx.x < 16 && row < M) {
 #pragma unroll
     for (int p = 1; p < 16; ++p) join(tops[p][r], sums[p][r]);
     const float l = top + logf(sum);
@@ -93,7 +100,7 @@ pgemm_status xent_forward(const XentCall &c) {
   st = launch_product<T, Lay::KC, Lay::KC, false, LseEpi>(g, p.logits, LseEpi::Args{part, at, c.target}, c.stream,
                                                           c.dev);
   if (st != PGEMM_OK) return st;
-  hipLaunchKernelGGL(lse_join_kernel<T>, dim3((unsigned)per(c.M, 64)), dim3(1024), 0, c.stream, part, at, c.target, c.loss,
+  hipLaunchKernelGGL(lse_join_kernel<T>, dim3((unsigned)per(c.M, 16)), dim3(1024), 0, c.stream, part, at, c.target, c.loss,
                      c.lse, c.M, c.V, (int)p.parts, c.ignore);
   return launched();
 }
