@@ -5,6 +5,9 @@ checks, planning, the int32 kernel), four units of NT kernel instances (f16
 and bf16, each with the direct-to-LDS and the register-staged loader), the C
 ABI of the fused operators, and their instances by operator and type.  They
 are compiled in parallel and linked into one shared library.
+
+Beside it, _binding.so: the fused operators' short way through Python, host C++
+against torch's headers.
 """
 from __future__ import annotations
 
@@ -21,6 +24,7 @@ UNITS = ["pgemm_api.hip", "inst_f16_direct.hip", "inst_f16_staged.hip", "inst_bf
          "inst_bf16_staged.hip", "fused_api.hip", "fused_gated_f16.hip", "fused_gated_bf16.hip", "fused_xent_f16.hip",
          "fused_xent_bf16.hip", "fused_q4_f16.hip", "fused_q4_bf16.hip"]
 LIB = os.path.join(HERE, "libpgemm.so")
+BINDING = os.path.join(HERE, "_binding.so")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
@@ -47,6 +51,24 @@ def _run(cmd):
     return msgs
 
 
+def build_binding(out: str = BINDING) -> str:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-attributes",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           "-I", sysconfig.get_paths()["include"]]
+    for path in cpp_extension.include_paths():
+        cmd += ["-isystem", path]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", out + ".tmp"]
+    for path in cpp_extension.library_paths():
+        cmd += ["-L", path]
+    _run(cmd + ["-ltorch_python", "-ltorch_cpu", "-lc10"])
+    os.replace(out + ".tmp", out)
+    return out
+
+
 def build(verbose: bool = False, lib: str = LIB, extra_flags=(), jobs: int = 0) -> str:
     """Compiles every unit (in parallel) and links libpgemm.so."""
     jobs = jobs or min(len(UNITS), os.cpu_count() or 1)
@@ -57,7 +79,10 @@ def build(verbose: bool = False, lib: str = LIB, extra_flags=(), jobs: int = 0) 
             return _run([hipcc(), *HIPCC_FLAGS, *extra_flags, "-c", os.path.join(CSRC, UNITS[i]), "-o", objs[i]])
 
         with ThreadPoolExecutor(jobs) as pool:
+            binding = pool.submit(build_binding) if lib == LIB else None
             msgs = [m for ms in pool.map(compile_one, range(len(UNITS))) for m in ms]
+            if binding:
+                binding.result()
         out = lib + ".tmp"
         msgs += _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", out])
         if verbose and msgs:

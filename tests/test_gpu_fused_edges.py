@@ -92,6 +92,33 @@ def test_workspace_that_is_missing_or_too_small(pg):
     assert L.pgemm_set_workspace(h, None, 0) == 0
 
 
+@pytest.mark.parametrize("fmt", FMT)
+def test_outputs_of_the_callers_own(pg, fmt):
+    # the same values, in the tensors that were given
+    def same(name, args, kw, **outs):
+        got = call(pg, fmt, name, *args, **kw, **outs)
+        want = call(pg, fmt, name, *args, **kw)
+        got, want = (t if isinstance(t, tuple) else (t,) for t in (got, want))
+        for g, w, o in zip(got, want, outs.values()):
+            assert g is o and torch.equal(g, w)
+
+    def like(*shape, dtype=TYPES[fmt]):
+        return torch.full(shape, math.nan, dtype=dtype, device="cuda")
+    M, F, D, V = 90, 40, 72, 333
+    x, w, dh = block(23, fmt, M, F, D)
+    same("gated", (x, w), dict(act="gelu"), out=like(M, F))
+    _, saved = call(pg, fmt, "gated", x, w, save=True)
+    same("gated_bwd", (dh, x, w), dict(saved=saved), dx=like(M, D), dw=like(2 * F, D))
+    hx, hw, target, dloss = head(24, fmt, M, V, D)
+    same("xent", (hx, hw, target), {}, loss=like(M, dtype=torch.float32), lse=like(M, dtype=torch.float32))
+    _, lse = call(pg, fmt, "xent", hx, hw, target)
+    same("xent_bwd", (dloss, hx, hw, target, lse), {}, dx=like(M, D), dw=like(V, D))
+    tok, values, scale, zero = q4_case(25, fmt, 3, 64, 200, 64, True)
+    packed = pg.pack_q4(values)
+    same("q4", (tok, packed, scale, zero), dict(group=64), out=like(3, 64))
+    same("q4_gated", (tok, packed, scale, zero), dict(group=64, act="gelu"), out=like(3, 32))
+
+
 # ------------------------------------------------------------ empty and masked
 
 @pytest.mark.parametrize("fmt", FMT)
