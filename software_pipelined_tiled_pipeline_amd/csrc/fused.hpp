@@ -42,41 +42,67 @@ struct Carver {
 // back (4 MB a microsecond).  Examples: 2048 x 2048 x 4096 takes 39 us in 256
 // small deep tiles, 52 with two slots; 8192 x 2048 x 2048 takes 58 in 256 large
 // ones and 80 in 1024 small ones.
+//
+// Large tiles that do not come out at whole rounds of 256 may leave the rest to
+// small ones in a launch of its own (`cut_m` rows or `cut_n` columns by large
+// tiles): 784 tiles take three rounds and a quarter's time instead of four.
 struct Tiling {
   bool large, deep;
   int split;
-  int64_t k_chunk;  // a multiple of 64 when split
+  int64_t k_chunk;       // a multiple of 64 when split
+  int64_t cut_m, cut_n;  // 0: one launch
 };
 
 constexpr int kMaxPieces = 16;
 constexpr int64_t kMaxWorkItems = (int64_t)1 << 32;  // of a dispatch
 
-inline Tiling plan_tiles(int64_t M, int64_t N, int64_t K, bool dual, bool can_split) {
-  Tiling best{false, false, 1, K};
+inline double small_tiles_us(int64_t blocks, double steps) {
+  if (blocks <= 256) return 0.45 * steps + 6.0;
+  const int64_t rest = blocks % 512;
+  return (double)(blocks / 512 + (rest > 256)) * (steps + 9.0) + (rest > 0 && rest <= 256 ? 0.72 * steps + 7.0 : 0.0);
+}
+inline double large_tiles_us(int64_t blocks, double steps) { return (double)per(blocks, 256) * (1.5 * steps + 12.0); }
+
+// How a product may be cut: in pieces of K, and by rows (a kernel whose results
+// depend on the width of a tile needs the same one in all rows).
+struct Cuts {
+  bool k, m;
+};
+
+inline Tiling plan_tiles(int64_t M, int64_t N, int64_t K, bool dual, Cuts may) {
+  Tiling best{false, false, 1, K, 0, 0};
   double least = -1.0;
+  auto take = [&](double us, const Tiling &t) {
+    if (least >= 0.0 && us >= least) return;
+    least = us;
+    best = t;
+  };
   for (int large = 0; large < 2; ++large) {
     const int64_t t = large ? 256 : 128;
     const int64_t tiles = per(M, t) * per(N, dual ? t / 2 : t);
-    for (int want = 1; want <= (can_split ? kMaxPieces : 1); ++want) {
+    for (int want = 1; want <= (may.k ? kMaxPieces : 1); ++want) {
       const int64_t chunk = want == 1 ? K : up_to(per(K, want), 64);
       const int split = chunk > 0 ? (int)per(K, chunk) : 1;
       if (split != want || (want > 1 && chunk < 256)) continue;
       const double steps = (double)per(chunk, 64);
       const int64_t blocks = tiles * split;
       if (!large && blocks * 512 >= kMaxWorkItems) continue;
-      double us;
-      if (large) {
-        us = (double)per(blocks, 256) * (1.5 * steps + 12.0);
-      } else {
-        const int64_t rest = blocks % 512;
-        us = (double)(blocks / 512 + (rest > 256)) * (steps + 9.0) + (rest > 0 && rest <= 256 ? 0.72 * steps + 7.0 : 0.0);
-        if (blocks <= 256) us = 0.45 * steps + 6.0;
-      }
+      double us = large ? large_tiles_us(blocks, steps) : small_tiles_us(blocks, steps);
       if (split > 1) us += 4.0 + (double)M * (double)N * (8.0 * split + 2.0) / 4e6;
-      if (least < 0.0 || us < least) {
-        least = us;
-        best = Tiling{large != 0, !large && blocks <= 256, split, chunk};
-      }
+      take(us, Tiling{large != 0, !large && blocks <= 256, split, chunk, 0, 0});
+    }
+  }
+  const double steps = (double)per(K, 64);
+  const int64_t tm = per(M, 256), bn = dual ? 128 : 256, tn = per(N, bn), rounds = tm * tn / 256;
+  if (rounds > 0) {
+    const int64_t n = rounds * 256 / tm, m = may.m ? rounds * 256 / tn : 0;
+    if (n > 0 && n < tn) {
+      const int64_t rest = per(M, 128) * per(N - n * bn, bn / 2);
+      take(large_tiles_us(tm * n, steps) + 3.0 + small_tiles_us(rest, steps), Tiling{true, rest <= 256, 1, K, 0, n * bn});
+    }
+    if (m > 0 && m < tm) {
+      const int64_t rest = per(M - m * 256, 128) * per(N, bn / 2);
+      take(large_tiles_us(m * tn, steps) + 3.0 + small_tiles_us(rest, steps), Tiling{true, rest <= 256, 1, K, m * 256, 0});
     }
   }
   return best;
@@ -89,6 +115,7 @@ inline Tiling shortened(Tiling t, int64_t K) {
     if (t.split < 1) t.split = 1;
   }
   if (t.split == 1) t.k_chunk = K;
+  t.cut_m = t.cut_n = 0;
   return t;
 }
 
@@ -122,11 +149,11 @@ inline GatedPlan plan_gated(int64_t M, int64_t F, int64_t D, bool backward, bool
     p.x = c.take(M * p.d8 * 2);
     p.w = c.take(2 * F * p.d8 * 2);
   }
-  p.forward = plan_tiles(M, F, p.d8, true, false);
+  p.forward = plan_tiles(M, F, p.d8, true, Cuts{false, true});
   if (backward) {
     p.dy = c.take(M * p.py * 2);
-    p.dx = plan_tiles(M, D, 2 * F, false, true);
-    p.dw = plan_tiles(2 * F, D, M, false, true);
+    p.dx = plan_tiles(M, D, 2 * F, false, Cuts{true, true});
+    p.dw = plan_tiles(2 * F, D, M, false, Cuts{true, true});
     const int64_t a = piece_bytes(p.dx, M, D), b = piece_bytes(p.dw, 2 * F, D);
     p.part = c.take(a > b ? a : b);
   }
@@ -160,9 +187,10 @@ inline XentPlan plan_xent(int64_t M, int64_t V, int64_t D, bool backward) {
     p.w = c.take(V * p.d8 * 2);
   }
   if (!backward) {
-    p.logits = plan_tiles(M, V, p.d8, false, false);
+    p.logits = plan_tiles(M, V, p.d8, false, Cuts{false, false});
     // wave columns: 128 on the large tile, 32 on the small one
-    p.parts = p.logits.large ? per(V, 256) * 2 : per(V, 128) * 4;
+    const int64_t wide = !p.logits.large ? 0 : p.logits.cut_n ? p.logits.cut_n : V;
+    p.parts = per(wide, 256) * 2 + (wide < V ? per(V - wide, 128) * 4 : 0);
     p.part = c.take(p.parts * M * 8);
     p.at = c.take(M * 4);
   } else {
@@ -175,9 +203,9 @@ inline XentPlan plan_xent(int64_t M, int64_t V, int64_t D, bool backward) {
       p.piece = V;
     p.pz = up_to(p.piece, 8);
     p.ps = up_to(D, 4);
-    p.logits = plan_tiles(M, p.piece, p.d8, false, false);
-    p.dx = plan_tiles(M, D, p.piece, false, true);
-    p.dw = plan_tiles(p.piece, D, M, false, true);
+    p.logits = plan_tiles(M, p.piece, p.d8, false, Cuts{false, true});
+    p.dx = plan_tiles(M, D, p.piece, false, Cuts{true, true});
+    p.dw = plan_tiles(p.piece, D, M, false, Cuts{true, true});
     const int64_t a = piece_bytes(p.dx, M, D), b = piece_bytes(p.dw, p.piece, D);
     p.part = c.take(a > b ? a : b);
     p.dz = c.take(M * p.pz * 2);

@@ -53,23 +53,35 @@ __device__ __forceinline__ float widen(uint16_t v) {
 
 // Copies columns [c0, c0 + BN) of a staged tile to out[m0..][n0..], row pitch
 // `po`: whole 16-byte pieces wherever they start (an odd pitch leaves them
-// at even addresses), single elements at the right edge.
+// at even addresses), single elements at the right edge.  A thread keeps its
+// columns and takes eight rows at a time, so that their LDS reads overlap.
 template <int BM, int BN, int THREADS>
 __device__ __forceinline__ void store_tile(const char *st, int pitch, int c0, uint16_t *out, int64_t po, int M, int N,
                                            int m0, int n0, int tid) {
-  constexpr int CH = BN / 8;
-  for (int idx = tid; idx < BM * CH; idx += THREADS) {
-    const int row = idx / CH, c = idx % CH;
-    const int gm = m0 + row, gn = n0 + 8 * c;
-    if (gm >= M || gn >= N) continue;
-    const u32x4 v = *reinterpret_cast<const u32x4 *>(st + row * pitch + (c0 + 8 * c) * 2);
-    uint16_t *dst = out + (int64_t)gm * po + gn;
-    if (gn + 8 <= N) {
-      *reinterpret_cast<u32x4_any *>(dst) = v;
-    } else {
+  constexpr int CH = BN / 8, ROWS = THREADS / CH, PASSES = BM / ROWS;
+  constexpr int U = PASSES < 8 ? PASSES : 8;
+  static_assert(THREADS % CH == 0 && BM % ROWS == 0 && PASSES % U == 0, "whole passes");
+  const int c = tid % CH, r0 = tid / CH, gn = n0 + 8 * c;
+  if (gn >= N) return;
+  const char *from = st + r0 * pitch + (c0 + 8 * c) * 2;
+  uint16_t *to = out + (int64_t)(m0 + r0) * po + gn;
+  const int rows = M - m0 - r0;  // inside the matrix, from this thread's first
+  for (int p = 0; p < PASSES; p += U) {
+    u32x4 v[U];
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (gn + x < N) dst[x] = (uint16_t)(v[x / 2] >> (16 * (x % 2)));
+    for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const u32x4 *>(from + (p + u) * ROWS * pitch);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int row = (p + u) * ROWS;
+      if (row >= rows) continue;
+      uint16_t *dst = to + row * po;
+      if (gn + 8 <= N) {
+        *reinterpret_cast<u32x4_any *>(dst) = v[u];
+      } else {
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (gn + x < N) dst[x] = (uint16_t)(v[u][x / 2] >> (16 * (x % 2)));
+      }
     }
   }
 }
@@ -291,7 +303,7 @@ struct RowLogits {
 // what few rows need, the vocabulary's end and the targets, is branched around.
 struct LseEpi {
   struct Args {
-    float2 *part;  // [tiles_n * WGN][M]
+    float2 *part;  // [tiles_n * WGN][M], of this launch's columns
     float *at;     // [M] the target's logit
     const int64_t *target;
   };
@@ -302,7 +314,7 @@ struct LseEpi {
       const int r = lane & 15, q = lane >> 4;
       const int c0 = n0 + wn * G::WN + 4 * q;
       const int row0 = m0 + wm * G::WM + r;
-      float2 *part = e.part + (int64_t)((n0 / G::BN) * G::WGN + wn) * g.M;
+      float2 *part = e.part + (int64_t)((n0 - g.n_base) / G::BN * G::WGN + wn) * g.M;
       int64_t target[W::TM];
 #pragma unroll
       for (int i = 0; i < W::TM; ++i) target[i] = e.target[row0 + 16 * i < g.M ? row0 + 16 * i : g.M - 1];

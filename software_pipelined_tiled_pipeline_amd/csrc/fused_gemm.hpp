@@ -48,6 +48,7 @@ struct FusedProduct {
   FusedOperand a, b;
   int M, N, K;  // N counts output columns (of one matrix when DUAL)
   int tiles_m, tiles_n, group_m;
+  int m_base, n_base;  // of the first tile
   int k_chunk;  // K of a piece (a multiple of 64), or K
   int piece;    // set in the kernel: which piece this workgroup does
 };
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(G::THREADS, G::OCC) fused_kernel(FusedProduct 
   int bm, bn, split;
   block_work(blockIdx.x, gridDim.x, g.tiles_m, g.tiles_n, g.group_m, &bm, &bn, &split);
   constexpr int ON = DUAL ? G::BN / 2 : G::BN;  // output columns of a tile
-  const int m0 = bm * G::BM, n0 = bn * ON;
+  const int m0 = g.m_base + bm * G::BM, n0 = g.n_base + bn * ON;
   const int wm = wave / G::WGN, wn = wave % G::WGN;
   g.piece = split;
   const int64_t k_end = ((int64_t)split + 1) * g.k_chunk;

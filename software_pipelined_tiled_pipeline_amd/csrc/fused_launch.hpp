@@ -47,28 +47,50 @@ inline unsigned row_grid(int64_t items) {
   return (unsigned)(b < 1 ? 1 : b > 16384 ? 16384 : b);
 }
 
+// Tiles of rows [g.m_base, m_end) and columns [g.n_base, n_end).
 template <typename T, class G, Lay LA, Lay LB, bool DUAL, class Epi>
-pgemm_status launch_tiles(FusedProduct g, const Tiling &t, const typename Epi::Args &e, hipStream_t stream, int dev) {
+pgemm_status launch_tiles(FusedProduct g, int64_t m_end, int64_t n_end, int split, int64_t k_chunk,
+                          const typename Epi::Args &e, hipStream_t stream, int dev) {
   static std::atomic<uint64_t> lds_set{0};
   auto kern = fused_kernel<T, G, LA, LB, DUAL, Epi>;
   pgemm_status st = allow_lds(kern, G::LDS_BYTES, dev, lds_set);
   if (st != PGEMM_OK) return st;
-  g.tiles_m = cdiv_i(g.M, G::BM);
-  g.tiles_n = cdiv_i(g.N, DUAL ? G::BN / 2 : G::BN);
+  g.tiles_m = cdiv_i((int)(m_end - g.m_base), G::BM);
+  g.tiles_n = cdiv_i((int)(n_end - g.n_base), DUAL ? G::BN / 2 : G::BN);
   g.group_m = kGroupM;
-  g.k_chunk = (int)t.k_chunk;
-  hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n * t.split)), dim3(G::THREADS), G::LDS_BYTES,
+  g.k_chunk = (int)k_chunk;
+  hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n * split)), dim3(G::THREADS), G::LDS_BYTES,
                      stream, g, e);
   return launched();
 }
 
 template <typename T, Lay LA, Lay LB, bool DUAL, class Epi>
-pgemm_status launch_product(const FusedProduct &g, const Tiling &t, const typename Epi::Args &e, hipStream_t stream,
-                            int dev) {
+pgemm_status launch_small(const FusedProduct &g, const Tiling &t, const typename Epi::Args &e, hipStream_t stream, int dev) {
+  if (t.deep) return launch_tiles<T, SwapGeomSmall<4>, LA, LB, DUAL, Epi>(g, g.M, g.N, t.split, t.k_chunk, e, stream, dev);
+  return launch_tiles<T, SwapGeomSmall<2>, LA, LB, DUAL, Epi>(g, g.M, g.N, t.split, t.k_chunk, e, stream, dev);
+}
+
+// What an epilogue needs of a cut product's second launch: statistics go after
+// those of the first one's tiles.
+template <class Args>
+Args second_launch(const Args &e, const FusedProduct &, const Tiling &) {
+  return e;
+}
+inline LseEpi::Args second_launch(LseEpi::Args e, const FusedProduct &g, const Tiling &t) {
+  e.part += t.cut_n / 256 * 2 * g.M;
+  return e;
+}
+
+template <typename T, Lay LA, Lay LB, bool DUAL, class Epi>
+pgemm_status launch_product(FusedProduct g, const Tiling &t, const typename Epi::Args &e, hipStream_t stream, int dev) {
   if (g.M == 0 || g.N == 0) return PGEMM_OK;
-  if (t.large) return launch_tiles<T, SwapGeom<2>, LA, LB, DUAL, Epi>(g, t, e, stream, dev);
-  if (t.deep) return launch_tiles<T, SwapGeomSmall<4>, LA, LB, DUAL, Epi>(g, t, e, stream, dev);
-  return launch_tiles<T, SwapGeomSmall<2>, LA, LB, DUAL, Epi>(g, t, e, stream, dev);
+  if (!t.large) return launch_small<T, LA, LB, DUAL, Epi>(g, t, e, stream, dev);
+  const int64_t m = t.cut_m && t.cut_m < g.M ? t.cut_m : g.M, n = t.cut_n && t.cut_n < g.N ? t.cut_n : g.N;
+  pgemm_status st = launch_tiles<T, SwapGeom<2>, LA, LB, DUAL, Epi>(g, m, n, t.split, t.k_chunk, e, stream, dev);
+  if (st != PGEMM_OK || (m == g.M && n == g.N)) return st;
+  g.m_base = m < g.M ? (int)m : 0;
+  g.n_base = n < g.N ? (int)n : 0;
+  return launch_small<T, LA, LB, DUAL, Epi>(g, t, second_launch(e, g, t), stream, dev);
 }
 
 // out = round(scale * (A B + what is in sum)): one product, or one of a series

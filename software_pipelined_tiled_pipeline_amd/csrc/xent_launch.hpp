@@ -59,8 +59,11 @@ __global__ void __launch_bounds__(1024) loss_scale_kernel(const float *__restric
                                                           float *__restrict__ scale) {
   __shared__ float tops[16];
   float top = 0.0f;
-  for (int64_t i = threadIdx.x; i < M; i += 1024)
-    if (target[i] != ignore) top = fmaxf(top, fabsf(dloss[i * dstep]));
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < M; i += 1024) {
+    const float d = fabsf(dloss[i * dstep]);
+    top = fmaxf(top, target[i] != ignore ? d : 0.0f);
+  }
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
   if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
