@@ -3,9 +3,10 @@
 //
 // A workgroup owns NT blocks of 16 weight rows and all of K; its waves take
 // blocks of 128 k in turn, so that a weight row's loads are in flight on
-// several waves at once, and add their sums up in LDS at the end.  There is
-// no LDS on the weights' way: a lane loads 16 bytes of row l % 16 and the
-// values go into v_mfma_f32_16x16x32 as they are, with the tokens (16 of
+// several waves at once, and add their sums up in LDS at the end.  Weights are
+// not staged in LDS: four lanes load 64 bytes of a row, so that a load is 16
+// requests and not one a lane, the values change lanes to where
+// v_mfma_f32_16x16x32 wants them, row l % 16, and meet the tokens (16 of
 // them, those past M repeat the last one) as the other operand:
 //   lane l, register r of an accumulator: token 4 (l / 16) + r, weight row l % 16.
 #pragma once
@@ -22,6 +23,14 @@ struct SkinnyArgs {
   int act;
 };
 
+// The 16 bytes of lane 4 (l % 16) + l / 16, for lane l.
+__device__ __forceinline__ u32x4 to_rows(u32x4 v, int from) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v[i]);
+  return r;
+}
+
 // A wave's K loop.  Whole blocks of 128 k (four MFMA steps) are loaded a block
 // ahead of their use, without bounds checks: a token past M repeats the last
 // one, a weight row past the end too (neither reaches a stored value), and a
@@ -35,28 +44,33 @@ struct SkinnyRun {
 
   const SkinnyArgs &a;
   const char *xbase[MT], *wbase[NT];  // of the wave's blocks of 16 rows
-  uint32_t xoff[MT], woff[NT];        // this lane's row there
+  uint32_t xoff[MT], woff[NT];        // what this lane loads there: row l / 4, 16-byte piece l % 4
+  int from;                           // the lane its fragments come from, in bytes
   f32x4 tot[MT][NT];
   u32x4 xr[XD][MT], wr[4][NT];  // the next steps' fragments
 
   __device__ __forceinline__ SkinnyRun(const SkinnyArgs &args) : a(args) {}
 
-  __device__ __forceinline__ void init(int c, int q, int m0, int n0, bool gated) {
+  // Rows of a block of 16 from row0 on: the offset of its row r, the last one's past the end.
+  __device__ __forceinline__ static uint32_t row_offset(int row0, int r, int rows, uint32_t pitch) {
+    return (uint32_t)((row0 + r < rows ? row0 + r : rows - 1) - (row0 < rows ? row0 : rows - 1)) * pitch;
+  }
+
+  __device__ __forceinline__ void init(int lane, int m0, int n0, bool gated) {
     const uint32_t pitch = (uint32_t)a.K * 2u;
+    from = (4 * (lane & 15) + (lane >> 4)) * 4;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int row0 = m0 + 16 * m < a.M ? m0 + 16 * m : a.M - 1;
-      const int row = m0 + 16 * m + c < a.M ? m0 + 16 * m + c : a.M - 1;
-      xbase[m] = reinterpret_cast<const char *>(a.x) + (int64_t)row0 * pitch;
-      xoff[m] = (uint32_t)(row - row0) * pitch + 16u * q;
+      const int row0 = m0 + 16 * m;
+      xbase[m] = reinterpret_cast<const char *>(a.x) + (int64_t)(row0 < a.M ? row0 : a.M - 1) * pitch;
+      xoff[m] = row_offset(row0, lane >> 2, a.M, pitch) + 16u * (lane & 3);
     }
 #pragma unroll
     for (int b = 0; b < NT; ++b) {
-      const int n = n0 + (gated ? b / 2 : b) * 16;
-      const int row0 = n < a.N ? n : a.N - 1;
-      const uint32_t row = (uint32_t)((n + c < a.N ? n + c : a.N - 1) - row0);
-      wbase[b] = reinterpret_cast<const char *>(a.w) + (row0 + (gated && (b & 1) ? (int64_t)a.N : 0)) * pitch;
-      woff[b] = row * pitch + 16u * q;
+      const int row0 = n0 + (gated ? b / 2 : b) * 16;
+      wbase[b] = reinterpret_cast<const char *>(a.w) +
+                 ((row0 < a.N ? row0 : a.N - 1) + (gated && (b & 1) ? (int64_t)a.N : 0)) * pitch;
+      woff[b] = row_offset(row0, lane >> 2, a.N, pitch) + 16u * (lane & 3);
     }
   }
 
@@ -74,10 +88,15 @@ struct SkinnyRun {
   __device__ __forceinline__ void whole(int kb, int nk) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
+      u32x4 x[MT];
 #pragma unroll
-      for (int b = 0; b < NT; ++b)
+      for (int m = 0; m < MT; ++m) x[m] = to_rows(xr[s % XD][m], from);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) tot[m][b] = F::mma(xr[s % XD][m], wr[s][b], tot[m][b]);
+      for (int b = 0; b < NT; ++b) {
+        const u32x4 w = to_rows(wr[s][b], from);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) tot[m][b] = F::mma(x[m], w, tot[m][b]);
+      }
       if (MORE) load_w(s, nk);
       // the slot of step s takes step s + XD
       if (s + XD < 4)
@@ -89,7 +108,8 @@ struct SkinnyRun {
 
   // Places first, first + step, .. below `full` in the order of blocks that
   // starts at `turn`, and the block that K ends in if it is `tail`.
-  __device__ __forceinline__ void run(int first, int step, int full, int turn, bool tail) {
+  __device__ __forceinline__ void run(int lane, int m0, int n0, bool gated, int first, int step, int full, int turn,
+                                      bool tail) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -109,19 +129,20 @@ struct SkinnyRun {
       whole<false>(kb, kb);
     }
     if (!tail) return;
-    const int q = (threadIdx.x & 63) >> 4;
-    auto row = [&](const char *base, uint32_t off) __attribute__((always_inline)) {
-      return reinterpret_cast<const uint16_t *>(base + (off - 16u * q));
-    };
+    // a lane loads its own fragments
+    const int c = lane & 15, q = lane >> 4;
+    const uint32_t pitch = (uint32_t)a.K * 2u;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int k = full * 128 + 32 * s + 8 * q;
       u32x4 x[MT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) x[m] = load_tail(row(xbase[m], xoff[m]), k, a.K);
+      for (int m = 0; m < MT; ++m)
+        x[m] = load_tail(reinterpret_cast<const uint16_t *>(xbase[m] + row_offset(m0 + 16 * m, c, a.M, pitch)), k, a.K);
 #pragma unroll
       for (int b = 0; b < NT; ++b) {
-        const u32x4 f = load_tail(row(wbase[b], woff[b]), k, a.K);
+        const u32x4 f = load_tail(
+            reinterpret_cast<const uint16_t *>(wbase[b] + row_offset(n0 + (gated ? b / 2 : b) * 16, c, a.N, pitch)), k, a.K);
 #pragma unroll
         for (int m = 0; m < MT; ++m) tot[m][b] = F::mma(x[m], f, tot[m][b]);
       }
@@ -137,12 +158,12 @@ __global__ void __launch_bounds__(WAVES * 64) skinny_kernel(SkinnyArgs a) {
   const int n0 = blockIdx.x * (GATED ? NT / 2 : NT) * 16, m0 = blockIdx.y * MT * 16;
 
   SkinnyRun<T, MT, NT> job(a);
-  job.init(lane & 15, lane >> 4, m0, n0, GATED);
+  job.init(lane, m0, n0, GATED);
   const int full = a.K / 128;
   // Each workgroup starts at another block: rows are often a multiple of the
   // memory channels' interleave apart, and all would meet on the same few.
   const int turn = full > 0 ? (int)((blockIdx.x * 0x9E3779B1u >> 12) % (unsigned)full) : 0;
-  job.run(wave, WAVES, full, turn, a.K % 128 != 0 && wave == full % WAVES);
+  job.run(lane, m0, n0, GATED, wave, WAVES, full, turn, a.K % 128 != 0 && wave == full % WAVES);
   constexpr int VALS = MT * NT * 4;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
