@@ -51,6 +51,7 @@ struct Tiling {
   int split;
   int64_t k_chunk;       // a multiple of 64 when split
   int64_t cut_m, cut_n;  // 0: one launch
+  double us;             // what the cut was taken for
 };
 
 constexpr int kMaxPieces = 16;
@@ -70,12 +71,13 @@ struct Cuts {
 };
 
 inline Tiling plan_tiles(int64_t M, int64_t N, int64_t K, bool dual, Cuts may) {
-  Tiling best{false, false, 1, K, 0, 0};
+  Tiling best{false, false, 1, K, 0, 0, 0.0};
   double least = -1.0;
   auto take = [&](double us, const Tiling &t) {
     if (least >= 0.0 && us >= least) return;
     least = us;
     best = t;
+    best.us = us;
   };
   for (int large = 0; large < 2; ++large) {
     const int64_t t = large ? 256 : 128;
@@ -89,7 +91,7 @@ inline Tiling plan_tiles(int64_t M, int64_t N, int64_t K, bool dual, Cuts may) {
       if (!large && blocks * 512 >= kMaxWorkItems) continue;
       double us = large ? large_tiles_us(blocks, steps) : small_tiles_us(blocks, steps);
       if (split > 1) us += 4.0 + (double)M * (double)N * (8.0 * split + 2.0) / 4e6;
-      take(us, Tiling{large != 0, !large && blocks <= 256, split, chunk, 0, 0});
+      take(us, Tiling{large != 0, !large && blocks <= 256, split, chunk, 0, 0, 0.0});
     }
   }
   const double steps = (double)per(K, 64);
@@ -98,11 +100,11 @@ inline Tiling plan_tiles(int64_t M, int64_t N, int64_t K, bool dual, Cuts may) {
     const int64_t n = rounds * 256 / tm, m = may.m ? rounds * 256 / tn : 0;
     if (n > 0 && n < tn) {
       const int64_t rest = per(M, 128) * per(N - n * bn, bn / 2);
-      take(large_tiles_us(tm * n, steps) + 3.0 + small_tiles_us(rest, steps), Tiling{true, rest <= 256, 1, K, 0, n * bn});
+      take(large_tiles_us(tm * n, steps) + 3.0 + small_tiles_us(rest, steps), Tiling{true, rest <= 256, 1, K, 0, n * bn, 0.0});
     }
     if (m > 0 && m < tm) {
       const int64_t rest = per(M - m * 256, 128) * per(N, bn / 2);
-      take(large_tiles_us(m * tn, steps) + 3.0 + small_tiles_us(rest, steps), Tiling{true, rest <= 256, 1, K, m * 256, 0});
+      take(large_tiles_us(m * tn, steps) + 3.0 + small_tiles_us(rest, steps), Tiling{true, rest <= 256, 1, K, m * 256, 0, 0.0});
     }
   }
   return best;
@@ -124,9 +126,17 @@ inline int64_t piece_bytes(const Tiling &t, int64_t M, int64_t N) {
   return t.split > 1 ? t.split * M * up_to(N, 4) * 4 : 0;
 }
 
-// Rows up to which the gated block's forward call runs as a product of few
-// rows (skinny.hpp) instead of tiles.
-constexpr int64_t kSkinnyRows = 64;
+// The gated block's forward call as a product of few rows (skinny.hpp), up to
+// 256 of them: microseconds, by what its workgroups of 16 hidden columns were
+// measured to take for a block of 128 k of up to 32 or 64 tokens.  Rows that do
+// not start on 16 bytes load slower there, but need no padded copy.  100 x 800 x
+// 4096 takes 14 us so and 25 in tiles, 64 x 12288 x 4096 47 and 36.
+constexpr int64_t kSkinnyRows = 256;
+inline double few_rows_us(int64_t M, int64_t F, int64_t D) {
+  const int64_t blocks = per(D, 128), groups = per(F, 16) * per(M, M <= 16 ? 16 : M <= 32 ? 32 : 64);
+  const int64_t per_cu = groups > 256 ? per(groups * blocks, 256) : blocks;
+  return 3.5 + (M <= 32 ? 0.28 : 0.45) * (D % 8 ? 1.8 : 1.0) * (double)per_cu;
+}
 
 // Operands whose rows do not start on 16 bytes are copied into rows that do.
 struct GatedPlan {
@@ -141,15 +151,18 @@ struct GatedPlan {
 inline GatedPlan plan_gated(int64_t M, int64_t F, int64_t D, bool backward, bool keep) {
   GatedPlan p{};
   Carver c;
-  p.skinny = !backward && !keep && M <= kSkinnyRows;
   p.d8 = up_to(D, 8);
   p.py = up_to(2 * F, 8);
+  p.forward = plan_tiles(M, F, p.d8, true, Cuts{false, true});
+  if (!backward && !keep && M <= kSkinnyRows) {
+    const double copies = D % 8 ? 3.0 + (double)(M + 2 * F) * (double)D / 1.1e6 : 0.0;  // 4.4 MB a microsecond
+    p.skinny = few_rows_us(M, F, D) < p.forward.us + copies;
+  }
   p.padded = !p.skinny && D % 8 != 0;
   if (p.padded) {
     p.x = c.take(M * p.d8 * 2);
     p.w = c.take(2 * F * p.d8 * 2);
   }
-  p.forward = plan_tiles(M, F, p.d8, true, Cuts{false, true});
   if (backward) {
     p.dy = c.take(M * p.py * 2);
     p.dx = plan_tiles(M, D, 2 * F, false, Cuts{true, true});

@@ -114,10 +114,10 @@ def test_workspaces(L):
         assert L.pgemm_fused_workspace(op, *sizes, ctypes.byref(n)) == SHAPE, (op, sizes)
     ws = fused.workspace_bytes
     # few rows, and rows that start on 16 bytes, need nothing
-    assert ws("gated", 64, 12288, 4097) == 0
+    assert ws("gated", 16, 12288, 4097) == 0
     assert ws("gated", 2048, 8192, 4096) == 0
     # odd rows: padded copies of both operands
-    assert ws("gated", 65, 100, 1001) == 131072 + 200 * 1008 * 2  # 65 x 1008 x 2 on 256 bytes
+    assert ws("gated", 300, 100, 1001) == 300 * 1008 * 2 + 128 + 200 * 1008 * 2  # parts on 256 bytes
     # the derivative by the projections
     assert ws("gated_bwd", 8192, 12288, 4096) == 8192 * 24576 * 2
     # statistics of every tile; at most 512 MiB of the derivative by the logits, and the running sum
