@@ -66,12 +66,20 @@ struct Frag8<__bf16> {
   // there is no packed bf16 addition: the weights stay 16 + q, and 16 + zero
   // times the sum of x is taken off the product
   static constexpr bool kExactZero = false;
-  __device__ __forceinline__ static u32x4 ones() { return u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}; }
+  __device__ __forceinline__ static u32x4 ones(bool in) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = vector_constant(in ? 0x3F803F80u : 0u);
+    return v;
+  }
   // a scale and a zero point in a dword: the scale's bits above the zero point
   __device__ __forceinline__ static uint32_t pack(uint16_t scale, uint32_t zero) { return (uint32_t)scale << 16 | zero; }
+  // what a unit of x adds too much, negative (exact: 8 bits times 9)
+  __device__ __forceinline__ static float excess(uint32_t packed) {
+    return widen<__bf16>((uint16_t)(packed >> 16)) * (-16.0f - (float)(packed & 0xffu));
+  }
   struct Zero {
-    float off;
-    __device__ __forceinline__ void set(uint32_t packed) { off = 16.0f + (float)(packed & 0xffu); }
+    __device__ __forceinline__ void set(uint32_t) {}
   };
   struct Bits {
     uint32_t mask = scalar_constant(0x00780078u), one = vector_constant(0x41804180u);
@@ -91,6 +99,9 @@ __device__ __forceinline__ u32x4 weight_order(u32x4 v) {
   o[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302u);
   return o;
 }
+
+typedef uint64_t __attribute__((aligned(2))) u64_any;
+typedef uint32_t __attribute__((aligned(1))) u32_any;
 
 template <typename U>
 __device__ __forceinline__ U load_at(const void *base, uint32_t off) {

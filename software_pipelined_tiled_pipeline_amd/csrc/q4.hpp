@@ -20,8 +20,18 @@
 // Waves: KW work on blocks of K in turn and join their sums in LDS at the end;
 // NW beside each other on different weight rows share their tokens in LDS
 // (worth it once reading x again for every 32 weight rows counts: more than
-// 16 tokens).  Two beside each other, and four along K, where four beside each
-// other would leave most CUs without a workgroup.  MT blocks of 16 tokens; XI loads of four tokens each hold them.
+// 16 tokens).  MT blocks of 16 tokens; XI loads of four tokens each hold them.
+//
+// What is left is vector instructions.  Taking a block's 4096 weights apart is
+// 72 (f16) or 56 (bf16) of them, a group's sums times its scale four for every
+// 16 tokens and 16 weight rows; all of it is 170 to 380 for a block, beside 12
+// to 40 MFMAs.  That is why what bf16 weights carry too much is taken off by
+// MFMAs (48 x 4096 x 12288 gated, groups of 32, 37.5 us, and 43.6 with a vector
+// instruction for each accumulator) and why scales are loaded four at a time
+// (one at a time took 80 of 480 instructions).  Deeper rings (three and four
+// slots for more than four tokens) changed nothing.  Measured, with weights of
+// two calls in turn: one token at 8192 x 8192 10.1 us (3.5 TB/s); 48 x 4096 x
+// 12288 gated in groups of 32 31.6 us in bf16, 26 in f16.
 #pragma once
 
 #include "few_rows.hpp"
@@ -43,20 +53,21 @@ struct Q4Args {
 };
 
 // waves a SIMD holds that LDS leaves room for
-constexpr int q4_per_simd(int xi, int nw) { return nw > 1 ? 2 : xi == 1 ? 4 : 3; }
+constexpr int q4_per_simd(int xi, int nw) { return nw == 3 ? 3 : nw > 1 ? 2 : xi == 1 ? 4 : 3; }
 
 template <typename T, bool GATED, int MT, int GS, int XI, int NW, int KW, int D>
 struct Q4Geom {
   static constexpr int NT = 2, WAVES = NW * KW, THREADS = WAVES * 64;
   static constexpr int ROWS = NW * 32;                  // weight rows of a workgroup
   static constexpr int COLS = GATED ? ROWS / 2 : ROWS;  // output columns
-  static constexpr int CB = NW == 1 ? 64 : 16;          // blocks of K whose scales are kept
+  static constexpr int CB = (NW == 1 ? 64 : NW < 4 ? 32 : 16) * GS;  // blocks of K whose scales are kept
   static constexpr int XBUFS = NW == 4 ? 2 : 1;
   static constexpr int RING = WAVES * D * 2048;
   static constexpr int XBYTES = KW * XBUFS * XI * 1024;
-  static constexpr int XW = XI / NW;  // loads of x a wave does for a block
+  static constexpr int XW = (XI + NW - 1) / NW;  // loads of x a wave does for a block
   static constexpr int JOIN = WAVES * MT * NT * 4 * 256;
-  static_assert(XI % NW == 0 && CB % KW == 0 && (XI == 4 * MT || (MT == 1 && XI == 1)), "");
+  static_assert(D >= 2 && D <= 4, "");
+  static_assert(CB % KW == 0 && (XI == 4 * MT || (MT == 1 && XI == 1)), "");
 };
 
 template <typename T, bool GATED, int MT, int GS, int XI, int NW, int KW, int D>
@@ -127,6 +138,7 @@ __global__ void __launch_bounds__(NW *KW * 64, q4_per_simd(XI, NW)) q4_kernel(Q4
 #pragma unroll
     for (int i = 0; i < XW; ++i) {
       const int row = 4 * (wn * XW + i) + (lane >> 4);
+      if (XI % NW != 0 && wn * XW + i >= XI) continue;
       *reinterpret_cast<u32x4 *>(to + row * 256 + (((lane & 15) ^ (row & 15)) * 16)) = weight_order(from[i]);
     }
   };
@@ -141,25 +153,37 @@ __global__ void __launch_bounds__(NW *KW * 64, q4_per_simd(XI, NW)) q4_kernel(Q4
   const uint32_t wread = c * 64 + q * 4;
   const int xr = XI < 4 ? c & (4 * XI - 1) : c;
   const uint32_t *myscales = scales + (wn * 32 + c) * a.sp;
+  // Where the weights carry 16 + zero too much, the sums of x take it out
+  // again: rows 4 g .. 4 g + 3 of `rows[g]` are ones, so that their products
+  // with x leave the sum of x over group l / 16 of the block, token l % 16, in
+  // lane l (zero past the last group): an operand of a product in fp32 with
+  // scale (16 + zero).
+  u32x4 rows[SG];
+  if constexpr (!F::kExactZero) {
+#pragma unroll
+    for (int g = 0; g < SG; ++g) rows[g] = F::ones(c >> 2 == g);
+  }
 
   auto compute = [&](const char *slot, const char *xs_, int kb, int g0) __attribute__((always_inline)) {
+    uint32_t sv[SG][NT];
 #pragma unroll
     for (int g = 0; g < SG; ++g) {
       const int gi = (int)((uint64_t)(uint32_t)(kb * 4 + GS * g) * a.per32 >> 40) - g0;
-      f32x4 acc[MT][NT], xs[MT];
+#pragma unroll
+      for (int b = 0; b < NT; ++b) sv[g][b] = myscales[b * 16 * a.sp + gi];
+    }
+    f32x4 xs[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xs[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int g = 0; g < SG; ++g) {
+      f32x4 acc[MT][NT];
       typename F::Zero z[NT];
-      float sc[NT];
 #pragma unroll
       for (int b = 0; b < NT; ++b) {
-        const uint32_t v = myscales[b * 16 * a.sp + gi];
-        sc[b] = widen<T>((uint16_t)(v >> 16));
-        z[b].set(v);
-      }
+        z[b].set(sv[g][b]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        xs[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int b = 0; b < NT; ++b) acc[m][b] = xs[m];
+        for (int m = 0; m < MT; ++m) acc[m][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       }
 #pragma unroll
       for (int s = g * GS; s < (g + 1) * GS; ++s) {
@@ -167,8 +191,7 @@ __global__ void __launch_bounds__(NW *KW * 64, q4_per_simd(XI, NW)) q4_kernel(Q4
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           xf[m] = *reinterpret_cast<const u32x4 *>(xs_ + (16 * m + xr) * 256 + (((4 * s + q) ^ xr) * 16));
-          // the weights carry 16 + zero too much: the sum of x takes it out again
-          if constexpr (!F::kExactZero) xs[m] = F::mma(xf[m], F::ones(), xs[m]);
+          if constexpr (!F::kExactZero) xs[m] = F::mma(rows[g], xf[m], xs[m]);
         }
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
@@ -179,15 +202,24 @@ __global__ void __launch_bounds__(NW *KW * 64, q4_per_simd(XI, NW)) q4_kernel(Q4
         }
       }
 #pragma unroll
-      for (int b = 0; b < NT; ++b)
+      for (int b = 0; b < NT; ++b) {
+        const float sc = widen<T>((uint16_t)(sv[g][b] >> 16));
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float v = acc[m][b][r];
-            if constexpr (!F::kExactZero) v -= z[b].off * xs[m][r];
-            tot[m][b][r] += sc[b] * v;
-          }
+          for (int r = 0; r < 4; ++r) tot[m][b][r] += sc * acc[m][b][r];
+      }
+    }
+    if constexpr (!F::kExactZero) {
+#pragma unroll
+      for (int b = 0; b < NT; ++b) {
+        uint32_t v = sv[SG - 1][b];  // of group l / 16
+#pragma unroll
+        for (int g = 0; g < SG - 1; ++g) v = q == g ? sv[g][b] : v;
+        const float off = F::excess(v);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) tot[m][b] = __builtin_amdgcn_mfma_f32_16x16x4f32(xs[m][0], off, tot[m][b], 0, 0, 0);
+      }
     }
   };
 
@@ -199,85 +231,115 @@ __global__ void __launch_bounds__(NW *KW * 64, q4_per_simd(XI, NW)) q4_kernel(Q4
     const int mine = wk < nb ? (nb - wk + KW - 1) / KW : 0;
     const int rounds = NW == 1 ? mine : (nb + KW - 1) / KW;
     auto block = [&](int i) {
-      const int p = wk + (i < mine ? i : mine - 1) * KW + turn;
+      const int p = mine > 0 ? wk + (i < mine ? i : mine - 1) * KW + turn : 0;
       return c0 + (p < nb ? p : p - nb);
     };
     // Loads are issued for every i, those past the last block with no bytes
     // (weights) or once more (x): the counts that the waits below rely on.
     u32x4 xreg[D - 1][XW];
-    if (mine > 0) {
 #pragma unroll
-      for (int i = 0; i < D - 1; ++i) {
-        load_x(xreg[i], block(i));
-        compiler_fence();
-        load_w(i, block(i), i < mine);
-        compiler_fence();
-      }
+    for (int i = 0; i < D - 1; ++i) {
+      load_x(xreg[i], block(i));
+      compiler_fence();
+      load_w(i, block(i), i < mine);
+      compiler_fence();
     }
     {
       const int g0 = (int)((uint64_t)(uint32_t)(c0 * 4) * a.per32 >> 40);
       const int ng = (int)((uint64_t)(uint32_t)((c0 + nb) * 4 - 1) * a.per32 >> 40) - g0 + 1;
-      const uint32_t by = 0xFFFFFFFFu / (uint32_t)ng + 1u;  // 0 for one group
-      const uint8_t *zp = a.zero ? a.zero : reinterpret_cast<const uint8_t *>(a.scale);
-      const int total = G::ROWS * ng;
-      auto stage = [&](auto at_once) __attribute__((always_inline)) {
+      // KW * 2 threads a row, four groups each at a time.  Groups past the row's
+      // end, whose products are zeros, get a scale of zero; rows past the
+      // matrix, which reach no stored value, repeat its last one.
+      constexpr int TPR = G::THREADS / G::ROWS;
+      const int r = tid / TPR;
+      int have;
+      int64_t row = block_row(r / 32, r / 16 % 2, &have);
+      row += have == 0 ? (int64_t)a.N - 1 - (row - (GATED && r / 16 % 2 ? a.N : 0)) : (r & 15) < have ? r & 15 : have - 1;
+      const uint16_t *srow = a.scale + row * a.groups;
+      const uint8_t *zrow = a.zero ? a.zero + row * a.groups : reinterpret_cast<const uint8_t *>(srow);
+      uint32_t *to = scales + r * a.sp;
+      auto stage = [&](int base, auto at_once) __attribute__((always_inline)) {
         constexpr int U = decltype(at_once)::value;
-        for (int base = tid; base < total; base += U * G::THREADS) {
-          uint32_t sv[U], zv[U];
-          int to[U];
+        uint64_t sv[U];
+        uint32_t zv[U];
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int idx = base + u * G::THREADS;
-            const int r = ng == 1 ? idx : (int)__umulhi((uint32_t)idx, by);
-            const int g = idx - r * ng;
-            int have;
-            const int64_t row = block_row(r / 32, r / 16 % 2, &have) + (r & 15);
-            // a row or group past the end: its products are zeros or not stored
-            const bool in = idx < total && (r & 15) < have && g0 + g < a.groups;
-            const int64_t at = in ? row * a.groups + g0 + g : 0;
-            sv[u] = a.scale[at];
-            zv[u] = zp[at];
-            to[u] = idx >= total ? -1 : in ? r * a.sp + g : r * a.sp + g + (1 << 30);
+        for (int u = 0; u < U; ++u) {
+          const int g = base + u * TPR * 4 + g0;
+          if (a.groups >= 4) {
+            const int at = g < a.groups - 4 ? g : a.groups - 4;
+            sv[u] = load_at<u64_any>(srow, (uint32_t)at * 2u);
+            zv[u] = load_at<u32_any>(zrow, (uint32_t)at);
+          } else {  // one load has them all
+            sv[u] = zv[u] = 0;
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+              const int at = e < a.groups ? e : a.groups - 1;
+              sv[u] |= (uint64_t)(e < a.groups ? srow[at] : 0) << (16 * e);
+              zv[u] |= (uint32_t)zrow[at] << (8 * e);
+            }
           }
+        }
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (to[u] >= 0)
-              scales[to[u] & ~(1 << 30)] = F::pack(to[u] >> 30 ? 0 : (uint16_t)sv[u], a.zero ? zv[u] : 8u);
+        for (int u = 0; u < U; ++u) {
+          const int g = base + u * TPR * 4;
+          const int past = a.groups >= 4 ? g + g0 - (a.groups - 4) : g + g0;
+          if (past > 0) {
+            sv[u] = past < 4 ? sv[u] >> (16 * past) : 0;
+            zv[u] = past < 4 ? zv[u] >> (8 * past) : 0;
+          }
+          if (g < ng) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              to[g + e] = F::pack((uint16_t)(sv[u] >> (16 * e)), a.zero ? zv[u] >> (8 * e) & 0xffu : 8u);
+          }
         }
       };
       // several loads at once: one after the other would each wait for memory
-      if (total <= G::THREADS)
-        stage(std::integral_constant<int, 1>{});
+      if (ng <= TPR * 4)
+        stage(tid % TPR * 4, std::integral_constant<int, 1>{});
       else
-        stage(std::integral_constant<int, 2048 / G::THREADS>{});
+        for (int base = tid % TPR * 4; base < ng; base += 4 * TPR * 4) stage(base, std::integral_constant<int, 4>{});
+      // All loads so far are over: those of the last scales have come after them.
+      // Said once more, because the compiler counts a load as in flight until a
+      // wait on every path, and a thread with no scale to keep skips its own: it
+      // then waited for all loads before each block's first MFMA.
+      wait_vmcnt<0>();
       lds_barrier();
-      auto round = [&](int i, u32x4(&x)[XW]) __attribute__((always_inline)) {
+      // `behind`: how many blocks' loads follow this block's by the time it is
+      // waited for.  The last D - 2 blocks load none of their own.
+      auto round = [&](int i, u32x4(&x)[XW], auto behind) __attribute__((always_inline)) {
+        constexpr int B = decltype(behind)::value;
         char *xs = xbuf + (G::XBUFS == 1 ? 0 : (i & 1)) * (XI * 1024);
         if (NW > 1 && G::XBUFS == 1) lds_barrier();  // the last block's tokens are no longer read
-        if (mine > 0) {
-          store_x(xs, x, block(i));
+        store_x(xs, x, block(i));
+        if constexpr (B == D - 1) {
           load_x(x, block(i + D - 1));
           wait_lgkmcnt0();  // the slot's last reads are over
           compiler_fence();
           load_w((i + D - 1) % D, block(i + D - 1), i + D - 1 < mine);
-          wait_vmcnt<(D - 1) * (XW + 2)>();
-          compiler_fence();
         }
+        compiler_fence();
+        wait_vmcnt<B *(XW + 2)>();
+        compiler_fence();
         if (NW > 1) lds_barrier();
         if (NW == 1 || i < mine) compute(ring + (i % D) * 2048, xs, block(i), g0);
       };
       int i = 0;
-      if constexpr (D == 2) {
-        for (; i < rounds; ++i) round(i, xreg[0]);
-      } else {
-        for (; i + 1 < rounds; i += 2) {
-          round(i, xreg[0]);
-          round(i + 1, xreg[D - 2]);
-        }
-        if (i < rounds) round(i, xreg[0]);
+      for (; i + D - 1 <= rounds; i += D - 1) {
+#pragma unroll
+        for (int j = 0; j < D - 1; ++j) round(i + j, xreg[j], std::integral_constant<int, D - 1>{});
       }
+      if constexpr (D > 2)
+        if (i < rounds) round(i, xreg[0], std::integral_constant<int, D - 2>{});
+      if constexpr (D > 3)
+        if (i + 1 < rounds) round(i + 1, xreg[1], std::integral_constant<int, D - 3>{});
     }
     wait_vmcnt<0>();
+    // no load of x may be left out for being unused: the waits count them all
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i)
+#pragma unroll
+      for (int k = 0; k < XW; ++k) asm volatile("" ::"v"(xreg[i][k]));
     __syncthreads();  // the ring, the tokens and the scales are free
   }
 

@@ -13,10 +13,10 @@ pgemm_status launch_q4_one(Q4Args a, hipStream_t stream, int dev) {
   static std::atomic<uint64_t> lds_set{0};
   constexpr int kMost = 160 * 1024;  // LDS per workgroup on gfx950
   const int64_t k = a.K < G::CB * 128 ? up_to(a.K, 128) : G::CB * 128;
-  a.sp = (int)(k / a.group + 2) | 1;
+  a.sp = (int)up_to(k / a.group + 2, 4) | 1;
   const int work = G::RING + G::XBYTES + G::ROWS * a.sp * 4;
   const int lds = work > G::JOIN ? work : G::JOIN;
-  static_assert(G::RING + G::XBYTES + G::ROWS * (G::CB * 4 + 3) * 4 <= kMost && G::JOIN <= kMost, "groups of 32 fit");
+  static_assert(G::RING + G::XBYTES + G::ROWS * (G::CB / GS * 4 + 5) * 4 <= kMost && G::JOIN <= kMost, "groups of 32 fit");
   auto kern = q4_kernel<T, GATED, MT, GS, XI, NW, KW, D>;
   if (lds > 65536) {
     pgemm_status st = allow_lds(kern, kMost, dev, lds_set);
@@ -41,15 +41,27 @@ pgemm_status launch_q4(const Q4Args &a, hipStream_t stream, int dev) {
     if (groups <= 256) return launch_q4_one<T, GATED, 1, GS, 4, 1, 8, 2>(a, stream, dev);
     return launch_q4_one<T, GATED, 1, GS, 4, 1, 4, 2>(a, stream, dev);
   }
-  // 64 workgroups of 128 rows take 38 us for 22 x 4489 x 4028 in groups of 32
-  if (groups < 4 * 128) {
-    if (a.M <= 32) return launch_q4_one<T, GATED, 2, GS, 8, 2, 4, 2>(a, stream, dev);
-    if (a.M <= 48) return launch_q4_one<T, GATED, 3, GS, 12, 2, 4, 2>(a, stream, dev);
-    return launch_q4_one<T, GATED, 4, GS, 16, 2, 4, 2>(a, stream, dev);
+  // Waves beside each other: a workgroup fills a CU.  Three (four) of them take
+  // 1.25 (1.4) times as long as two, and need fewer rounds of 256 workgroups.
+  // Groups of 64, K 4096, microseconds with two and with three (M 32 and 48) or
+  // four (M 64):
+  //   N      16384       24576       32000       49152
+  //   M 32   17.1 19.8   29.7 20.6   29.9 36.9   43.7 38.4
+  //   M 48   20.9 25.5   37.1 26.0   37.5 47.7   55.0 49.5
+  //   M 64   25.6 33.9   46.3 33.9   47.0 35.6   69.0 65.2
+  const int64_t blocks_m = per(a.M, 64);
+  auto rounds = [&](int nw) { return per(per(groups, nw) * blocks_m, 256); };
+  const int64_t two = rounds(2);
+  if (a.M <= 48) {
+    const bool three = rounds(3) * 5 < two * 4;
+    if (a.M <= 32)
+      return three ? launch_q4_one<T, GATED, 2, GS, 8, 3, 4, 2>(a, stream, dev)
+                   : launch_q4_one<T, GATED, 2, GS, 8, 2, 4, 2>(a, stream, dev);
+    return three ? launch_q4_one<T, GATED, 3, GS, 12, 3, 4, 2>(a, stream, dev)
+                 : launch_q4_one<T, GATED, 3, GS, 12, 2, 4, 2>(a, stream, dev);
   }
-  if (a.M <= 32) return launch_q4_one<T, GATED, 2, GS, 8, 4, 2, 2>(a, stream, dev);
-  if (a.M <= 48) return launch_q4_one<T, GATED, 3, GS, 12, 4, 2, 2>(a, stream, dev);
-  return launch_q4_one<T, GATED, 4, GS, 16, 4, 2, 2>(a, stream, dev);
+  return rounds(4) * 7 < two * 5 ? launch_q4_one<T, GATED, 4, GS, 16, 4, 2, 2>(a, stream, dev)
+                                 : launch_q4_one<T, GATED, 4, GS, 16, 2, 4, 2>(a, stream, dev);
 }
 
 template <typename T, bool GATED>

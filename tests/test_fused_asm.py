@@ -124,6 +124,25 @@ def test_no_spills_among_mfmas(unit_asm, unit):
                 assert "scratch_" not in block, name
 
 
+Q4 = re.compile(r"^(_ZN5pgemm9q4_kernelI\S*?Lb[01]ELi(\d+)ELi\d+ELi(\d+)ELi(\d+)ELi\d+ELi\d+E\S*):.*?\n(.*?)s_endpgm", re.S | re.M)
+
+
+@pytest.mark.parametrize("unit", [u for u in ALL if u.startswith("fused_q4")])
+def test_loads_that_waits_count(unit_asm, unit):
+    # A block's weights (two loads into LDS) are waited for by the number of
+    # loads after them: each pair has its tokens' loads before it, none of
+    # which the compiler may leave out where it sees no use of their values.
+    kernels = 0
+    for m in Q4.finditer(unit_asm[unit]):
+        name, per_block = m.group(1), -(-int(m.group(3)) // int(m.group(4)))
+        kinds = "".join("w" if " lds" in line else "x" for line in m.group(5).splitlines()
+                        if re.match(r"\s+(global_load_dwordx4|buffer_load_dwordx4\s.*\blds)\b", line))
+        assert kinds.count("w") >= 4, name
+        assert kinds == ("x" * per_block + "ww") * (kinds.count("w") // 2), f"{name}: {kinds}"
+        kernels += 1
+    assert kernels >= 60
+
+
 def test_the_check_finds_planted_faults():
     good = "\ts_mov_b32 m0, s3\n\ts_nop 0\n\tbuffer_load_dwordx4 v1, s[4:7], 0 offen lds\n"
     assert lds_load_faults(good) == ([], 1)

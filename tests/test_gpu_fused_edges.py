@@ -337,6 +337,22 @@ def test_q4_sizes(pg, fmt, M, N, K, group):
                 *ref.q4(x, values, scale, zero, group, act="gelu"))
 
 
+# three and four waves beside each other, more than one stretch of scales, and
+# every number of blocks that a wave may be left with
+Q4_WAVES = [(24, 16420, 4500, 32), (48, 16400, 1000, 64), (33, 16400, 2500, 96), (130, 8200, 700, 32),
+            (50, 16390, 2200, 32)] + [(M, 48, 128 * blocks - 5, 32) for M in (3, 11, 30) for blocks in (5, 9, 18, 27, 37)]
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("M,N,K,group", Q4_WAVES)
+def test_q4_waves(pg, fmt, M, N, K, group):
+    x, values, scale, zero = q4_case(M + N + K, fmt, M, N, K, group, True)
+    packed = pg.pack_q4(values)
+    check("y", call(pg, fmt, "q4", x, packed, scale, zero, group=group), ref.q4(x, values, scale, zero, group))
+    check_range("h", call(pg, fmt, "q4_gated", x, packed, scale, zero, group=group, act="silu"),
+                *ref.q4(x, values, scale, zero, group, act="silu"))
+
+
 @pytest.mark.parametrize("fmt", FMT)
 def test_q4_any_byte_as_zero_point(pg, fmt):
     x, values, scale, _ = q4_case(15, fmt, 5, 256, 256, 32, True)
