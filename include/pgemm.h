@@ -365,6 +365,8 @@ pgemm_status pgemm_bf16_xent(const uint16_t *x, const uint16_t *w, const int64_t
  * or one value that all rows share (dloss_step 0), 4-byte aligned.  lse: from
  * the forward call.  The logits are computed again in pieces of the
  * vocabulary.  dloss = 0 gives a row no gradient whatever its logits are.
+ * A row that is ignored or whose dloss is 0 adds 0 times its x to dw: infinities
+ * and NaN in that x still reach dw's columns, as they do in any product.
  */
 pgemm_status pgemm_f16_xent_bwd(const float *dloss, int dloss_step, const uint16_t *x, const uint16_t *w,
                                 const int64_t *target, const float *lse, uint16_t *dx, uint16_t *dw, int64_t M,

@@ -130,7 +130,7 @@ inline int64_t piece_bytes(const Tiling &t, int64_t M, int64_t N) {
 // 256 of them: microseconds, by what its workgroups of 16 hidden columns were
 // measured to take for a block of 128 k of up to 32 or 64 tokens.  Rows that do
 // not start on 16 bytes load slower there, but need no padded copy.  100 x 800 x
-// 4096 takes 14 us so and 25 in tiles, 64 x 12288 x 4096 47 and 36.
+// 4096 takes 14 us so and 25 in tiles, 64 x 12288 x 4096 47 and 32.
 constexpr int64_t kSkinnyRows = 256;
 inline double few_rows_us(int64_t M, int64_t F, int64_t D) {
   const int64_t blocks = per(D, 128), groups = per(F, 16) * per(M, M <= 16 ? 16 : M <= 32 ? 32 : 64);

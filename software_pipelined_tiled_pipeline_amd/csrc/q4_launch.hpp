@@ -27,8 +27,8 @@ pgemm_status launch_q4_one(Q4Args a, hipStream_t stream, int dev) {
   return launched();
 }
 
-// Waves along K: so many that all workgroups together give each CU about
-// sixteen.
+// Waves along K, up to 16 tokens: so many that all workgroups together give
+// each CU about sixteen.
 template <typename T, bool GATED, int GS>
 pgemm_status launch_q4(const Q4Args &a, hipStream_t stream, int dev) {
   const int64_t groups = per(a.N, GATED ? 16 : 32);
