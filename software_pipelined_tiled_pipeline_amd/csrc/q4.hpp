@@ -19,8 +19,8 @@
 //
 // Waves: KW work on blocks of K in turn and join their sums in LDS at the end;
 // NW beside each other on different weight rows share their tokens in LDS
-// (worth it once reading x again for every 32 weight rows counts: more than
-// 16 tokens).  MT blocks of 16 tokens; XI loads of four tokens each hold them.
+// (worth it where more than 16 tokens would read the weights of many rows more
+// than once).  MT blocks of 16 tokens; XI loads of four tokens each hold them.
 //
 // What is left is vector instructions.  Taking a block's 4096 weights apart is
 // 72 (f16) or 56 (bf16) of them, a group's sums times its scale four for every

@@ -27,7 +27,7 @@ pgemm_status launch_q4_one(Q4Args a, hipStream_t stream, int dev) {
   return launched();
 }
 
-// Waves along K, up to 16 tokens: so many that all workgroups together give
+// Waves along K, with 16 tokens a workgroup: so many that all workgroups together give
 // each CU about sixteen.
 template <typename T, bool GATED, int GS>
 pgemm_status launch_q4(const Q4Args &a, hipStream_t stream, int dev) {
@@ -37,31 +37,34 @@ pgemm_status launch_q4(const Q4Args &a, hipStream_t stream, int dev) {
     if (groups <= 512) return launch_q4_one<T, GATED, 1, GS, 1, 1, 8, 3>(a, stream, dev);
     return launch_q4_one<T, GATED, 1, GS, 1, 1, 4, 3>(a, stream, dev);
   }
-  if (a.M <= 16) {
+  // More than 16 tokens: 16 of them a workgroup, which reads weights again for
+  // every 16 but has no wave wait for another, or up to 64 shared by two, three
+  // or four waves beside each other, whose workgroup fills a CU.  The costs are
+  // of a round of 256 workgroups, in tenths of a microsecond at K 4096.  Groups
+  // of 64, bf16, K 4096, microseconds with 16 tokens a workgroup, two waves, and
+  // three (M 32 and 48) or four (M 64):
+  //   N          4480             12288            16384            24576            49152
+  //   M 32   10.3 14.8 18.4   14.9 16.1 19.6   19.1 16.9 19.8   26.9 29.7 20.6   50.7 43.7 38.4
+  //   M 48   10.6 18.8 23.9   22.0 20.4 24.8   27.7 21.3 25.5   39.6 37.1 26.0   72.6 55.0 49.5
+  //   M 64   14.8 22.9 32.2   25.8 25.1 34.0   34.3 26.1 33.9   49.4 46.3 33.9   95.4 69.0 65.2
+  const int blocks = a.M <= 32 ? 2 : a.M <= 48 ? 3 : 4;  // of 16 tokens, beside two waves or more
+  const int64_t blocks_m = per(a.M, 64);
+  auto rounds = [&](int nw) { return per(per(groups, nw) * blocks_m, 256); };
+  const int64_t one = 25 + 42 * per(groups * per(a.M, 16), 256);
+  const int64_t two = (blocks == 2 ? 155 : blocks == 3 ? 195 : 240) * rounds(2);
+  const int64_t more = blocks == 4 ? 340 * rounds(4) : (blocks == 2 ? 200 : 255) * rounds(3);
+  if (a.M <= 16 || (one < two && one < more)) {
     if (groups <= 256) return launch_q4_one<T, GATED, 1, GS, 4, 1, 8, 2>(a, stream, dev);
     return launch_q4_one<T, GATED, 1, GS, 4, 1, 4, 2>(a, stream, dev);
   }
-  // Waves beside each other: a workgroup fills a CU.  Three (four) of them take
-  // 1.25 (1.4) times as long as two, and need fewer rounds of 256 workgroups.
-  // Groups of 64, K 4096, microseconds with two and with three (M 32 and 48) or
-  // four (M 64):
-  //   N      16384       24576       32000       49152
-  //   M 32   17.1 19.8   29.7 20.6   29.9 36.9   43.7 38.4
-  //   M 48   20.9 25.5   37.1 26.0   37.5 47.7   55.0 49.5
-  //   M 64   25.6 33.9   46.3 33.9   47.0 35.6   69.0 65.2
-  const int64_t blocks_m = per(a.M, 64);
-  auto rounds = [&](int nw) { return per(per(groups, nw) * blocks_m, 256); };
-  const int64_t two = rounds(2);
-  if (a.M <= 48) {
-    const bool three = rounds(3) * 5 < two * 4;
-    if (a.M <= 32)
-      return three ? launch_q4_one<T, GATED, 2, GS, 8, 3, 4, 2>(a, stream, dev)
-                   : launch_q4_one<T, GATED, 2, GS, 8, 2, 4, 2>(a, stream, dev);
-    return three ? launch_q4_one<T, GATED, 3, GS, 12, 3, 4, 2>(a, stream, dev)
-                 : launch_q4_one<T, GATED, 3, GS, 12, 2, 4, 2>(a, stream, dev);
-  }
-  return rounds(4) * 7 < two * 5 ? launch_q4_one<T, GATED, 4, GS, 16, 4, 2, 2>(a, stream, dev)
-                                 : launch_q4_one<T, GATED, 4, GS, 16, 2, 4, 2>(a, stream, dev);
+  if (blocks == 2)
+    return two <= more ? launch_q4_one<T, GATED, 2, GS, 8, 2, 4, 2>(a, stream, dev)
+                       : launch_q4_one<T, GATED, 2, GS, 8, 3, 4, 2>(a, stream, dev);
+  if (blocks == 3)
+    return two <= more ? launch_q4_one<T, GATED, 3, GS, 12, 2, 4, 2>(a, stream, dev)
+                       : launch_q4_one<T, GATED, 3, GS, 12, 3, 4, 2>(a, stream, dev);
+  return two <= more ? launch_q4_one<T, GATED, 4, GS, 16, 2, 4, 2>(a, stream, dev)
+                     : launch_q4_one<T, GATED, 4, GS, 16, 4, 2, 2>(a, stream, dev);
 }
 
 template <typename T, bool GATED>

@@ -337,10 +337,12 @@ def test_q4_sizes(pg, fmt, M, N, K, group):
                 *ref.q4(x, values, scale, zero, group, act="gelu"))
 
 
-# three and four waves beside each other, more than one stretch of scales, and
+# two, three and four waves beside each other, 16 tokens a workgroup with more
+# than 16 of them, more than one stretch of scales, and
 # every number of blocks that a wave may be left with
 Q4_WAVES = [(24, 16420, 4500, 32), (48, 16400, 1000, 64), (33, 16400, 2500, 96), (130, 8200, 700, 32),
-            (50, 16390, 2200, 32)] + [(M, 48, 128 * blocks - 5, 32) for M in (3, 11, 30) for blocks in (5, 9, 18, 27, 37)]
+            (50, 16390, 2200, 32), (24, 13000, 4500, 32), (40, 13010, 1000, 64), (60, 13020, 300, 128),
+            (31, 130, 8300, 32), (64, 500, 1450, 64), (100, 2000, 520, 128)] + [(M, 48, 128 * blocks - 5, 32) for M in (3, 11, 30) for blocks in (5, 9, 18, 27, 37)]
 
 
 @pytest.mark.parametrize("fmt", FMT)
