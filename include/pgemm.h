@@ -303,6 +303,9 @@ pgemm_status pgemm_plan_arena(int32_t n, const pgemm_lds_block *blocks, int64_t 
  *   - All sums, statistics and activations are fp32; a result is rounded to
  *     its type once.  The backward calls also round the derivative by the
  *     projections or logits to the operand type, since they multiply by it.
+ *     In f16 it is scaled there by a power of two, so that it does not leave
+ *     the type's range where the gradients do not.  Until they are written,
+ *     dx and dw may hold intermediate values.
  *   - Pointers are 16-byte aligned and outputs do not overlap inputs.  An
  *     empty matrix's pointer may be NULL.
  *   - Some calls need a workspace: pgemm_fused_workspace gives its bytes, and

@@ -86,6 +86,15 @@ __device__ __forceinline__ void store_tile(const char *st, int pitch, int c0, ui
   }
 }
 
+// Exponents of the powers of two that an output still has to be multiplied by
+// may wait in the output itself: in the first element of each 128 x 128 block
+// (DyScale).  A tile's own is read by its workgroup alone, before it stores the
+// tile.
+constexpr int kSeedStep = 128;  // tiles start at multiples of it
+__device__ __forceinline__ float seeded_scale(const uint16_t *out, int64_t po, int m0, int n0) {
+  return ldexpf(1.0f, (int16_t)out[(int64_t)m0 * po + n0]);
+}
+
 // out = round((sum + acc) * *scale): one product, or the last of several whose
 // running sum is kept in fp32 (SumEpi).
 struct StoreEpi {
@@ -93,6 +102,7 @@ struct StoreEpi {
     uint16_t *out;
     int64_t po;
     const float *scale;  // one device float, or null
+    bool seeded;         // the factor is a power of two that waits in out
   };
   template <typename T, class G, class W>
   struct Run {
@@ -100,7 +110,7 @@ struct StoreEpi {
     __device__ __forceinline__ static void finish(W &w, const Args &e, const FusedProduct &g, char *smem, int m0,
                                                   int n0, int wm, int wn, int lane, int tid, const float *sum, int ps) {
       constexpr int PITCH = Staging<G::BN>::PITCH;
-      const float k = e.scale ? *e.scale : 1.0f;
+      const float k = e.seeded ? seeded_scale(e.out, e.po, m0, n0) : e.scale ? *e.scale : 1.0f;
       const int lr = wm * G::WM + (lane & 15), lc = wn * G::WN + 4 * (lane >> 4);
 #pragma unroll
       for (int i = 0; i < W::TM; ++i)
@@ -157,17 +167,20 @@ struct SumEpi {
   };
 };
 
-// A piece of K: the sums as they are, fp32, for join_pieces_kernel.
+// A piece of K: the sums in fp32, for join_pieces_kernel.
 struct PieceEpi {
   struct Args {
     float *part;  // [pieces][M][pp]
     int pp;       // a multiple of 4
+    const uint16_t *seeds;  // null, or the output whose factors are taken here (exactly), and its pitch
+    int64_t po;
   };
   template <typename T, class G, class W>
   struct Run {
     __device__ __forceinline__ void operator()(W &w, const Args &e, const FusedProduct &g, char *smem, int m0, int n0,
                                                int wm, int wn, int lane, int tid) const {
       float *part = e.part + (int64_t)g.piece * g.M * e.pp;
+      const float k = e.seeds ? seeded_scale(e.seeds, e.po, m0, n0) : 1.0f;
 #pragma unroll
       for (int i = 0; i < W::TM; ++i) {
         const int row = m0 + wm * G::WM + 16 * i + (lane & 15);
@@ -175,7 +188,7 @@ struct PieceEpi {
 #pragma unroll
         for (int j = 0; j < W::TN; ++j) {
           const int col = n0 + wn * G::WN + 16 * j + 4 * (lane >> 4);
-          if (col < g.N) *reinterpret_cast<f32x4 *>(part + (int64_t)row * e.pp + col) = w.acc[i][j];
+          if (col < g.N) *reinterpret_cast<f32x4 *>(part + (int64_t)row * e.pp + col) = w.acc[i][j] * k;
         }
       }
     }
@@ -223,6 +236,62 @@ struct GatedEpi {
   };
 };
 
+// The factor of dy = [dh up act'(gate) | dh act(gate)] in f16, where dy is
+// rounded to 16 bits between the products: binary16 ends at 65504 and has fewer
+// bits below 2^-14, so that a mean loss's dh of 1e-5 cost dW 2.8e-3 instead of
+// 2.9e-4, and a dy past its end made dx and dW infinite that were not.
+//
+// |act'| < 1.13, |act(g)| <= |g|, and |g| and |up| are at most |x's row| |w's row|, so
+// no entry passes 1.13 B with B = max |dh| * max |x's row| * max |w's row|.  The factor
+// is the power of two that takes B into [2^14, 2^15): no entry overflows, and
+// those down to B / 2^29 keep all their bits (a usual one is some 2^10 below B).
+// dx and dW are multiplied by its inverse, exactly, before they are rounded.
+//
+// gated_range_kernel takes the maxima.  Their `parts` wait in rows of dw, and
+// the inverse's exponent at the tiles' starts in dx and dw: the workspace has no
+// room for them.
+struct DyScale {
+  const float4 *part;  // max |dh|, and bounds of the squared norms of x's and w's rows
+  int parts;           // -1: no factor; 0: the exponent is in dx already
+  uint16_t *dx, *dw;
+  int64_t rows_x, rows_w, D;
+
+  __device__ __forceinline__ static float4 top(float4 a, float4 b) {
+    return make_float4(fmaxf(a.x, b.x), fmaxf(a.y, b.y), fmaxf(a.z, b.z), 0.0f);
+  }
+  __device__ __forceinline__ static float4 wave_top(float4 t) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) t = top(t, make_float4(__shfl_xor(t.x, d), __shfl_xor(t.y, d), __shfl_xor(t.z, d), 0.0f));
+    return t;
+  }
+  // the inverse's exponent
+  __device__ __forceinline__ static int exponent(float4 t) {
+    const float bound = t.x * sqrtf(t.y) * sqrtf(t.z);  // at most 2^70
+    int e = 15;
+    if (bound > 0.0f) frexpf(bound, &e);
+    return e - 15;
+  }
+  // leaves it where the products look for it; `first`, step: which of the starts
+  __device__ __forceinline__ void seed(int e, int64_t first, int64_t step) const {
+    const int64_t across = (D + kSeedStep - 1) / kSeedStep;
+    const int64_t in_x = (rows_x + kSeedStep - 1) / kSeedStep * across, in_w = (rows_w + kSeedStep - 1) / kSeedStep * across;
+    for (int64_t i = first; i < in_x + in_w; i += step) {
+      const int64_t j = i < in_x ? i : i - in_x;
+      (i < in_x ? dx : dw)[j / across * kSeedStep * D + j % across * kSeedStep] = (uint16_t)(int16_t)e;
+    }
+  }
+  // The factor, by every wave of every workgroup of dy's kernel.
+  __device__ __forceinline__ float take(int tid, int threads) const {
+    if (parts < 0) return 1.0f;
+    if (parts == 0) return ldexpf(1.0f, -(int16_t)*dx);
+    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = tid & 63; i < parts; i += 64) t = top(t, part[i]);
+    const int e = exponent(wave_top(t));
+    seed(e, (int64_t)blockIdx.x * threads + tid, (int64_t)gridDim.x * threads);
+    return ldexpf(1.0f, -e);
+  }
+};
+
 // The gated block's derivative from recomputed projections: with dh read
 // here, dy[m] = [dh up act'(gate) | dh act(gate)], one row of 2 N values.
 struct GatedSlopeEpi {
@@ -231,6 +300,7 @@ struct GatedSlopeEpi {
     uint16_t *dy;
     int64_t py;
     int act;
+    DyScale scale;
   };
   template <typename T, class G, class W>
   struct Run {
@@ -238,6 +308,7 @@ struct GatedSlopeEpi {
                                                int wm, int wn, int lane, int tid) const {
       constexpr int ON = G::BN / 2, PITCH = Staging<G::BN>::PITCH;
       const int r = lane & 15, q = lane >> 4;
+      const float s = e.scale.take(tid, G::THREADS);
 #pragma unroll
       for (int i = 0; i < W::TM; ++i) {
         const int lrow = wm * G::WM + 16 * i + r;
@@ -263,8 +334,8 @@ struct GatedSlopeEpi {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const Activation v = activate_slope(e.act, ga[x]);
-            dg[x] = d[x] * up[x] * v.d;
-            du[x] = d[x] * v.a;
+            dg[x] = d[x] * s * up[x] * v.d;
+            du[x] = d[x] * s * v.a;
           }
           char *st = smem + lrow * PITCH + lcol * 2;
           *reinterpret_cast<u32x2 *>(st) = Mfma<T>::pack4(dg[0], dg[1], dg[2], dg[3]);

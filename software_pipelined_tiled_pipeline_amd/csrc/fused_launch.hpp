@@ -103,7 +103,8 @@ pgemm_status launch_sum(const FusedProduct &g, const Tiling &t, const SumEpi::Ar
   if (t.split > 1) {
     const int pp = (int)up_to(g.N, 4);
     float *sums = reinterpret_cast<float *>(part);
-    pgemm_status st = launch_product<T, LA, LB, false, PieceEpi>(g, t, PieceEpi::Args{sums, pp}, stream, dev);
+    pgemm_status st = launch_product<T, LA, LB, false, PieceEpi>(
+        g, t, PieceEpi::Args{sums, pp, e.out.seeded ? e.out.out : nullptr, e.out.po}, stream, dev);
     if (st != PGEMM_OK) return st;
     hipLaunchKernelGGL(join_pieces_kernel<T>, dim3(row_grid((int64_t)g.M * (pp / 4))), dim3(256), 0, stream, sums, t.split,
                        g.M, g.N, pp, e);

@@ -145,7 +145,7 @@ pgemm_status xent_backward(const XentCall &c) {
     g.N = (int)c.D;
     g.K = (int)c.M;
     st = launch_sum<T, Lay::KR, Lay::KR>(g, p.dw,
-                                         SumEpi::Args{nullptr, 0, 1, 1, {c.dw + v0 * c.D, c.D, unscale}}, c.ws + p.part,
+                                         SumEpi::Args{nullptr, 0, 1, 1, {c.dw + v0 * c.D, c.D, unscale, false}}, c.ws + p.part,
                                          c.stream, c.dev);
     if (st != PGEMM_OK) return st;
     // dx += dz W
@@ -156,7 +156,7 @@ pgemm_status xent_backward(const XentCall &c) {
     g.K = (int)n;
     st = launch_sum<T, Lay::KC, Lay::KR>(
         g, shortened(p.dx, n),
-        SumEpi::Args{sum, (int)p.ps, v0 == 0, v0 + n == c.V, {c.dx, c.D, unscale}}, c.ws + p.part, c.stream, c.dev);
+        SumEpi::Args{sum, (int)p.ps, v0 == 0, v0 + n == c.V, {c.dx, c.D, unscale, false}}, c.ws + p.part, c.stream, c.dev);
     if (st != PGEMM_OK) return st;
   }
   return PGEMM_OK;
