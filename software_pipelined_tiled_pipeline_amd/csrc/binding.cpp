@@ -64,6 +64,11 @@ struct Call {
     if (v == -1 && PyErr_Occurred()) ok = false;
     return v;
   }
+  bool truth(int i) {
+    const int v = ok ? PyObject_IsTrue(args[i]) : 0;
+    if (v < 0) ok = false;
+    return v > 0;
+  }
   bool none(int i) const { return args[i] == Py_None; }
 };
 
@@ -106,10 +111,10 @@ PyObject *gated(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const at::Tensor *x = c.ok ? c.tensor(0, c.type, {-1, -1}) : nullptr;
     const at::Tensor *w = x ? c.tensor(1, c.type, {-1, x->size(1)}) : nullptr;
     const int act = (int)c.integer(2);
+    const bool save = c.truth(3);
     if (!c.ok || w->size(0) % 2) return nothing();
     const int64_t M = x->size(0), F = w->size(0) / 2, D = x->size(1);
     at::Tensor h = made(x, c.type, {M, F}), saved;
-    const bool save = c.args[3] == Py_True;
     if (save) saved = made(x, at::kFloat, {M, per(F, 4), 8});
     const auto f = reinterpret_cast<decltype(&pgemm_f16_gated)>(c.entry);
     if (f(ptr(x), ptr(w), ptr(&h), save ? ptr<float>(&saved) : nullptr, M, F, D, act, c.stream) != PGEMM_OK) return nothing();
