@@ -109,6 +109,14 @@ def _act(act):
     return ACTS[act]
 
 
+def _ignored(ignore_index):
+    """ignore_index as the library's 64 bits: ctypes would cut a longer one off without a word."""
+    i = int(ignore_index)
+    if not -(1 << 63) <= i < 1 << 63:
+        raise ValueError(f"ignore_index must fit 64 bits, not {ignore_index!r}")
+    return i
+
+
 # A call first takes the short way: _binding checks its tensors, allocates the
 # outputs and calls the library (8.3 us -> 5.4 for a product of one token).  It
 # returns None for anything that is not plainly right, and where the stream's
@@ -267,11 +275,12 @@ def _make(fmt, dtype_name):
                 both = _binding.xent(address, dev, handle, code_of, x, w, target, ignore_index)
                 if both is not None:
                     return both
+        ignore = _ignored(ignore_index)
         M, V, D, dev = head(x, w, target, getattr(torch, dtype_name))
         loss = _out("loss", loss, torch.float32, (M,), dev, x)
         lse = _out("lse", lse, torch.float32, (M,), dev, x)
         _run(XENT, dev, (x.data_ptr(), w.data_ptr(), target.data_ptr(), loss.data_ptr(), lse.data_ptr(), M, V, D,
-                         int(ignore_index)), workspace_bytes("xent", M, V, D))
+                         ignore), workspace_bytes("xent", M, V, D))
         return loss, lse
 
     xent.__doc__ = (f"(loss[M], lse[M]) in fp32: softmax cross entropy of the logits x w^T for {dtype_name} x [M,D] and w "
@@ -288,7 +297,7 @@ def _make(fmt, dtype_name):
                 both = _binding.xent_bwd(address, dev, handle, code_of, dloss, x, w, target, lse, ignore_index)
                 if both is not None:
                     return both
-        dtype = getattr(torch, dtype_name)
+        dtype, ignore = getattr(torch, dtype_name), _ignored(ignore_index)
         M, V, D, dev = head(x, w, target, dtype)
         _want("lse", lse, torch.float32, (M,), dev)
         if dloss.dtype != torch.float32 or dloss.get_device() != dev:
@@ -302,7 +311,7 @@ def _make(fmt, dtype_name):
         dx = _out("dx", dx, dtype, (M, D), dev, x)
         dw = _out("dw", dw, dtype, (V, D), dev, x)
         _run(XENT_BWD, dev, (dloss.data_ptr(), step, x.data_ptr(), w.data_ptr(), target.data_ptr(), lse.data_ptr(),
-                             dx.data_ptr(), dw.data_ptr(), M, V, D, int(ignore_index)),
+                             dx.data_ptr(), dw.data_ptr(), M, V, D, ignore),
              workspace_bytes("xent_bwd", M, V, D))
         return dx, dw
 
@@ -310,9 +319,9 @@ def _make(fmt, dtype_name):
                         "the forward call's lse.")
 
     def q4_operands(x, q, scale, zero, group, dtype):
+        if group <= 0 or group % 32 or group >= 1 << 31:
+            raise ValueError("group must be a positive multiple of 32 below 2^31")
         M, K, dev = _first("x", x, dtype)
-        if group <= 0 or group % 32:
-            raise ValueError("group must be a positive multiple of 32")
         rows, groups = _rows("q", q, torch.uint8, -(-K // 32) * 16, dev), -(-K // group)
         _want("scale", scale, dtype, (rows, groups), dev)
         if zero is not None:
