@@ -298,8 +298,8 @@ pgemm_status pgemm_plan_arena(int32_t n, const pgemm_lds_block *blocks, int64_t 
  *   - Matrices are row-major and contiguous, M rows of tokens; weights have
  *     one row per output feature, as rhs in the NT calls.  Any sizes: odd
  *     widths and tails cost a padded copy of an operand, or guarded loads.
- *     D, 2 F (gated) and K (q4) at most 2^22, other sizes below 2^31; M rows of a q4 call
- *     at most 2^20 - 16.
+ *     D, 2 F (gated) and K (q4) at most 2^22, other sizes at most 2^31 - 256 (group: below
+ *     2^31); M rows of a q4 call at most 2^20 - 16.
  *   - All sums, statistics and activations are fp32; a result is rounded to
  *     its type once.  The backward calls also round the derivative by the
  *     projections or logits to the operand type, since they multiply by it.

@@ -55,7 +55,7 @@ struct Tiling {
 };
 
 constexpr int kMaxPieces = 16;
-constexpr int64_t kMaxWorkItems = (int64_t)1 << 32;  // of a dispatch
+constexpr int64_t kMaxWorkItems = (int64_t)1 << 32;  // a dispatch's are fewer
 
 inline double small_tiles_us(int64_t blocks, double steps) {
   if (blocks <= 256) return 0.45 * steps + 6.0;
@@ -88,7 +88,7 @@ inline Tiling plan_tiles(int64_t M, int64_t N, int64_t K, bool dual, Cuts may) {
       if (split != want || (want > 1 && chunk < 256)) continue;
       const double steps = (double)per(chunk, 64);
       const int64_t blocks = tiles * split;
-      if (!large && blocks * 512 >= kMaxWorkItems) continue;
+      if (blocks * (large ? 256 : 512) >= kMaxWorkItems) continue;
       double us = large ? large_tiles_us(blocks, steps) : small_tiles_us(blocks, steps);
       if (split > 1) us += 4.0 + (double)M * (double)N * (8.0 * split + 2.0) / 4e6;
       take(us, Tiling{large != 0, !large && blocks <= 256, split, chunk, 0, 0, 0.0});
@@ -97,14 +97,17 @@ inline Tiling plan_tiles(int64_t M, int64_t N, int64_t K, bool dual, Cuts may) {
   const double steps = (double)per(K, 64);
   const int64_t tm = per(M, 256), bn = dual ? 128 : 256, tn = per(N, bn), rounds = tm * tn / 256;
   if (rounds > 0) {
+    auto fits = [](int64_t rest) { return rest * 512 < kMaxWorkItems; };
     const int64_t n = rounds * 256 / tm, m = may.m ? rounds * 256 / tn : 0;
     if (n > 0 && n < tn) {
       const int64_t rest = per(M, 128) * per(N - n * bn, bn / 2);
-      take(large_tiles_us(tm * n, steps) + 3.0 + small_tiles_us(rest, steps), Tiling{true, rest <= 256, 1, K, 0, n * bn, 0.0});
+      if (fits(rest))
+        take(large_tiles_us(tm * n, steps) + 3.0 + small_tiles_us(rest, steps), Tiling{true, rest <= 256, 1, K, 0, n * bn, 0.0});
     }
     if (m > 0 && m < tm) {
       const int64_t rest = per(M - m * 256, 128) * per(N, bn / 2);
-      take(large_tiles_us(m * tn, steps) + 3.0 + small_tiles_us(rest, steps), Tiling{true, rest <= 256, 1, K, m * 256, 0, 0.0});
+      if (fits(rest))
+        take(large_tiles_us(m * tn, steps) + 3.0 + small_tiles_us(rest, steps), Tiling{true, rest <= 256, 1, K, m * 256, 0, 0.0});
     }
   }
   return best;
@@ -228,6 +231,10 @@ inline XentPlan plan_xent(int64_t M, int64_t V, int64_t D, bool backward) {
   p.bytes = c.bytes;
   return p;
 }
+
+// Workgroups of 1024 that join the softmax statistics, 16 rows each at a time:
+// all of them up to 2^24 rows, which then take several.
+inline int64_t join_groups(int64_t M) { return per(M, 16) < (1 << 20) ? per(M, 16) : 1 << 20; }
 
 struct GatedCall {
   const uint16_t *x, *w, *dh;

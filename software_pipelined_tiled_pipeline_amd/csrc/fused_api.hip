@@ -8,7 +8,8 @@ namespace {
 
 using namespace pgemm;
 
-constexpr int64_t kMaxDim = (int64_t)1 << 31;
+// Below 2^31, and so are the rows of the last tile that lie past a matrix's end.
+constexpr int64_t kMaxDim = ((int64_t)1 << 31) - 255;
 // Widths that are a row pitch inside a product (D, 2 F, K): a tile's rows or
 // its 64 K rows then stay below 2^31 bytes, the reach of a buffer offset.
 constexpr int64_t kMaxPitch = (int64_t)1 << 22;
@@ -18,7 +19,8 @@ bool missing(const void *p, int64_t n) { return n > 0 && !p; }
 bool dim(int64_t n) { return n >= 0 && n < kMaxDim; }
 bool pitch(int64_t n) { return n >= 0 && n <= kMaxPitch; }
 // a product's grid, in work-items, fits a dispatch in large tiles of 256 x 128
-// columns or more (plan_tiles takes no cut that does not)
+// columns or more (plan_tiles takes no other cut that does not, and the other
+// kernels' grids are bounded where they are launched)
 bool grid_fits(int64_t M, int64_t N) { return per(M, 256) * per(N, 128) * 256 < kMaxWorkItems; }
 bool act_ok(int act) { return act == PGEMM_ACT_SILU || act == PGEMM_ACT_GELU; }
 
@@ -168,7 +170,7 @@ template <typename Launch>
 pgemm_status q4(Launch launch, const uint16_t *x, const uint8_t *q, const uint16_t *scale, const uint8_t *zero,
                 uint16_t *out, int64_t M, int64_t N, int64_t K, int64_t group, bool gated, int act, void *stream) {
   const int64_t rows = gated ? 2 * N : N;
-  if (!dim(M) || !dim(N) || !dim(rows) || !pitch(K) || group <= 0 || group % 32 != 0 || !dim(group) || !act_ok(act))
+  if (!dim(M) || !dim(N) || !dim(rows) || !pitch(K) || group <= 0 || group % 32 != 0 || group >= (int64_t)1 << 31 || !act_ok(act))
     return PGEMM_ERR_SHAPE;
   // tokens are the grid's second dimension, at least 16 a workgroup
   if (per(M, 16) > 65535 || per(N, 16) * 512 >= kMaxWorkItems) return PGEMM_ERR_SHAPE;

@@ -17,38 +17,43 @@ __global__ void __launch_bounds__(1024) lse_join_kernel(const float2 *__restrict
                                                         int64_t ignore) {
   __shared__ float tops[16][16], sums[16][16];
   const int r = threadIdx.x & 15, w = threadIdx.x >> 6;
-  const int64_t row = (int64_t)blockIdx.x * 16 + r;
-  float top = -INFINITY, sum = 0.0f;
+  float top, sum;
   auto join = [&](float t, float s) {
     const float m = fmaxf(top, t);
     const float ref = m == -INFINITY ? 0.0f : m;
     sum = sum * fast_exp(top - ref) + s * fast_exp(t - ref);
     top = m;
   };
-  if (row < M) {
+  for (int64_t row0 = (int64_t)blockIdx.x * 16; row0 < M; row0 += (int64_t)gridDim.x * 16) {
+    const int64_t row = row0 + r;
+    top = -INFINITY;
+    sum = 0.0f;
+    if (row < M) {
 #pragma unroll 4
-    for (int p = threadIdx.x >> 4; p < parts; p += 64) {
-      const float2 v = part[(int64_t)p * M + row];
-      join(v.x, v.y);
+      for (int p = threadIdx.x >> 4; p < parts; p += 64) {
+        const float2 v = part[(int64_t)p * M + row];
+        join(v.x, v.y);
+      }
     }
-  }
 #pragma unroll
-  for (int d = 16; d <= 32; d *= 2) {
-    const float t = __shfl_xor(top, d), s = __shfl_xor(sum, d);
-    join(t, s);
-  }
-  if ((threadIdx.x & 63) < 16) {
-    tops[w][r] = top;
-    sums[w][r] = sum;
-  }
-  __syncthreads();
-  if (threadIdx.x < 16 && row < M) {
+    for (int d = 16; d <= 32; d *= 2) {
+      const float t = __shfl_xor(top, d), s = __shfl_xor(sum, d);
+      join(t, s);
+    }
+    if ((threadIdx.x & 63) < 16) {
+      tops[w][r] = top;
+      sums[w][r] = sum;
+    }
+    __syncthreads();
+    if (threadIdx.x < 16 && row < M) {
 #pragma unroll
-    for (int p = 1; p < 16; ++p) join(tops[p][r], sums[p][r]);
-    const float l = top + logf(sum);
-    const int64_t t = target[row];
-    lse[row] = l;
-    loss[row] = t == ignore ? 0.0f : (t < 0 || t >= V) ? NAN : l - at[row];
+      for (int p = 1; p < 16; ++p) join(tops[p][r], sums[p][r]);
+      const float l = top + logf(sum);
+      const int64_t t = target[row];
+      lse[row] = l;
+      loss[row] = t == ignore ? 0.0f : (t < 0 || t >= V) ? NAN : l - at[row];
+    }
+    __syncthreads();  // the next rows' go to the same place
   }
 }
 
@@ -105,7 +110,7 @@ pgemm_status xent_forward(const XentCall &c) {
   st = launch_product<T, Lay::KC, Lay::KC, false, LseEpi>(g, p.logits, LseEpi::Args{part, at, c.target}, c.stream,
                                                           c.dev);
   if (st != PGEMM_OK) return st;
-  hipLaunchKernelGGL(lse_join_kernel<T>, dim3((unsigned)per(c.M, 16)), dim3(1024), 0, c.stream, part, at, c.target, c.loss,
+  hipLaunchKernelGGL(lse_join_kernel<T>, dim3((unsigned)join_groups(c.M)), dim3(1024), 0, c.stream, part, at, c.target, c.loss,
                      c.lse, c.M, c.V, (int)p.parts, c.ignore);
   return launched();
 }

@@ -38,3 +38,25 @@ def test_a_row_that_is_not_finite_leaves_the_rest(pg, fmt, size, poison):
     dx, dw = call(pg, fmt, "xent_bwd", one, x, w, target, lse)
     check("dx", dx, want["dx"])
     check("dw", dw, want["dw"])
+
+
+def test_more_rows_than_one_join_of_a_dispatch(pg):
+    # 2^26 rows and a few: some of them in every turn of the statistics' join
+    M, V, D = (1 << 26) + 5, 10, 8
+    gen = torch.Generator(device="cuda").manual_seed(51)
+    x = torch.randn(M, D, generator=gen, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(V, D, generator=gen, device="cuda", dtype=torch.bfloat16)
+    target = torch.randint(0, V, (M,), generator=gen, device="cuda")
+    rows = torch.cat([torch.arange(20), (1 << 24) + torch.arange(-20, 20), torch.randint(0, M, (2000,)),
+                      (1 << 26) + torch.arange(-20, 5)]).cuda()
+    one = torch.ones((), device="cuda")
+    want = ref.xent(x[rows], w, target[rows], dloss=one)
+    loss, lse = pg.pgemm_bf16_xent(x, w, target)
+    check("lse", lse[rows], want["lse"])
+    check("loss", loss[rows], want["loss"])
+    dx, dw = pg.pgemm_bf16_xent_bwd(one, x, w, target, lse)
+    check("dx", dx[rows], want["dx"])
+    assert dw.isfinite().all()
+    del x, target, loss, lse, dx
+    pg.release_workspace()
+    torch.cuda.empty_cache()
