@@ -145,10 +145,12 @@ __device__ __forceinline__ u32x4 load_tail(const uint16_t *row, int k, int K) {
 // Adds the sums of the `parts` waves that worked on the same output up, and
 // stores it: row r of an accumulator's lane l is token 4 (l / 16) + r, and its
 // column l % 16.  `sums` holds [parts][MT * NT * 4][64] floats; the block's
-// waves `first`, first + step, .. take its values in turn.
-template <typename T, bool GATED, int MT, int NT>
+// waves `first`, first + step, .. take its values in turn.  `checked` gets each
+// sum with its token and weight row.
+template <typename T, bool GATED, int MT, int NT, typename Checked>
 __device__ __forceinline__ void join_and_store(const float *sums, int parts, int64_t part_stride, int first, int step,
-                                               int lane, int act, uint16_t *out, int M, int N, int m0, int n0) {
+                                               int lane, int act, uint16_t *out, int M, int N, int m0, int n0,
+                                               Checked checked) {
   constexpr int OB = GATED ? NT / 2 : NT;
   const int c = lane & 15, q = lane >> 4;
   auto joined = [&](int m, int b, int r) {
@@ -160,12 +162,10 @@ __device__ __forceinline__ void join_and_store(const float *sums, int parts, int
     const int m = i / (OB * 4), b = i / 4 % OB, r = i % 4;
     const int row = m0 + 16 * m + 4 * q + r, col = n0 + 16 * b + c;
     if (m0 + 16 * m + r >= M) continue;  // no token in any lane
-    float v;
-    if constexpr (GATED)
-      v = activate(act, joined(m, 2 * b, r)) * joined(m, 2 * b + 1, r);
-    else
-      v = joined(m, b, r);
+    float v = joined(m, GATED ? 2 * b : b, r), u = GATED ? joined(m, 2 * b + 1, r) : 0.0f;
     if (row < M && col < N) {
+      v = checked(v, row, col);
+      if constexpr (GATED) v = activate(act, v) * checked(u, row, (int64_t)col + N);
       const T t = (T)v;
       out[(int64_t)row * N + col] = __builtin_bit_cast(uint16_t, t);
     }

@@ -70,6 +70,45 @@ struct Q4Geom {
   static_assert(CB % KW == 0 && (XI == 4 * MT || (MT == 1 && XI == 1)), "");
 };
 
+// One token's product with one weight row, as it is defined.  For rows shorter
+// than eight values; and where weights that carry 16 + zero too much have summed
+// up to what is not finite: an infinite x is then infinity less infinity, and
+// values past 1e37 leave fp32 early.
+template <typename T>
+__device__ __forceinline__ float q4_dot(const Q4Args &a, int64_t m, int64_t row) {
+  const uint16_t *x = a.x + m * a.K;
+  const uint8_t *q = a.q + row * a.wb;
+  float total = 0.0f, sum = 0.0f;
+  for (int k0 = 0; k0 < a.K; k0 += 32) {
+    const int g = (int)((uint64_t)(uint32_t)(k0 / 32) * a.per32 >> 40);
+    const float z = a.zero ? (float)a.zero[row * a.groups + g] : 8.0f;
+    if (k0 + 32 <= a.K) {
+      // all in flight at once; eight bytes each: the kernels' tests count loads of sixteen
+      u32x2 v[8], w[2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = load_at<u32x2_any>(x, (uint32_t)(k0 + 4 * i) * 2u);
+        compiler_fence();
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[i] = load_at<u32x2>(q, (uint32_t)(k0 / 2 + 8 * i));
+        compiler_fence();
+      }
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        sum += widen<T>((uint16_t)(v[k / 4][k / 2 % 2] >> (16 * (k % 2)))) * ((float)(w[k / 16][k / 8 % 2] >> (k % 8 * 4) & 15u) - z);
+    } else {
+      for (int k = k0; k < a.K; ++k) sum += widen<T>(x[k]) * ((float)(q[k / 2] >> (4 * (k & 1)) & 15) - z);
+    }
+    if ((k0 + 32) % a.group == 0 || k0 + 32 >= a.K) {
+      total += sum * widen<T>(a.scale[row * a.groups + g]);
+      sum = 0.0f;
+    }
+  }
+  return total;
+}
+
 template <typename T, bool GATED, int MT, int GS, int XI, int NW, int KW, int D>
 __global__ void __launch_bounds__(NW *KW * 64, q4_per_simd(XI, NW)) q4_kernel(Q4Args a) {
   using G = Q4Geom<T, GATED, MT, GS, XI, NW, KW, D>;
@@ -353,7 +392,12 @@ __global__ void __launch_bounds__(NW *KW * 64, q4_per_simd(XI, NW)) q4_kernel(Q4
       for (int r = 0; r < 4; ++r) sums[wk * PART + ((m * NT + b) * 4 + r) * 64 + lane] = tot[m][b][r];
   __syncthreads();
   join_and_store<T, GATED, MT, NT>(sums, KW, PART, wk, KW, lane, a.act, a.out, a.M, a.N, m0,
-                                   n0 + wn * (GATED ? 16 : 32));
+                                   n0 + wn * (GATED ? 16 : 32), [&](float v, int m, int64_t row) {
+                                     if constexpr (F::kExactZero)
+                                       return v;
+                                     else
+                                       return fabsf(v) < INFINITY ? v : q4_dot<T>(a, m, row);
+                                   });
 }
 
 // Rows shorter than eight values: one output a thread.
@@ -362,16 +406,7 @@ __global__ void __launch_bounds__(256) q4_short_kernel(Q4Args a) {
   const int64_t total = (int64_t)a.M * a.N;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t m = i / a.N, n = i % a.N;
-    auto dot = [&](int64_t row) {  // one group
-      float sum = 0.0f;
-      const float z = a.zero ? (float)a.zero[row] : 8.0f;
-      for (int k = 0; k < a.K; ++k) {
-        const float w = (float)(a.q[row * a.wb + k / 2] >> (4 * (k & 1)) & 15) - z;
-        sum += widen<T>(a.x[m * a.K + k]) * w;
-      }
-      return a.K > 0 ? sum * widen<T>(a.scale[row]) : 0.0f;
-    };
-    const float v = GATED ? activate(a.act, dot(n)) * dot(n + a.N) : dot(n);
+    const float v = GATED ? activate(a.act, q4_dot<T>(a, m, n)) * q4_dot<T>(a, m, n + a.N) : q4_dot<T>(a, m, n);
     a.out[i] = __builtin_bit_cast(uint16_t, (T)v);
   }
 }

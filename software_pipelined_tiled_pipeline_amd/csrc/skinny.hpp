@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(WAVES * 64) skinny_kernel(SkinnyArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) sums[(wave * VALS + (m * NT + b) * 4 + r) * 64 + lane] = job.tot[m][b][r];
   __syncthreads();
-  join_and_store<T, GATED, MT, NT>(sums, WAVES, VALS * 64, wave, WAVES, lane, a.act, a.out, a.M, a.N, m0, n0);
+  join_and_store<T, GATED, MT, NT>(sums, WAVES, VALS * 64, wave, WAVES, lane, a.act, a.out, a.M, a.N, m0, n0,
+                                     [](float v, int, int64_t) { return v; });
 }
 
 }  // namespace pgemm
