@@ -197,7 +197,7 @@ pgemm_status gated_forward(const GatedCall &c) {
     a.N = (int)c.F;
     a.K = (int)c.D;
     a.act = c.act;
-    return launch_skinny<T, true>(a, c.stream, c.dev);
+    return launch_skinny<T>(a, c.stream);
   }
   const uint16_t *x, *w;
   pgemm_status st = gated_operands<T>(c, p, &x, &w);

@@ -1,7 +1,7 @@
-// Products with few rows (tokens) and 16-bit weights: out = x W^T, or the gated
-// block act(x Wg^T) * (x Wu^T), bound by reading the weights once.
+// The gated block act(x Wg^T) * (x Wu^T) for few rows (tokens) and 16-bit weights,
+// bound by reading the weights once.
 //
-// A workgroup owns NT blocks of 16 weight rows and all of K; its waves take
+// A workgroup owns 16 gate rows, the same 16 up rows and all of K; its waves take
 // blocks of 128 k in turn, so that a weight row's loads are in flight on
 // several waves at once, and add their sums up in LDS at the end.  Weights are
 // not staged in LDS: four lanes load 64 bytes of a row, so that a load is 16
@@ -22,9 +22,9 @@ namespace pgemm {
 
 struct SkinnyArgs {
   const uint16_t *x;  // [M][K]
-  const uint16_t *w;  // [rows][K]
+  const uint16_t *w;  // [2 N][K]
   uint16_t *out;      // [M][N]
-  int M, N, K;        // N output columns; the gated block has 2 N weight rows
+  int M, N, K;
   int act;
 };
 
@@ -42,9 +42,10 @@ __device__ __forceinline__ u32x4 to_rows(u32x4 v, int from) {
 // block that K ends in is left to one wave's guarded loads after the loop.
 // Addresses are a base that is the same for the wave and moves along K, and a
 // lane's offset of 32 bits.
-template <typename T, int MT, int NT>
+template <typename T, int MT>
 struct SkinnyRun {
   using F = Frag8<T>;
+  static constexpr int NT = 2;                // blocks of weight rows: gate, up
   static constexpr int XD = MT == 1 ? 4 : 2;  // steps that x is loaded ahead
 
   const SkinnyArgs &a;
@@ -61,7 +62,7 @@ struct SkinnyRun {
     return (uint32_t)((row0 + r < rows ? row0 + r : rows - 1) - (row0 < rows ? row0 : rows - 1)) * pitch;
   }
 
-  __device__ __forceinline__ void init(int lane, int m0, int n0, bool gated) {
+  __device__ __forceinline__ void init(int lane, int m0, int n0) {
     const uint32_t pitch = (uint32_t)a.K * 2u;
     from = (4 * (lane & 15) + (lane >> 4)) * 4;
 #pragma unroll
@@ -72,10 +73,8 @@ struct SkinnyRun {
     }
 #pragma unroll
     for (int b = 0; b < NT; ++b) {
-      const int row0 = n0 + (gated ? b / 2 : b) * 16;
-      wbase[b] = reinterpret_cast<const char *>(a.w) +
-                 ((row0 < a.N ? row0 : a.N - 1) + (gated && (b & 1) ? (int64_t)a.N : 0)) * pitch;
-      woff[b] = row_offset(row0, lane >> 2, a.N, pitch) + 16u * (lane & 3);
+      wbase[b] = reinterpret_cast<const char *>(a.w) + ((n0 < a.N ? n0 : a.N - 1) + (int64_t)b * a.N) * pitch;
+      woff[b] = row_offset(n0, lane >> 2, a.N, pitch) + 16u * (lane & 3);
     }
   }
 
@@ -113,8 +112,7 @@ struct SkinnyRun {
 
   // Places first, first + step, .. below `full` in the order of blocks that
   // starts at `turn`, and the block that K ends in if it is `tail`.
-  __device__ __forceinline__ void run(int lane, int m0, int n0, bool gated, int first, int step, int full, int turn,
-                                      bool tail) {
+  __device__ __forceinline__ void run(int lane, int m0, int n0, int first, int step, int full, int turn, bool tail) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -146,8 +144,7 @@ struct SkinnyRun {
         x[m] = load_tail(reinterpret_cast<const uint16_t *>(xbase[m] + row_offset(m0 + 16 * m, c, a.M, pitch)), k, a.K);
 #pragma unroll
       for (int b = 0; b < NT; ++b) {
-        const u32x4 f = load_tail(
-            reinterpret_cast<const uint16_t *>(wbase[b] + row_offset(n0 + (gated ? b / 2 : b) * 16, c, a.N, pitch)), k, a.K);
+        const u32x4 f = load_tail(reinterpret_cast<const uint16_t *>(wbase[b] + row_offset(n0, c, a.N, pitch)), k, a.K);
 #pragma unroll
         for (int m = 0; m < MT; ++m) tot[m][b] = F::mma(x[m], f, tot[m][b]);
       }
@@ -155,20 +152,20 @@ struct SkinnyRun {
   }
 };
 
-template <typename T, bool GATED, int MT, int NT, int WAVES>
+template <typename T, int MT, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64) skinny_kernel(SkinnyArgs a) {
-  static_assert(!GATED || NT % 2 == 0, "gate and up blocks come in pairs");
+  constexpr int NT = SkinnyRun<T, MT>::NT;
   extern __shared__ __attribute__((aligned(16))) float sums[];  // [WAVES][MT * NT * 4][64]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * (GATED ? NT / 2 : NT) * 16, m0 = blockIdx.y * MT * 16;
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * MT * 16;
 
-  SkinnyRun<T, MT, NT> job(a);
-  job.init(lane, m0, n0, GATED);
+  SkinnyRun<T, MT> job(a);
+  job.init(lane, m0, n0);
   const int full = a.K / 128;
   // Each workgroup starts at another block: rows are often a multiple of the
   // memory channels' interleave apart, and all would meet on the same few.
   const int turn = full > 0 ? (int)((blockIdx.x * 0x9E3779B1u >> 12) % (unsigned)full) : 0;
-  job.run(lane, m0, n0, GATED, wave, WAVES, full, turn, a.K % 128 != 0 && wave == full % WAVES);
+  job.run(lane, m0, n0, wave, WAVES, full, turn, a.K % 128 != 0 && wave == full % WAVES);
   constexpr int VALS = MT * NT * 4;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -177,8 +174,8 @@ __global__ void __launch_bounds__(WAVES * 64) skinny_kernel(SkinnyArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) sums[(wave * VALS + (m * NT + b) * 4 + r) * 64 + lane] = job.tot[m][b][r];
   __syncthreads();
-  join_and_store<T, GATED, MT, NT>(sums, WAVES, VALS * 64, wave, WAVES, lane, a.act, a.out, a.M, a.N, m0, n0,
-                                     [](float v, int, int64_t) { return v; });
+  join_and_store<T, true, MT, NT>(sums, WAVES, VALS * 64, wave, WAVES, lane, a.act, a.out, a.M, a.N, m0, n0,
+                                  [](float v, int, int64_t) { return v; });
 }
 
 }  // namespace pgemm

@@ -1,4 +1,4 @@
-// Launch templates of the products with few rows.
+// Launch templates of the gated block with few rows.
 #pragma once
 
 #include "fused_launch.hpp"
@@ -7,36 +7,30 @@
 namespace pgemm {
 namespace launch_detail {
 
-template <typename T, bool GATED, int MT, int NT, int WAVES>
-pgemm_status launch_skinny_one(const SkinnyArgs &a, hipStream_t stream, int dev) {
-  static std::atomic<uint64_t> lds_set{0};
-  constexpr int LDS = WAVES * MT * NT * 4 * 64 * 4;
-  auto kern = skinny_kernel<T, GATED, MT, NT, WAVES>;
-  if (LDS > 65536) {
-    pgemm_status st = allow_lds(kern, LDS, dev, lds_set);
-    if (st != PGEMM_OK) return st;
-  }
-  constexpr int cols = (GATED ? NT / 2 : NT) * 16;
-  hipLaunchKernelGGL(kern, dim3((unsigned)per(a.N, cols), (unsigned)per(a.M, 16 * MT)), dim3(WAVES * 64), LDS, stream,
-                     a);
+template <typename T, int MT, int WAVES>
+pgemm_status launch_skinny_one(const SkinnyArgs &a, hipStream_t stream) {
+  constexpr int LDS = WAVES * MT * SkinnyRun<T, MT>::NT * 4 * 64 * 4;
+  static_assert(LDS <= 65536, "what a kernel may use without asking");
+  auto kern = skinny_kernel<T, MT, WAVES>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)per(a.N, 16), (unsigned)per(a.M, 16 * MT)), dim3(WAVES * 64), LDS, stream, a);
   return launched();
 }
 
 // Waves along K: so many that all workgroups together give each CU about
 // sixteen.
-template <typename T, bool GATED, int MT>
-pgemm_status launch_skinny_waves(const SkinnyArgs &a, hipStream_t stream, int dev) {
-  const int64_t groups = per(a.N, GATED ? 16 : 32) * per(a.M, 16 * MT);
-  if (groups <= 512) return launch_skinny_one<T, GATED, MT, 2, 8>(a, stream, dev);
-  return launch_skinny_one<T, GATED, MT, 2, 4>(a, stream, dev);
+template <typename T, int MT>
+pgemm_status launch_skinny_waves(const SkinnyArgs &a, hipStream_t stream) {
+  const int64_t groups = per(a.N, 16) * per(a.M, 16 * MT);
+  if (groups <= 512) return launch_skinny_one<T, MT, 8>(a, stream);
+  return launch_skinny_one<T, MT, 4>(a, stream);
 }
 
 // Token blocks of 16 a workgroup takes: as many as there are, up to four.
-template <typename T, bool GATED>
-pgemm_status launch_skinny(const SkinnyArgs &a, hipStream_t stream, int dev) {
-  if (a.M <= 16) return launch_skinny_waves<T, GATED, 1>(a, stream, dev);
-  if (a.M <= 32) return launch_skinny_waves<T, GATED, 2>(a, stream, dev);
-  return launch_skinny_waves<T, GATED, 4>(a, stream, dev);
+template <typename T>
+pgemm_status launch_skinny(const SkinnyArgs &a, hipStream_t stream) {
+  if (a.M <= 16) return launch_skinny_waves<T, 1>(a, stream);
+  if (a.M <= 32) return launch_skinny_waves<T, 2>(a, stream);
+  return launch_skinny_waves<T, 4>(a, stream);
 }
 
 }  // namespace launch_detail
