@@ -356,7 +356,7 @@ pgemm_status pgemm_bf16_gated_bwd(const uint16_t *dh, const uint16_t *x, const u
  *   x: [M, D]; w: [V, D], V >= 1; target: int64 [M]; loss, lse: fp32 [M].
  *   A target equal to ignore_index does not count: its loss is 0 and it adds
  *   nothing to the gradients.  Any other target outside 0 .. V-1 makes its
- *   loss NaN, and every gradient that it reaches.
+ *   loss NaN, and every gradient that it reaches (where its dloss is not 0).
  */
 pgemm_status pgemm_f16_xent(const uint16_t *x, const uint16_t *w, const int64_t *target, float *loss, float *lse,
                             int64_t M, int64_t V, int64_t D, int64_t ignore_index, void *stream);
@@ -367,7 +367,8 @@ pgemm_status pgemm_bf16_xent(const uint16_t *x, const uint16_t *w, const int64_t
  * Its gradients: dx [M, D] and dw [V, D] for dloss, fp32 [M] (dloss_step 1)
  * or one value that all rows share (dloss_step 0), 4-byte aligned.  lse: from
  * the forward call.  The logits are computed again in pieces of the
- * vocabulary.  dloss = 0 gives a row no gradient whatever its logits are.
+ * vocabulary.  dloss = 0 gives a row no gradient, whatever its logits and its
+ * target are.
  * A row that is ignored or whose dloss is 0 adds 0 times its x to dw: infinities
  * and NaN in that x still reach dw's columns, as they do in any product.
  */

@@ -430,7 +430,7 @@ struct LseEpi {
 
 // The loss's derivative by a tile of logits, dz = s (e^(z - lse) - [v = t])
 // with s = kDzUnit dloss / *top (0 for an ignored row, NaN for a target
-// outside the vocabulary), rounded to T; the products after it multiply by
+// outside the vocabulary whose dloss is not 0), rounded to T; the products after it multiply by
 // *top / kDzUnit again.  *top is the largest |dloss|: with the usual dloss, the
 // same for all rows, s is a power of two and an improbable target's entry,
 // close to -s, rounds to next to nothing, where -dloss itself would give
@@ -473,7 +473,7 @@ struct SlopeEpi {
 #pragma unroll
       for (int i = 0; i < W::TM; ++i) {
         const int64_t t = target[i];
-        const float s = t == e.ignore ? 0.0f : (t < 0 || t >= e.V) ? NAN : dloss[i] / top * kDzUnit<T>;
+        const float s = t == e.ignore || dloss[i] == 0.0f ? 0.0f : (t < 0 || t >= e.V) ? NAN : dloss[i] / top * kDzUnit<T>;
         const uint32_t keep = s == 0.0f ? 0u : ~0u;  // an ignored row is zero whatever its logits are
         const float off = lse[i] * kLog2e;
         RowLogits<G, W> z(w, i, edge, c0, g.N);

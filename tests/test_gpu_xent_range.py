@@ -40,6 +40,23 @@ def test_a_row_that_is_not_finite_leaves_the_rest(pg, fmt, size, poison):
     check("dw", dw, want["dw"])
 
 
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+def test_no_gradient_where_dloss_is_zero(pg, fmt):
+    # whatever the row's target is; its loss says that it is none of the vocabulary's
+    M, V, D = 130, 500, 64
+    x, w, target, dloss = head(52, fmt, M, V, D)
+    dloss[17], dloss[18] = 0.0, -0.0
+    want = None
+    for wrong in (3, -1, V, 1 << 40):
+        target[17:19] = wrong
+        loss, lse = call(pg, fmt, "xent", x, w, target)
+        assert loss[17:19].isnan().all() == (wrong != 3) and loss.isnan().sum() == (0 if wrong == 3 else 2)
+        got = call(pg, fmt, "xent_bwd", dloss, x, w, target, lse)
+        assert not got[0][17:19].any()
+        want = want or got
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_more_rows_than_one_join_of_a_dispatch(pg):
     # 2^26 rows and a few: some of them in every turn of the statistics' join
     M, V, D = (1 << 26) + 5, 10, 8
