@@ -388,7 +388,7 @@ pgemm_status pgemm_bf16_xent_bwd(const float *dloss, int dloss_step, const uint1
  *   shape, or NULL for 8 everywhere; group: a multiple of 32; out: [M, N].
  *   Weights enter the products as exact integers; each group's fp32 sum is
  *   scaled in fp32.  The call suits few rows: the weights are read once per
- *   64 of them.
+ *   16 to 64 of them.
  */
 pgemm_status pgemm_f16_q4(const uint16_t *x, const uint8_t *q, const uint16_t *scale, const uint8_t *zero,
                           uint16_t *out, int64_t M, int64_t N, int64_t K, int64_t group, void *stream);

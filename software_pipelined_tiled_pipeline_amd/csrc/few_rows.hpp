@@ -20,7 +20,9 @@ __device__ __forceinline__ uint32_t vector_constant(uint32_t v) {
 // MFMA fragments of eight values, and how eight 4-bit weights (a dword, the
 // first in the lowest bits) become one.  A pair of weights j and j + 4 is cut
 // out of both halves of the dword at once and put into the fraction of a power
-// of two; the fragment's order is 0 4 1 5 2 6 3 7.
+// of two; the fragment's order is 0 4 1 5 2 6 3 7.  (Integers made floating point in
+// this way: Y. J. Kim et al., "Who Says Elephants Can't Run: Bringing Large Scale
+// MoE Models into Cloud Scale Production", 2022.)
 template <typename T>
 struct Frag8;
 template <>

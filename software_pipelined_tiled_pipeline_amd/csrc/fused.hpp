@@ -36,7 +36,10 @@ struct Carver {
 //   large, one to a CU:         1.5 a K tile and 12 to fill and store
 //   small, deep, one to a CU:   0.45 and 6
 //   small, two to a CU:         1.0 and 9 (0.72 and 7 for one left over)
-// so a large tile has the work of four small ones for less than the time of
+// with K along the rows of both operands.  With K down the rows of one, 256 deep
+// tiles take 0.60 a K tile in 86 of them and 0.63 to 0.73 in 196, which the cut
+// does not go by: such long products may be better off in pieces of large tiles.
+// By these, a large tile has the work of four small ones for less than the time of
 // four, but leaves CUs idle when there are fewer than 256, or few more than a
 // multiple.  Pieces cost a second launch (4) and their sums' way to memory and
 // back (4 MB a microsecond).  Examples: 2048 x 2048 x 4096 takes 39 us in 256

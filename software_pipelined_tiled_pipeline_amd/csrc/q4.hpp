@@ -5,9 +5,9 @@
 //
 // Bound by reading the weights once: two of them are a byte, so what a byte
 // costs elsewhere counts four times as much as with 16-bit weights.  A lane
-// that loaded its own weight row's bytes, as the 16-bit kernel does, would
-// make every lane of a load a request of its own, and the address unit, not
-// the memory, would set the pace.  So weights come in whole lines:
+// that loads its own weight row's bytes makes every lane of a load a request of
+// its own, about 50 a load: 24.6 us instead of 10 at 8192 x 8192.  So weights come
+// in whole lines:
 //
 //  * weights: a wave's blocks of 32 weight rows and 128 k (2 KiB) go straight
 //    into a ring of D slots in LDS, four lanes to a row's 64 bytes, and are
@@ -26,12 +26,14 @@
 // 72 (f16) or 56 (bf16) of them, a group's sums times its scale four for every
 // 16 tokens and 16 weight rows; all of it is 170 to 380 for a block, beside 12
 // to 40 MFMAs.  That is why what bf16 weights carry too much is taken off by
-// MFMAs (48 x 4096 x 12288 gated, groups of 32, 37.5 us, and 43.6 with a vector
-// instruction for each accumulator) and why scales are loaded four at a time
-// (one at a time took 80 of 480 instructions).  Deeper rings (three and four
-// slots for more than four tokens) changed nothing.  Measured, with weights of
-// two calls in turn: one token at 8192 x 8192 10.1 us (3.5 TB/s); 48 x 4096 x
-// 12288 gated in groups of 32 31.6 us in bf16, 26 in f16.
+// MFMAs (48 x 4096 x 12288 gated, groups of 32, went from 43.6 us with a vector
+// instruction for each accumulator to 37.5) and why scales are loaded four at a
+// time (one at a time took 80 of 480 instructions).  Deeper rings (three and four
+// slots for more than four tokens) changed nothing.  Measured with the weights
+// of two calls in turn, which the last-level cache holds, and with those of so
+// many that it does not: one token at 8192 x 8192 10.1 and 11.7 us (3.5 and 3.0
+// TB/s); 48 x 4096 x 12288 gated in groups of 32 28.1 and 31.1 us in bf16, 25.2 in
+// f16 with two.
 #pragma once
 
 #include "few_rows.hpp"

@@ -27,8 +27,9 @@ pgemm_status launch_q4_one(Q4Args a, hipStream_t stream, int dev) {
   return launched();
 }
 
-// Waves along K, with 16 tokens a workgroup: so many that all workgroups together give
-// each CU about sixteen.
+// Waves along K, with up to 4 tokens: so many that all workgroups together give each CU
+// about sixteen.  With 5 to 16 tokens a workgroup has eight waves up to 256
+// workgroups and four beyond, so that a CU has 4 to 8 waves between 257 and 512 of them.
 template <typename T, bool GATED, int GS>
 pgemm_status launch_q4(const Q4Args &a, hipStream_t stream, int dev) {
   const int64_t groups = per(a.N, GATED ? 16 : 32);
@@ -40,9 +41,9 @@ pgemm_status launch_q4(const Q4Args &a, hipStream_t stream, int dev) {
   // More than 16 tokens: 16 of them a workgroup, which reads weights again for
   // every 16 but has no wave wait for another, or up to 64 shared by two, three
   // or four waves beside each other, whose workgroup fills a CU.  The costs are
-  // of a round of 256 workgroups, in tenths of a microsecond at K 4096.  Groups
-  // of 64, bf16, K 4096, microseconds with 16 tokens a workgroup, two waves, and
-  // three (M 32 and 48) or four (M 64):
+  // of a round of 256 workgroups, in tenths of a microsecond, measured at K 4096 in
+  // groups of 64 in bf16; they decide for every K, group and type.  Microseconds
+  // there with 16 tokens a workgroup, two waves, and three (M 32 and 48) or four (M 64):
   //   N          4480             12288            16384            24576            49152
   //   M 32   10.3 14.8 18.4   14.9 16.1 19.6   19.1 16.9 19.8   26.9 29.7 20.6   50.7 43.7 38.4
   //   M 48   10.6 18.8 23.9   22.0 20.4 24.8   27.7 21.3 25.5   39.6 37.1 26.0   72.6 55.0 49.5

@@ -10,9 +10,9 @@
 // them, those past M repeat the last one) as the other operand:
 //   lane l, register r of an accumulator: token 4 (l / 16) + r, weight row l % 16.
 //
-// One token at 4096 x 12288 gated takes 34.6 us, 5.8 TB/s.  With one row a lane,
-// each a request of its own, the address unit set the pace: 18 tokens at 421 x
-// 3264 12.7 us, 7.4 in whole lines.  More tokens read x again for every 32 weight
+// One token at 4096 x 12288 gated takes 34.6 us, 5.8 TB/s, also where no cache
+// holds the weights.  With one row a lane, each a request of its own, 18 tokens at
+// 421 x 3264 took 12.7 us, 7.4 in whole lines.  More tokens read x again for every 32 weight
 // rows, and from about 64 on tiles take less (few_rows_us).
 #pragma once
 

@@ -5,6 +5,12 @@ The functions are reached through :mod:`pgemm`, next to the products:
 ``_q4`` and ``_q4_gated``.  Tensors live on the current GPU; every function also
 takes a ``stream`` to run on.  What a call needs as workspace is a torch tensor
 on the call's stream, registered there and kept for later calls.  All arithmetic runs in the library's kernels.
+
+Like the products, the functions are not part of torch's autograd: what they
+return carries no graph, also where an operand requires gradients.  Each forward
+call has its backward call, and examples/gated_lm.py joins them in
+torch.autograd.Function.  With a `stream` of its own, a call's operands have to be
+ready on that stream and to live until it has read them.
 """
 from __future__ import annotations
 
