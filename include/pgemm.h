@@ -402,6 +402,108 @@ pgemm_status pgemm_f16_q4_gated(const uint16_t *x, const uint8_t *q, const uint1
 pgemm_status pgemm_bf16_q4_gated(const uint16_t *x, const uint8_t *q, const uint16_t *scale, const uint8_t *zero,
                                  uint16_t *out, int64_t M, int64_t F, int64_t K, int64_t group, int act, void *stream);
 
+/*
+ * Serving operators: what a model's tokens pass on their way to the next one.
+ * The fused operators' rules hold here too.
+ */
+
+/*
+ * Rows of 16-bit values as 8-bit integers with a scale for each row:
+ *     scale[m] = max(max_k |x[m, k]| / 127, 2^-126),   q[m, k] = x[m, k] / scale[m]
+ *   rounded to the nearest integer, halves to the even one (of the quotient by
+ *   the scale as it is stored).  x: [M, K]; q: [M, B] bytes, B = 16 ceil(K / 16),
+ *   a row's last bytes zeros; scale: fp32 [M].  A row that holds an infinity or
+ *   a NaN gets the scale NaN and zeros.  K at most 2^22.
+ */
+pgemm_status pgemm_f16_quant_i8(const uint16_t *x, int8_t *q, float *scale, int64_t M, int64_t K, void *stream);
+pgemm_status pgemm_bf16_quant_i8(const uint16_t *x, int8_t *q, float *scale, int64_t M, int64_t K, void *stream);
+
+/*
+ * Products of 8-bit integers with a scale for each token and each weight row:
+ *     out[m, n] = xs[m] * ws[n] * sum over k of x[m, k] w[n, k]
+ *   w: [N, B] and ws: fp32 [N] as pgemm_*_quant_i8 gives them.  xs not NULL: x
+ *   is [M, B] integers with the scales xs, fp32 [M]; the sum is over all B
+ *   bytes of a row, so that those past K are zero in one of the two.  xs NULL:
+ *   x is [M, K] of the 16-bit type, and the call makes integers of its rows
+ *   first, as pgemm_*_quant_i8 does.  out: [M, N] of the 16-bit type.
+ *   The integers' sum is exact (K at most 2^17 - 16); it is rounded to fp32,
+ *   scaled, and rounded to the type.
+ */
+pgemm_status pgemm_f16_i8(const void *x, const float *xs, const int8_t *w, const float *ws, uint16_t *out, int64_t M,
+                          int64_t N, int64_t K, void *stream);
+pgemm_status pgemm_bf16_i8(const void *x, const float *xs, const int8_t *w, const float *ws, uint16_t *out, int64_t M,
+                           int64_t N, int64_t K, void *stream);
+
+/* The gated block on 8-bit weights: w and ws have 2 F rows, the gate rows
+ * first; out: [M, F]; act: a pgemm_act. */
+pgemm_status pgemm_f16_i8_gated(const void *x, const float *xs, const int8_t *w, const float *ws, uint16_t *out, int64_t M,
+                                int64_t F, int64_t K, int act, void *stream);
+pgemm_status pgemm_bf16_i8_gated(const void *x, const float *xs, const int8_t *w, const float *ws, uint16_t *out,
+                                 int64_t M, int64_t F, int64_t K, int act, void *stream);
+
+/* Bytes of workspace of an 8-bit product; quantized: the call has xs. */
+pgemm_status pgemm_i8_workspace(int64_t M, int64_t N, int64_t K, int gated, int quantized, int64_t *bytes);
+
+/*
+ * A mixture-of-experts layer for few tokens: the router, the chosen experts'
+ * gated blocks, their second products and the weighted sum:
+ *     l = x R^T,   e_1 .. e_top_k: the experts of the largest l, the lowest
+ *                  index of equal ones first,
+ *     p_j = e^l[e_j] / Z,   y = sum over j of p_j W2[e_j] (a(Wg[e_j] x) * (Wu[e_j] x))
+ *   with Z the sum of e^l over the chosen experts (normalize 1) or over all of
+ *   them (normalize 0).  x: [M, D]; router: [E, D]; w: [E, 2 F, D], an expert's
+ *   F gate rows and then its F up rows; down: [E, D, F]; y: [M, D]; experts:
+ *   int32 [M, top_k] and weights: fp32 [M, top_k], what was chosen and p, each
+ *   may be NULL; act: a pgemm_act.
+ *   The logits are sums in 64 bits, so that the choice does not depend on
+ *   their order.  The products of the gated block are fp32; its values are
+ *   rounded to the 16-bit type for the second product, in f16 after a power
+ *   of two that keeps them in its range.  An expert that a token does not
+ *   choose has no part in its result, whatever its weights hold.  A logit that
+ *   is NaN comes last.
+ *   E at most 1024, top_k at most 32 and E, M below 32768, D and 2 F at most
+ *   2^22.  Weights are read once for every 64 tokens that reach their expert.
+ */
+pgemm_status pgemm_f16_moe(const uint16_t *x, const uint16_t *router, const uint16_t *w, const uint16_t *down, uint16_t *y,
+                           int32_t *experts, float *weights, int64_t M, int64_t E, int64_t D, int64_t F, int64_t top_k,
+                           int normalize, int act, void *stream);
+pgemm_status pgemm_bf16_moe(const uint16_t *x, const uint16_t *router, const uint16_t *w, const uint16_t *down,
+                            uint16_t *y, int32_t *experts, float *weights, int64_t M, int64_t E, int64_t D, int64_t F,
+                            int64_t top_k, int normalize, int act, void *stream);
+
+/* Bytes of workspace of a mixture-of-experts layer. */
+pgemm_status pgemm_moe_workspace(int64_t M, int64_t E, int64_t D, int64_t F, int64_t top_k, int64_t *bytes);
+
+/*
+ * One token for each row of logits z [M, V], from given random numbers u,
+ * fp32 [M] in [0, 1).  A row's tokens in order, the largest logit first and
+ * the lowest index of equal ones, have the shares e^((z - z_1) / temperature).
+ * Kept are the first top_k (0 or less: all), of these the fewest whose shares
+ * reach top_p of their sum (1 or more: all), and of these the ones whose share
+ * is at least min_p of the first one's (0 or less: all); the first always.
+ * The token is the first whose running sum exceeds u times the kept ones' sum
+ * (the last kept where u is 1 or more).  Temperature 0 takes the first.
+ *   temperature, top_p, min_p: fp32, top_k: int32; [M] values, or one for all
+ *   rows where `shared` has its bit, or NULL (temperature 1, the others off);
+ *   4-byte aligned, as u.  token: int64 [M].
+ *   Shares and sums are in 64 bits.  Minus infinity is never taken.  A row
+ *   that has nothing else, or a NaN in its logits, settings or u, or a
+ *   temperature below 0, gets -1.  V at most 2^30.
+ */
+typedef enum {
+  PGEMM_SAMPLE_TEMPERATURE = 1,
+  PGEMM_SAMPLE_TOP_K = 2,
+  PGEMM_SAMPLE_TOP_P = 4,
+  PGEMM_SAMPLE_MIN_P = 8
+} pgemm_sample_setting;
+
+pgemm_status pgemm_f16_sample(const uint16_t *logits, const float *u, const float *temperature, const int32_t *top_k,
+                              const float *top_p, const float *min_p, int shared, int64_t *token, int64_t M, int64_t V,
+                              void *stream);
+pgemm_status pgemm_bf16_sample(const uint16_t *logits, const float *u, const float *temperature, const int32_t *top_k,
+                               const float *top_p, const float *min_p, int shared, int64_t *token, int64_t M, int64_t V,
+                               void *stream);
+
 const char *pgemm_strerror(pgemm_status status);
 int pgemm_abi_version(void);
 

@@ -1,12 +1,13 @@
 """Builds libpgemm.so (HIP, gfx950 only) in-tree with hipcc.
 
-The library is twelve translation units: the C ABI of the products (argument
+The library is eighteen translation units: the C ABI of the products (argument
 checks, planning, the int32 kernel), four units of NT kernel instances (f16
 and bf16, each with the direct-to-LDS and the register-staged loader), the C
-ABI of the fused operators, and their instances by operator and type.  They
-are compiled in parallel and linked into one shared library.
+ABI of the fused operators and their instances by operator and type, and the
+same for the serving operators.  They are compiled in parallel and linked into
+one shared library.
 
-Beside it, _binding.so: the fused operators' short way through Python, host C++
+Beside it, _binding.so: the fused and serving operators' short way through Python, host C++
 against torch's headers.
 """
 from __future__ import annotations
@@ -22,7 +23,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 UNITS = ["pgemm_api.hip", "inst_f16_direct.hip", "inst_f16_staged.hip", "inst_bf16_direct.hip",
          "inst_bf16_staged.hip", "fused_api.hip", "fused_gated_f16.hip", "fused_gated_bf16.hip", "fused_xent_f16.hip",
-         "fused_xent_bf16.hip", "fused_q4_f16.hip", "fused_q4_bf16.hip"]
+         "fused_xent_bf16.hip", "fused_q4_f16.hip", "fused_q4_bf16.hip", "serve_api.hip", "serve_i8_f16.hip",
+         "serve_i8_bf16.hip", "serve_moe_f16.hip", "serve_moe_bf16.hip", "serve_sample.hip"]
 LIB = os.path.join(HERE, "libpgemm.so")
 BINDING = os.path.join(HERE, "_binding.so")
 

@@ -1,0 +1,393 @@
+// Products of 8-bit integers with a scale for each token and each weight row:
+//
+//   out[m][n] = xs[m] ws[n] * sum over k of x[m][k] w[n][k]
+//
+// and the gated block on them.  Sums are int32 and exact (widths end where
+// 128 * 128 * K could leave it); the scales are applied in fp32 once.
+// Rows are padded to 16 bytes, with zeros on the tokens' side.
+#pragma once
+
+#include "fused_launch.hpp"
+#include "row_stream.hpp"
+
+namespace pgemm {
+
+// The integers' row width in bytes.
+inline int64_t i8_width(int64_t K) { return up_to(K, 16); }
+
+// acc xs ws without leaving fp32 where the result does not: a scale of at most
+// 1 comes first, after which the sum is below 2^31; above 1 it comes last,
+// where it overflows only if the result does.  What falls below 2^-126 on the
+// way is an integer times a subnormal scale, and exact.
+__device__ __forceinline__ float i8_scaled(int acc, float xs, float ws) {
+  const float a = (float)acc;
+  const bool small = fabsf(xs) <= 1.0f;
+  return a * (small ? xs : ws) * (small ? ws : xs);
+}
+
+// --------------------------------------------------------- quantization ---
+
+// A row's scale from its largest magnitude, at least the smallest normal
+// number; NaN for a row that holds an infinity or a NaN.
+__device__ __forceinline__ float i8_scale(float top) {
+  return top < INFINITY ? fmaxf(top / 127.0f, 0x1p-126f) : NAN;
+}
+
+// x / s rounded to the nearest integer, to the even one of two: the quotient
+// by way of the reciprocal is off by one where it lies next to a half at most,
+// and the remainder, which is exact there (x has at most 11 bits, n s at most
+// 31, and their difference is about s / 2), says so.  Above 127 it cannot come
+// out: s is at least (1 - 2^-24) max |x| / 127.  A NaN scale gives zero.
+__device__ __forceinline__ int i8_quantized(float x, float s, float inverse) {
+  const float n = __builtin_rintf(x * inverse);
+  const float twice = 2.0f * __builtin_fmaf(-n, s, x);
+  const bool odd = ((int)n & 1) != 0;
+  float to = n;
+  if (twice > s || (twice == s && odd)) to += 1.0f;
+  if (twice < -s || (twice == -s && odd)) to -= 1.0f;
+  return s == s ? (int)to : 0;
+}
+
+template <typename T>
+__device__ __forceinline__ float largest(u32x4 v, float top, bool *odd) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float a = fabsf(widen<T>((uint16_t)(v[e / 2] >> (16 * (e % 2)))));
+    *odd |= !(a < INFINITY);
+    top = fmaxf(top, a);
+  }
+  return top;
+}
+
+template <typename T>
+__device__ __forceinline__ u32x2 i8_packed(u32x4 v, float s, float inverse) {
+  u32x2 p = {0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int q = i8_quantized(widen<T>((uint16_t)(v[e / 2] >> (16 * (e % 2)))), s, inverse);
+    p[e / 4] |= ((uint32_t)q & 0xffu) << (8 * (e % 4));
+  }
+  return p;
+}
+
+// Eight values of a row from k on, zeros from K on.
+__device__ __forceinline__ u32x4 load_eight(const uint16_t *row, int k, int K) {
+  if (k + 8 <= K) return *reinterpret_cast<const u32x4_any *>(row + k);
+  return k < K ? load_tail(row, k, K) : u32x4{0u, 0u, 0u, 0u};
+}
+
+__device__ __forceinline__ float wave_largest(float top) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  return top;
+}
+
+// A wave a row, kept in registers between its maximum and its integers where
+// it has up to 512 C values; longer rows are read twice.
+template <typename T, int C>
+__global__ void __launch_bounds__(256) quant_rows_kernel(const uint16_t *__restrict__ x, int8_t *__restrict__ q,
+                                                         float *__restrict__ scale, int64_t M, int K, int width) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); m < M; m += (int64_t)gridDim.x * 4) {
+    const uint16_t *row = x + m * K;
+    int8_t *to = q + m * width;
+    float top = 0.0f;
+    bool odd = false;
+    u32x4 v[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = load_eight(row, (i * 64 + lane) * 8, K);
+#pragma unroll
+    for (int i = 0; i < C; ++i) top = largest<T>(v[i], top, &odd);
+    for (int k = (C * 64 + lane) * 8; k < K; k += 512) top = largest<T>(load_eight(row, k, K), top, &odd);
+    const float s = i8_scale(__any(odd) ? INFINITY : wave_largest(top)), inverse = 1.0f / s;
+    if (lane == 0) scale[m] = s;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int k = (i * 64 + lane) * 8;
+      if (k < width) *reinterpret_cast<u32x2 *>(to + k) = i8_packed<T>(v[i], s, inverse);
+    }
+    for (int k = (C * 64 + lane) * 8; k < width; k += 512)
+      *reinterpret_cast<u32x2 *>(to + k) = i8_packed<T>(load_eight(row, k, K), s, inverse);
+  }
+}
+
+// ------------------------------------------------------------ few tokens ---
+
+struct I8Args {
+  const uint16_t *x;  // [M][K], or null:
+  const int8_t *q;    // [M][width]
+  const float *xs;    // [M]
+  const int8_t *w;    // [N or 2 N][width]
+  const float *ws;
+  uint16_t *out;  // [M][N]
+  int M, N, K, width;
+  int act;
+};
+
+constexpr int kI8OwnTokens = 4;     // tokens that a workgroup makes integers of itself,
+constexpr int kI8OwnWidth = 8192;   // of at most so many values
+
+// A workgroup has 32 weight rows (16 of the gate and the same 16 of the up
+// projection) and all of K; its waves take blocks of 256 bytes in turn and add
+// their sums up in LDS.  XL: tokens of 16 bits are made integers by every
+// workgroup for itself while its first weights are on the way, which saves a
+// launch.
+template <typename T, bool GATED, int MT, int WAVES, bool XL>
+__global__ void __launch_bounds__(WAVES * 64) i8_few_kernel(I8Args a) {
+  constexpr int NT = 2, THREADS = WAVES * 64, VALS = MT * NT * 4;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = blockIdx.x * (GATED ? 16 : 32), m0 = blockIdx.y * MT * 16;
+  float *scales = reinterpret_cast<float *>(smem);  // XL: the tokens' scales
+  int *sums = reinterpret_cast<int *>(smem + (XL ? 64 : 0));
+  char *tokens = smem + 64 + WAVES * VALS * 256;
+
+  using Stream = RowStream<Int8Step, MT, NT, XL ? Tokens::Lds : Tokens::Rows>;
+  Stream job;
+  job.init(lane, a.width / 2);
+  typename Stream::Place at, next;
+  const int64_t rows = GATED ? 2 * (int64_t)a.N : a.N;
+#pragma unroll
+  for (int b = 0; b < NT; ++b) {
+    const int r = n0 + (GATED ? 0 : 16 * b) + (lane >> 2);
+    at.w[b] = row_of(a.w, GATED ? (int64_t)(r < a.N ? r : a.N - 1) + (int64_t)b * a.N : r, rows, a.width);
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) at.x[m] = XL ? nullptr : row_of(a.q, m0 + 16 * m + (lane >> 2), a.M, a.width);
+  const int blocks = job.blocks(), turn = first_turn(blockIdx.x, blocks);
+  auto block = [&](int i) { return i + turn < blocks ? i + turn : i + turn - blocks; };
+  next = at;
+  at.kb = wave < blocks ? block(wave) : 0;
+
+  if constexpr (XL) {
+    constexpr int C = kI8OwnWidth / (THREADS * 8);
+    static_assert(C * THREADS * 8 == kI8OwnWidth && WAVES * kI8OwnTokens * 4 <= WAVES * VALS * 256, "");
+    const int pitch = blocks * 256 + 16;
+    u32x4 v[kI8OwnTokens][C];
+#pragma unroll
+    for (int m = 0; m < kI8OwnTokens; ++m)
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        v[m][i] = m < a.M ? load_eight(a.x + (int64_t)m * a.K, (i * THREADS + tid) * 8, a.K) : u32x4{0u, 0u, 0u, 0u};
+    compiler_fence();  // the tokens first: waiting for them is then not waiting for the weights
+    if (wave < blocks) job.begin(at);
+    compiler_fence();
+    float *tops = reinterpret_cast<float *>(sums);  // [tokens][waves]
+#pragma unroll
+    for (int m = 0; m < kI8OwnTokens; ++m) {
+      if (m >= a.M) continue;
+      float top = 0.0f;
+      bool odd = false;
+#pragma unroll
+      for (int i = 0; i < C; ++i) top = largest<T>(v[m][i], top, &odd);
+      top = __any(odd) ? INFINITY : wave_largest(top);
+      if (lane == 0) tops[m * WAVES + wave] = top;
+    }
+    lds_barrier();
+#pragma unroll
+    for (int m = 0; m < kI8OwnTokens; ++m) {
+      if (m >= a.M) continue;
+      float top = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, tops[m * WAVES + w]);
+      const float s = i8_scale(top), inverse = 1.0f / s;
+      if (tid == 0) scales[m] = s;
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const int k = (i * THREADS + tid) * 8;
+        if (k < blocks * 256) *reinterpret_cast<u32x2 *>(tokens + m * pitch + k) = i8_packed<T>(v[m][i], s, inverse);
+      }
+    }
+    lds_barrier();
+    const int row = lane & 15;
+    job.xl = tokens + (row < a.M ? row : a.M - 1) * pitch + 16 * (lane >> 4);
+  } else {
+    if (wave < blocks) job.begin(at);
+  }
+  if (wave < blocks) {
+    for (int i = wave + WAVES; i < blocks; i += WAVES) {
+      next.kb = block(i);
+      job.template block<true>(at, next);
+      at.kb = next.kb;
+    }
+    job.template block<false>(at, at);
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int b = 0; b < NT; ++b) {
+      const i32x4 v = __builtin_bit_cast(i32x4, job.tot[m][b]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sums[(wave * VALS + (m * NT + b) * 4 + r) * 64 + lane] = v[r];
+    }
+  __syncthreads();
+
+  constexpr int OB = GATED ? 1 : NT;
+  const int c = lane & 15, q = lane >> 4;
+  for (int i = wave; i < MT * OB * 4; i += WAVES) {
+    const int m = i / (OB * 4), b = i / 4 % OB, r = i % 4;
+    const int row = m0 + 16 * m + 4 * q + r, col = n0 + 16 * b + c;
+    if (row >= a.M || col >= a.N) continue;
+    auto joined = [&](int block) {
+      int v = 0;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) v += sums[(w * VALS + (m * NT + block) * 4 + r) * 64 + lane];
+      return v;
+    };
+    const float xs = XL ? scales[row] : a.xs[row];
+    float v = i8_scaled(joined(b), xs, a.ws[col]);
+    if constexpr (GATED) v = activate(a.act, v) * i8_scaled(joined(1), xs, a.ws[(int64_t)col + a.N]);
+    a.out[(int64_t)row * a.N + col] = __builtin_bit_cast(uint16_t, (T)v);
+  }
+}
+
+// ------------------------------------------------------------ many tokens ---
+//
+// The tiled product (fused_gemm.hpp) on rows of bytes: a granule of 16 bytes
+// holds 16 integers of K instead of eight values, and
+// v_mfma_i32_16x16x64_i8 takes as long as v_mfma_f32_16x16x32 with twice the
+// operations.  Accumulators keep int32 bits.
+
+template <>
+struct Mfma<int8_t> {
+  template <bool ACC_AGPR>
+  __device__ __forceinline__ static void run(u32x4 src0, u32x4 src1, f32x4 &acc) {
+    if constexpr (ACC_AGPR)
+      asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(src0), "v"(src1));
+    else
+      asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+v"(acc) : "v"(src0), "v"(src1));
+  }
+};
+
+// A lane's column scales, those past the matrix's last column repeated.
+__device__ __forceinline__ f32x4 i8_column_scales(const float *ws, int col, int N) {
+  f32x4 v;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) v[x] = ws[col + x < N ? col + x : N - 1];
+  return v;
+}
+
+template <typename O>
+struct I8Epi {
+  struct Args {
+    uint16_t *out;
+    const float *xs, *ws;
+  };
+  template <typename T, class G, class W>
+  struct Run {
+    __device__ __forceinline__ void operator()(W &w, const Args &e, const FusedProduct &g, char *smem, int m0, int n0,
+                                               int wm, int wn, int lane, int tid) const {
+      constexpr int PITCH = Staging<G::BN>::PITCH;
+      const int lr = wm * G::WM + (lane & 15), lc = wn * G::WN + 4 * (lane >> 4);
+      float xs[W::TM];
+#pragma unroll
+      for (int i = 0; i < W::TM; ++i) xs[i] = e.xs[m0 + lr + 16 * i < g.M ? m0 + lr + 16 * i : g.M - 1];
+#pragma unroll
+      for (int j = 0; j < W::TN; ++j) {
+        const f32x4 ws = i8_column_scales(e.ws, n0 + lc + 16 * j, g.N);
+#pragma unroll
+        for (int i = 0; i < W::TM; ++i) {
+          const i32x4 v = __builtin_bit_cast(i32x4, w.acc[i][j]);
+          *reinterpret_cast<u32x2 *>(smem + (lr + 16 * i) * PITCH + (lc + 16 * j) * 2) =
+              Mfma<O>::pack4(i8_scaled(v[0], xs[i], ws[0]), i8_scaled(v[1], xs[i], ws[1]), i8_scaled(v[2], xs[i], ws[2]),
+                             i8_scaled(v[3], xs[i], ws[3]));
+        }
+      }
+      __syncthreads();
+      store_tile<G::BM, G::BN, G::THREADS>(smem, PITCH, 0, e.out, g.N, g.M, g.N, m0, n0, tid);
+    }
+  };
+};
+
+template <typename O>
+struct I8GatedEpi {
+  struct Args {
+    uint16_t *out;
+    const float *xs, *ws;
+    int act;
+  };
+  template <typename T, class G, class W>
+  struct Run {
+    __device__ __forceinline__ void operator()(W &w, const Args &e, const FusedProduct &g, char *smem, int m0, int n0,
+                                               int wm, int wn, int lane, int tid) const {
+      constexpr int ON = G::BN / 2, PITCH = Staging<ON>::PITCH;
+      const int r = lane & 15, q = lane >> 4;
+      float xs[W::TM];
+#pragma unroll
+      for (int i = 0; i < W::TM; ++i) {
+        const int row = m0 + wm * G::WM + 16 * i + r;
+        xs[i] = e.xs[row < g.M ? row : g.M - 1];
+      }
+#pragma unroll
+      for (int p = 0; p < W::TN / 2; ++p) {
+        const int lcol = wn * (G::WN / 2) + 16 * p + 4 * q;
+        const f32x4 wg = i8_column_scales(e.ws, n0 + lcol, g.N), wu = i8_column_scales(e.ws + g.N, n0 + lcol, g.N);
+#pragma unroll
+        for (int i = 0; i < W::TM; ++i) {
+          const i32x4 ga = __builtin_bit_cast(i32x4, w.acc[i][2 * p]), up = __builtin_bit_cast(i32x4, w.acc[i][2 * p + 1]);
+          f32x4 h;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            h[x] = activate(e.act, i8_scaled(ga[x], xs[i], wg[x])) * i8_scaled(up[x], xs[i], wu[x]);
+          *reinterpret_cast<u32x2 *>(smem + (wm * G::WM + 16 * i + r) * PITCH + lcol * 2) = Mfma<O>::pack4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      __syncthreads();
+      store_tile<G::BM, ON, G::THREADS>(smem, PITCH, 0, e.out, g.N, g.M, g.N, m0, n0, tid);
+    }
+  };
+};
+
+// A piece of K: the sums as they are, for i8_join_kernel.
+struct I8PieceEpi {
+  struct Args {
+    int *part;  // [pieces][M][pp]
+    int pp;     // a multiple of 4
+  };
+  template <typename T, class G, class W>
+  struct Run {
+    __device__ __forceinline__ void operator()(W &w, const Args &e, const FusedProduct &g, char *smem, int m0, int n0,
+                                               int wm, int wn, int lane, int tid) const {
+      int *part = e.part + (int64_t)g.piece * g.M * e.pp;
+#pragma unroll
+      for (int i = 0; i < W::TM; ++i) {
+        const int row = m0 + wm * G::WM + 16 * i + (lane & 15);
+        if (row >= g.M) continue;
+#pragma unroll
+        for (int j = 0; j < W::TN; ++j) {
+          const int col = n0 + wn * G::WN + 16 * j + 4 * (lane >> 4);
+          if (col < g.N) *reinterpret_cast<f32x4 *>(part + (int64_t)row * e.pp + col) = w.acc[i][j];
+        }
+      }
+    }
+  };
+};
+
+template <typename O>
+__global__ void __launch_bounds__(256) i8_join_kernel(const int *__restrict__ part, int pieces, int M, int N, int pp,
+                                                      const float *__restrict__ xs, const float *__restrict__ ws,
+                                                      uint16_t *__restrict__ out) {
+  const int per_row = pp / 4;
+  const int64_t total = (int64_t)M * per_row, stride = (int64_t)M * pp;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per_row;
+    const int col = (int)(i % per_row) * 4;
+    i32x4 v = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = 0; s < pieces; ++s) v += *reinterpret_cast<const i32x4 *>(part + i * 4 + s * stride);
+    const f32x4 w = i8_column_scales(ws, col, N);
+    const float x = xs[row];
+    const u32x2 r = Mfma<O>::pack4(i8_scaled(v[0], x, w[0]), i8_scaled(v[1], x, w[1]), i8_scaled(v[2], x, w[2]),
+                                   i8_scaled(v[3], x, w[3]));
+    uint16_t *dst = out + row * N + col;
+    if (col + 4 <= N) {
+      *reinterpret_cast<u32x2_any *>(dst) = r;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + e < N) dst[e] = (uint16_t)(r[e / 2] >> (16 * (e % 2)));
+    }
+  }
+}
+
+}  // namespace pgemm

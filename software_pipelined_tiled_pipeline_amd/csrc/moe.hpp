@@ -1,0 +1,412 @@
+// A mixture-of-experts layer for few tokens:
+//
+//   l = x R^T, the top_k experts e of each token by l, p = softmax of l,
+//   h_e = act(x Wg_e^T) * (x Wu_e^T),   y = sum over e of p_e h_e Wd_e^T.
+//
+// Bound by reading the reached experts' weights once.  Four launches: the
+// router's logits, the choice, the gated blocks and the second products.  Tokens
+// are taken in chunks of 64, which do not know of each other.  A chunk has
+// slots for the experts it may reach: one for each expert, or, where it has
+// fewer choices than there are experts, one for each choice, used by the first
+// choice of an expert.
+#pragma once
+
+#include "row_stream.hpp"
+#include "serve.hpp"
+
+namespace pgemm {
+
+struct MoeArgs {
+  const uint16_t *x, *router, *w, *down;
+  uint16_t *y;
+  int32_t *experts;    // [M][k]
+  float *weights;      // [M][k]
+  double *logits;      // [M][E]
+  char *h;             // [M k][F]: T, or fp32 where T is f16
+  uint32_t *tops;      // [M k] largest |h|, f16 only
+  uint32_t *counts;    // [chunks][slots] choices of the slot's expert, and the expert << 8
+  uint16_t *lists;     // [chunks][slots][64] which choices of the chunk they are
+  int M, E, D, F, k, slots;
+  bool by_choice;      // slots are choices
+  int act;
+  bool normalize;
+};
+
+// The hidden values are multiplied again on the matrix units and rounded to T
+// for that.  binary16 ends at 65504, which h may pass where y does not: in f16
+// they are kept in fp32 with each choice's largest, and rounded after a power
+// of two that takes this into [2^14, 2^15).
+template <typename T>
+constexpr bool kWideHidden = std::is_same_v<T, _Float16>;
+
+// ------------------------------------------------------------ the choice ---
+
+// Logits in 64 bits: which experts a token gets must not depend on the order
+// of the sum.  A wave takes two experts, eight values a lane at a time.
+template <typename T>
+__global__ void __launch_bounds__(256) moe_logits_kernel(MoeArgs a) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int m = blockIdx.y, e0 = (blockIdx.x * 4 + wave) * 2;
+  if (e0 >= a.E) return;
+  const uint16_t *x = a.x + (int64_t)m * a.D;
+  const uint16_t *r[2] = {a.router + (int64_t)e0 * a.D, a.router + (int64_t)(e0 + 1 < a.E ? e0 + 1 : e0) * a.D};
+  double sum[2] = {0.0, 0.0};
+  for (int k = lane * 8; k < a.D; k += 512) {
+    const u32x4 xv = k + 8 <= a.D ? *reinterpret_cast<const u32x4_any *>(x + k) : load_tail(x, k, a.D);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const u32x4 rv = k + 8 <= a.D ? *reinterpret_cast<const u32x4_any *>(r[i] + k) : load_tail(r[i], k, a.D);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        sum[i] = __builtin_fma((double)widen<T>((uint16_t)(xv[e / 2] >> (16 * (e % 2)))),
+                               (double)widen<T>((uint16_t)(rv[e / 2] >> (16 * (e % 2)))), sum[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) sum[i] += __shfl_xor(sum[i], d);
+    if (lane == 0 && e0 + i < a.E) a.logits[(int64_t)m * a.E + e0 + i] = sum[i];
+  }
+}
+
+// Numbers as integers of the same order; a NaN is behind minus infinity.
+__device__ __forceinline__ uint64_t moe_order(double v) {
+  if (v != v) return 1;
+  const uint64_t b = __builtin_bit_cast(uint64_t, v == 0.0 ? 0.0 : v);
+  return b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ double moe_value(uint64_t o) {
+  if (o == 1) return NAN;
+  return __builtin_bit_cast(double, o >> 63 ? o ^ 1ull << 63 : ~o);
+}
+
+constexpr int kMoeExperts = 1024, kMoeTop = 32, kMoeChunk = 64;
+
+// A wave a token: top_k times the largest logit that is left, the lowest index
+// of equal ones.
+static __global__ void __launch_bounds__(64) moe_choose_kernel(MoeArgs a) {
+  constexpr int PER = kMoeExperts / 64;
+  const int lane = threadIdx.x, m = blockIdx.x;
+  const double *l = a.logits + (int64_t)m * a.E;
+  uint64_t left[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) left[i] = i * 64 + lane < a.E ? moe_order(l[i * 64 + lane]) : 0;
+  double first = 0.0, total = 0.0, mine = 0.0;
+  int my_expert = 0;
+  for (int j = 0; j < a.k; ++j) {
+    uint64_t best = left[0];
+    int at = lane;
+#pragma unroll
+    for (int i = 1; i < PER; ++i)
+      if (i * 64 < a.E && left[i] > best) {
+        best = left[i];
+        at = i * 64 + lane;
+      }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      const uint64_t other = __shfl_xor((unsigned long long)best, d);
+      const int where = __shfl_xor(at, d);
+      if (other > best || (other == best && where < at)) {
+        best = other;
+        at = where;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (at == i * 64 + lane) left[i] = 0;
+    const double v = moe_value(best);
+    if (j == 0) first = v;
+    const double e = exp(v - first);
+    total += e;
+    if (lane == j) {
+      mine = e;
+      my_expert = at;
+    }
+  }
+  if (!a.normalize) {
+    total = 0.0;
+    for (int e = lane; e < a.E; e += 64) total += exp(l[e] - first);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) total += __shfl_xor(total, d);
+  }
+  if (lane < a.k) {
+    const int64_t at = (int64_t)m * a.k + lane;
+    a.experts[at] = my_expert;
+    a.weights[at] = (float)(mine / total);
+    if (a.tops) a.tops[at] = 0;
+  }
+}
+
+// ---------------------------------------------------------- gated blocks ---
+
+// A workgroup has an expert's 16 gate rows and the same 16 up rows; its waves
+// take blocks of K in turn and join their sums in LDS.  More than 16 MT tokens
+// of an expert take another pass over these weights.
+template <typename T, int MT, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64) moe_gated_kernel(MoeArgs a) {
+  constexpr int NT = 2, VALS = MT * NT * 4;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  uint16_t *list = reinterpret_cast<uint16_t *>(smem);  // [64]
+  int *found = reinterpret_cast<int *>(smem + 128);
+  float *sums = reinterpret_cast<float *>(smem + 144);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int slot = blockIdx.y, chunk = blockIdx.z, f0 = blockIdx.x * 16;
+  const int t0 = chunk * kMoeChunk, tokens = a.M - t0 < kMoeChunk ? a.M - t0 : kMoeChunk;
+  const int choices = tokens * a.k;
+  const int32_t *experts = a.experts + (int64_t)t0 * a.k;
+  if (a.by_choice && slot >= choices) {  // a last chunk of few tokens
+    if (blockIdx.x == 0 && tid == 0) a.counts[(int64_t)chunk * a.slots + slot] = 0;
+    return;
+  }
+  const int expert = a.by_choice ? __builtin_amdgcn_readfirstlane(experts[slot]) : slot;
+  if (wave == 0) {
+    int n = 0;
+    bool taken = false;  // an earlier choice has this expert's slot
+    for (int base = 0; base < choices; base += 64) {
+      const int c = base + lane;
+      const bool is = c < choices && experts[c] == expert;
+      const uint64_t who = __ballot(is);
+      if (is) list[n + __popcll(who & ((1ull << lane) - 1))] = (uint16_t)c;
+      if (a.by_choice) taken |= __ballot(is && c < slot) != 0;
+      n += __popcll(who);
+    }
+    if (taken) n = 0;
+    if (lane == 0) *found = n;
+  }
+  __syncthreads();
+  const int n = __builtin_amdgcn_readfirstlane(*found);
+  if (blockIdx.x == 0) {
+    const int64_t at = (int64_t)chunk * a.slots + slot;
+    if (tid == 0) a.counts[at] = (uint32_t)n | (uint32_t)expert << 8;
+    if (tid < n) a.lists[at * kMoeChunk + tid] = list[tid];
+  }
+  if (n == 0) return;
+
+  using Stream = RowStream<Frag8<T>, MT, NT>;
+  Stream job;
+  job.init(lane, a.D);
+  typename Stream::Place at, next;
+  const int blocks = job.blocks(), turn = first_turn(blockIdx.x + slot * 7, blocks);
+  auto block = [&](int i) { return i + turn < blocks ? i + turn : i + turn - blocks; };
+  const uint16_t *w = a.w + (int64_t)expert * 2 * a.F * a.D;
+  const int64_t pitch = (int64_t)a.D * 2;
+  const int c = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int b = 0; b < NT; ++b) at.w[b] = row_of(w + (int64_t)b * a.F * a.D, f0 + (lane >> 2), a.F, pitch);
+  for (int first = 0; first < n; first += 16 * MT) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int i = first + 16 * m + (lane >> 2);
+      at.x[m] = row_of(a.x, t0 + list[i < n ? i : n - 1] / a.k, a.M, pitch);
+    }
+    next = at;
+    job.clear();
+    if (a.D < 8) {
+      if (wave == 0 && a.D > 0) job.short_rows(at);
+    } else if (wave < blocks) {
+      at.kb = block(wave);
+      job.begin(at);
+      for (int i = wave + WAVES; i < blocks; i += WAVES) {
+        next.kb = block(i);
+        job.template block<true>(at, next);
+        at.kb = next.kb;
+      }
+      job.template block<false>(at, at);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sums[(wave * VALS + (m * NT + b) * 4 + r) * 64 + lane] = job.tot[m][b][r];
+    __syncthreads();
+    for (int i = wave; i < MT * 4; i += WAVES) {
+      const int m = i / 4, r = i % 4, place = first + 16 * m + 4 * q + r, col = f0 + c;
+      if (first + 16 * m + r >= n) continue;  // no token in any lane
+      auto joined = [&](int b) {
+        float v = 0.0f;
+#pragma unroll
+        for (int u = 0; u < WAVES; ++u) v += sums[(u * VALS + (m * NT + b) * 4 + r) * 64 + lane];
+        return v;
+      };
+      const float h = activate(a.act, joined(0)) * joined(1);
+      const bool in = place < n && col < a.F;
+      const int64_t choice = (int64_t)t0 * a.k + list[place < n ? place : n - 1];
+      if constexpr (kWideHidden<T>) {
+        if (in) reinterpret_cast<float *>(a.h)[choice * a.F + col] = h;
+        // of the finite ones: the others end where the definition has them end
+        uint32_t top = in && fabsf(h) < INFINITY ? __builtin_bit_cast(uint32_t, fabsf(h)) : 0u;
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) {
+          const uint32_t other = (uint32_t)__shfl_xor((int)top, d);
+          top = other > top ? other : top;
+        }
+        if (c == 0 && place < n) atomicMax(a.tops + choice, top);
+      } else {
+        if (in) reinterpret_cast<uint16_t *>(a.h)[choice * a.F + col] = __builtin_bit_cast(uint16_t, (T)h);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------- second products ---
+
+// The exponent of the factor of a choice's hidden values, from the largest one's bits.
+__device__ __forceinline__ int moe_exponent(uint32_t top) {
+  if (top == 0) return 0;
+  int e;
+  frexpf(__builtin_bit_cast(float, top), &e);
+  return 15 - e > 127 ? 127 : 15 - e;
+}
+
+__host__ __device__ constexpr int up_even(int n) { return (n + 1) & ~1; }
+// LDS of moe_down_kernel
+inline int moe_down_lds(int waves, int tokens, int k, int slots) {
+  const int choices = tokens * k;
+  return waves * tokens * 64 + choices * 12 + up_even(choices) * 2 + slots * 4 + 4 + choices;
+}
+
+// A workgroup has 16 columns of y and all experts of a chunk.  Their blocks of
+// K, one expert's after the other's, are dealt to the waves in runs of the same
+// length; where a run leaves an expert (or 16 MT of its tokens), the wave adds
+// its sums, times the choices' weights, to its own copy of the chunk's rows,
+// and the copies are added up in order at the end.
+template <typename T, int MT, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(MoeArgs a) {
+  constexpr int THREADS = WAVES * 64;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int chunk = blockIdx.y, d0 = blockIdx.x * 16;
+  const int t0 = chunk * kMoeChunk, tokens = a.M - t0 < kMoeChunk ? a.M - t0 : kMoeChunk;
+  const int choices = tokens * a.k;
+  float *rows = reinterpret_cast<float *>(smem);                        // [WAVES][tokens][16]
+  float *weight = rows + WAVES * tokens * 16;                           // [choices], by slot
+  uint32_t *part = reinterpret_cast<uint32_t *>(weight + choices);      // [choices] of a part: first place in the list, how many << 16; expert
+  uint16_t *list = reinterpret_cast<uint16_t *>(part + 2 * choices);    // [choices], by slot
+  uint32_t *from_slot = reinterpret_cast<uint32_t *>(list + up_even(choices));  // [slots] first place in the list, how many << 16
+  int *parts_found = reinterpret_cast<int *>(from_slot + a.slots);
+  int8_t *power = reinterpret_cast<int8_t *>(parts_found + 1);  // [choices] exponents (f16)
+
+  for (int i = tid; i < WAVES * tokens * 16; i += THREADS) rows[i] = 0.0f;
+  const int blocks = (a.F + 127) / 128;
+  if (wave == 0) {
+    int at = 0, parts = 0;
+    for (int base = 0; base < a.slots; base += 64) {
+      const int s = base + lane;
+      const uint32_t v = s < a.slots && blocks > 0 ? a.counts[(int64_t)chunk * a.slots + s] : 0u;
+      const int n = (int)(v & 0xffu), mine = (n + 16 * MT - 1) / (16 * MT);
+      int before = n, parts_before = mine;  // sums over the lanes up to this one
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(before, d), p = __shfl_up(parts_before, d);
+        before += lane >= d ? u : 0;
+        parts_before += lane >= d ? p : 0;
+      }
+      const int to = at + before - n;
+      if (s < a.slots) from_slot[s] = (uint32_t)to | (uint32_t)n << 16;
+      for (int i = 0; i < mine; ++i) {
+        const int left = n - i * 16 * MT;
+        const int p = parts + parts_before - mine + i;
+        part[2 * p] = (uint32_t)(to + i * 16 * MT) | (uint32_t)(left < 16 * MT ? left : 16 * MT) << 16;
+        part[2 * p + 1] = v >> 8;
+      }
+      at += __shfl(before, 63);
+      parts += __shfl(parts_before, 63);
+    }
+    if (lane == 0) *parts_found = parts;
+  }
+  __syncthreads();
+  for (int i = tid; i < a.slots * kMoeChunk; i += THREADS) {
+    const uint32_t v = from_slot[i / kMoeChunk];
+    if (i % kMoeChunk < (int)(v >> 16))
+      list[(v & 0xffffu) + i % kMoeChunk] = a.lists[(int64_t)chunk * a.slots * kMoeChunk + i];
+  }
+  __syncthreads();
+  const int parts = __builtin_amdgcn_readfirstlane(*parts_found);
+  for (int i = tid; i < choices && parts > 0; i += THREADS) {
+    const int64_t choice = (int64_t)t0 * a.k + list[i];
+    weight[i] = a.weights[choice];
+    if constexpr (kWideHidden<T>) power[i] = (int8_t)moe_exponent(a.tops[choice]);
+  }
+  __syncthreads();
+
+  using Stream = RowStream<Frag8<T>, MT, 1, kWideHidden<T> ? Tokens::Wide : Tokens::Rows, T>;
+  Stream job;
+  job.init(lane, a.F);
+  const int64_t pitch = (int64_t)a.F * 2, total = (int64_t)parts * blocks;
+  const int c = lane & 15, q = lane >> 4;
+  int64_t i = total * wave / WAVES;
+  const int64_t end = total * (wave + 1) / WAVES;
+  auto place = [&](typename Stream::Place &p, int g, int kb) __attribute__((always_inline)) {
+    const uint32_t v = part[2 * g];
+    const int from = (int)(v & 0xffffu), n = (int)(v >> 16), expert = __builtin_amdgcn_readfirstlane((int)part[2 * g + 1]);
+    p.kb = kb;
+    p.w[0] = row_of(a.down + (int64_t)expert * a.D * a.F, d0 + (lane >> 2), a.D, pitch);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int j = 16 * m + (lane >> 2), which = from + (j < n ? j : n - 1);
+      const int64_t choice = (int64_t)t0 * a.k + list[which];
+      p.x[m] = a.h + choice * a.F * (kWideHidden<T> ? 4 : 2);
+      p.scale[m] = kWideHidden<T> ? ldexpf(1.0f, power[which]) : 1.0f;
+    }
+  };
+  auto add = [&](int g) __attribute__((always_inline)) {
+    const uint32_t v = part[2 * g];
+    const int from = (int)(v & 0xffffu), n = (int)(v >> 16);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int j = 16 * m + 4 * q + r;
+        if (j >= n) continue;
+        const int token = list[from + j] / a.k;
+        float s = job.tot[m][0][r];
+        if constexpr (kWideHidden<T>) s = ldexpf(s, -power[from + j]);
+        rows[(wave * tokens + token) * 16 + c] += weight[from + j] * s;
+      }
+    job.clear();
+  };
+  if (i < end) {
+    int g = __builtin_amdgcn_readfirstlane((int)(i / blocks)), kb = __builtin_amdgcn_readfirstlane((int)(i % blocks));
+    typename Stream::Place at, next;
+    if (a.F < 8) {
+      for (; i < end; ++i) {
+        place(at, (int)i, 0);
+        job.short_rows(at);
+        add((int)i);
+      }
+    } else {
+    place(at, g, kb);
+    job.begin(at);
+    for (++i; i < end; ++i) {
+      if (kb + 1 < blocks) {
+        next = at;
+        next.kb = ++kb;
+        job.template block<true>(at, next);
+      } else {
+        kb = 0;
+        place(next, g + 1, 0);
+        job.template block<true>(at, next);
+        add(g);
+        ++g;
+      }
+      at = next;
+    }
+    job.template block<false>(at, at);
+    add(g);
+    }
+  }
+  __syncthreads();
+  for (int j = tid; j < tokens * 16; j += THREADS) {
+    const int col = d0 + j % 16;
+    if (col >= a.D) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) v += rows[w * tokens * 16 + j];
+    a.y[(int64_t)(t0 + j / 16) * a.D + col] = __builtin_bit_cast(uint16_t, (T)v);
+  }
+}
+
+}  // namespace pgemm

@@ -1,0 +1,78 @@
+// Launches of the mixture of experts.
+#pragma once
+
+#include "fused_launch.hpp"
+#include "moe.hpp"
+
+namespace pgemm {
+namespace launch_detail {
+
+template <typename T, int MT, int WAVES>
+pgemm_status launch_moe_gated(const MoeArgs &a, int64_t chunks, hipStream_t stream) {
+  constexpr int LDS = 144 + WAVES * MT * 2 * 4 * 256;
+  static_assert(LDS <= 65536, "what a kernel may use without asking");
+  auto kern = moe_gated_kernel<T, MT, WAVES>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)per(a.F, 16), (unsigned)a.slots, (unsigned)chunks), dim3(WAVES * 64), LDS, stream, a);
+  return launched();
+}
+
+template <typename T, int MT, int WAVES>
+pgemm_status launch_moe_down(const MoeArgs &a, int64_t chunks, hipStream_t stream, int dev) {
+  static std::atomic<uint64_t> lds_set{0};
+  constexpr int kMost = 160 * 1024;
+  auto kern = moe_down_kernel<T, MT, WAVES>;
+  const int lds = moe_down_lds(WAVES, a.M < kMoeChunk ? a.M : kMoeChunk, a.k, a.slots);
+  if (lds > 65536) {
+    pgemm_status st = allow_lds(kern, kMost, dev, lds_set);
+    if (st != PGEMM_OK) return st;
+  }
+  hipLaunchKernelGGL(kern, dim3((unsigned)per(a.D, 16), (unsigned)chunks), dim3(WAVES * 64), lds, stream, a);
+  return launched();
+}
+
+template <typename T>
+pgemm_status moe_layer(const MoeCall &c) {
+  const MoePlan p = plan_moe(c.M, c.E, c.F, c.top_k);
+  const int64_t chunks = per(c.M, kMoeChunkTokens);
+  MoeArgs a{};
+  a.x = c.x;
+  a.router = c.router;
+  a.w = c.w;
+  a.down = c.down;
+  a.y = c.y;
+  a.experts = c.experts ? c.experts : reinterpret_cast<int32_t *>(c.workspace + p.experts);
+  a.weights = c.weights ? c.weights : reinterpret_cast<float *>(c.workspace + p.weights);
+  a.logits = reinterpret_cast<double *>(c.workspace + p.logits);
+  a.h = c.workspace + p.h;
+  a.tops = kWideHidden<T> ? reinterpret_cast<uint32_t *>(c.workspace + p.tops) : nullptr;
+  a.counts = reinterpret_cast<uint32_t *>(c.workspace + p.counts);
+  a.lists = reinterpret_cast<uint16_t *>(c.workspace + p.lists);
+  a.M = (int)c.M;
+  a.E = (int)c.E;
+  a.D = (int)c.D;
+  a.F = (int)c.F;
+  a.k = (int)c.top_k;
+  a.slots = (int)p.slots;
+  a.by_choice = p.by_choice;
+  a.act = c.act;
+  a.normalize = c.normalize;
+  hipLaunchKernelGGL(moe_logits_kernel<T>, dim3((unsigned)per(c.E, 8), (unsigned)c.M), dim3(256), 0, c.stream, a);
+  pgemm_status st = launched();
+  if (st != PGEMM_OK) return st;
+  hipLaunchKernelGGL(moe_choose_kernel, dim3((unsigned)c.M), dim3(64), 0, c.stream, a);
+  st = launched();
+  if (st != PGEMM_OK || c.D == 0) return st;
+  // tokens an expert has on average
+  const int64_t mean = (c.M < kMoeChunkTokens ? c.M : kMoeChunkTokens) * c.top_k / c.E;
+  if (c.F > 0) {
+    st = mean <= 8 ? launch_moe_gated<T, 1, 8>(a, chunks, c.stream)
+                   : mean <= 24 ? launch_moe_gated<T, 2, 8>(a, chunks, c.stream) : launch_moe_gated<T, 4, 4>(a, chunks, c.stream);
+    if (st != PGEMM_OK) return st;
+  }
+  return mean <= 8 ? launch_moe_down<T, 1, 8>(a, chunks, c.stream, c.dev)
+                   : mean <= 24 ? launch_moe_down<T, 2, 8>(a, chunks, c.stream, c.dev)
+                                : launch_moe_down<T, 4, 8>(a, chunks, c.stream, c.dev);
+}
+
+}  // namespace launch_detail
+}  // namespace pgemm

@@ -16,7 +16,7 @@ from __future__ import annotations
 import ctypes
 import os
 
-from . import fused
+from . import fused, serve
 from .fused import pack_q4  # noqa: F401
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -61,6 +61,7 @@ def lib() -> ctypes.CDLL:
             f.argtypes = [P, P, P, I64, I64, I64, I, P]
             f.restype = I
         fused.declare(L)
+        serve.declare(L)
         L.pgemm_query.argtypes = [I, I, I64, I64, I64, ctypes.POINTER(KernelInfo)]
         L.pgemm_query.restype = I
         L.pgemm_debug_status.argtypes = [P]
@@ -215,6 +216,8 @@ pgemm_bf16_nt_ws = _nt("pgemm_bf16_nt_ws", "bfloat16")
 
 # the fused operators: pgemm_{f16,bf16}_{gated,gated_bwd,xent,xent_bwd,q4,q4_gated}
 globals().update(fused.FUNCTIONS)
+# the serving operators: pgemm_{f16,bf16}_{quant_i8,i8,i8_gated,moe,sample}
+globals().update(serve.FUNCTIONS)
 
 
 def pgemm_query(op: str, stages: int, M: int, N: int, K: int) -> dict:
