@@ -33,11 +33,33 @@ __device__ __forceinline__ float i8_scale(float top) {
   return top < INFINITY ? fmaxf(top / 127.0f, 0x1p-126f) : NAN;
 }
 
-// x / s rounded to the nearest integer, to the even one of two: the quotient
-// by way of the reciprocal is off by one where it lies next to a half at most,
-// and the remainder, which is exact there (x has at most 11 bits, n s at most
-// 31, and their difference is about s / 2), says so.  Above 127 it cannot come
-// out: s is at least (1 - 2^-24) max |x| / 127.  A NaN scale gives zero.
+// Whether a row holds an infinity or a NaN shows in the largest of its
+// magnitudes' bits, which have their values' order: two at a time.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+struct Largest {
+  u16x2 top = {0, 0};
+  __device__ __forceinline__ void take(const u32x4 &v) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, v[d] & 0x7FFF7FFFu));
+  }
+  __device__ __forceinline__ uint32_t bits() const { return top[0] > top[1] ? top[0] : top[1]; }
+};
+template <typename T>
+__device__ __forceinline__ float i8_scale_of(uint32_t bits) {
+  return i8_scale(bits < (std::is_same_v<T, _Float16> ? 0x7C00u : 0x7F80u) ? widen<T>((uint16_t)bits) : INFINITY);
+}
+__device__ __forceinline__ uint32_t wave_largest(uint32_t top) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)top, d);
+    top = o > top ? o : top;
+  }
+  return top;
+}
+
+// x / s rounded to the nearest integer n, to the even one of two, by the sign
+// of what x is above n s or below it and half an s more: exact, since x has at
+// most 11 bits, n s at most 31, and their difference is about s / 2.
 __device__ __forceinline__ int i8_quantized(float x, float s, float inverse) {
   const float n = __builtin_rintf(x * inverse);
   const float twice = 2.0f * __builtin_fmaf(-n, s, x);
@@ -45,68 +67,100 @@ __device__ __forceinline__ int i8_quantized(float x, float s, float inverse) {
   float to = n;
   if (twice > s || (twice == s && odd)) to += 1.0f;
   if (twice < -s || (twice == -s && odd)) to -= 1.0f;
-  return s == s ? (int)to : 0;
+  return (int)to;
 }
 
+// Eight values' integers.  x times the reciprocal is within 2^-16 of the
+// quotient (|x / s| <= 127, two roundings of 2^-24), so that its nearest integer is the
+// right one unless it lies that near to a half, where i8_quantized takes over.
+// 1.5 * 2^23 added to it leaves the integer in the lowest byte.  Beyond 127 it
+// does not come: s is at least (1 - 2^-24) max |x| / 127.
 template <typename T>
-__device__ __forceinline__ float largest(u32x4 v, float top, bool *odd) {
+__device__ __forceinline__ u32x2 i8_packed(const u32x4 &v, float s, float inverse) {
+  constexpr float MAGIC = 12582912.0f, NEAR = 0.5f - 0x1p-15f;
+  uint32_t q[8];
+  float off = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float a = fabsf(widen<T>((uint16_t)(v[e / 2] >> (16 * (e % 2)))));
-    *odd |= !(a < INFINITY);
-    top = fmaxf(top, a);
+    const float x = widen<T>((uint16_t)(v[e / 2] >> (16 * (e % 2))));
+    const float f = __builtin_fmaf(x, inverse, MAGIC);
+    q[e] = __builtin_bit_cast(uint32_t, f);
+    off = fmaxf(off, fabsf(__builtin_fmaf(x, inverse, MAGIC - f)));
   }
-  return top;
-}
-
-template <typename T>
-__device__ __forceinline__ u32x2 i8_packed(u32x4 v, float s, float inverse) {
-  u32x2 p = {0u, 0u};
+  if (!(off < NEAR)) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int q = i8_quantized(widen<T>((uint16_t)(v[e / 2] >> (16 * (e % 2)))), s, inverse);
-    p[e / 4] |= ((uint32_t)q & 0xffu) << (8 * (e % 4));
+    for (int e = 0; e < 8; ++e) q[e] = (uint32_t)i8_quantized(widen<T>((uint16_t)(v[e / 2] >> (16 * (e % 2)))), s, inverse);
   }
-  return p;
+  u32x2 p;
+#pragma unroll
+  for (int e = 0; e < 8; e += 4) {
+    const uint32_t lo = __builtin_amdgcn_perm(q[e + 1], q[e], 0x0c0c0400u), hi = __builtin_amdgcn_perm(q[e + 3], q[e + 2], 0x04000c0cu);
+    p[e / 4] = lo | hi;
+  }
+  return s == s ? p : u32x2{0u, 0u};
 }
 
-// Eight values of a row from k on, zeros from K on.
+// Eight values of a row from k on, zeros from K on (K at least eight).
 __device__ __forceinline__ u32x4 load_eight(const uint16_t *row, int k, int K) {
-  if (k + 8 <= K) return *reinterpret_cast<const u32x4_any *>(row + k);
-  return k < K ? load_tail(row, k, K) : u32x4{0u, 0u, 0u, 0u};
+  if (k >= K) return u32x4{0u, 0u, 0u, 0u};
+  const int at = k < K - 8 ? k : K - 8;
+  const u32x4 v = *reinterpret_cast<const u32x4_any *>(row + at);
+  return k > at ? drop_values(v, k - at) : v;
 }
 
-__device__ __forceinline__ float wave_largest(float top) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  return top;
+// Rows shorter than eight values, one a thread.
+template <typename T>
+__global__ void __launch_bounds__(256) quant_short_kernel(const uint16_t *__restrict__ x, int8_t *__restrict__ q,
+                                                          float *__restrict__ scale, int64_t M, int K) {
+  for (int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x; m < M; m += (int64_t)gridDim.x * 256) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (K > 0) v = load_tail(x + m * K, 0, K);
+    Largest top;
+    top.take(v);
+    const float s = i8_scale_of<T>(top.bits());
+    const u32x2 p = i8_packed<T>(v, s, 1.0f / s);
+    scale[m] = s;
+    if (K > 0) *reinterpret_cast<u32x4 *>(q + m * 16) = u32x4{p[0], p[1], 0u, 0u};
+  }
 }
 
-// A wave a row, kept in registers between its maximum and its integers where
-// it has up to 512 C values; longer rows are read twice.
-template <typename T, int C>
-__global__ void __launch_bounds__(256) quant_rows_kernel(const uint16_t *__restrict__ x, int8_t *__restrict__ q,
-                                                         float *__restrict__ scale, int64_t M, int K, int width) {
-  const int lane = threadIdx.x & 63;
-  for (int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); m < M; m += (int64_t)gridDim.x * 4) {
+// WAVES waves a row, which is kept in registers between its maximum and its
+// integers where it has up to 512 WAVES C values; longer rows are read twice.
+// Bound by memory.
+template <typename T, int WAVES, int C>
+__global__ void __launch_bounds__(256, 6) quant_rows_kernel(const uint16_t *__restrict__ x, int8_t *__restrict__ q,
+                                                            float *__restrict__ scale, int64_t M, int K, int width) {
+  constexpr int THREADS = WAVES * 64, ROWS = 4 / WAVES;  // of a workgroup
+  __shared__ uint32_t tops[2][4];
+  const int tid = threadIdx.x % THREADS, wave = threadIdx.x >> 6;
+  int turn = 0;
+  for (int64_t m0 = (int64_t)blockIdx.x * ROWS; m0 < M; m0 += (int64_t)gridDim.x * ROWS, turn ^= 1) {
+    const int64_t m = m0 + threadIdx.x / THREADS;
+    if (WAVES == 1 && m >= M) continue;
     const uint16_t *row = x + m * K;
     int8_t *to = q + m * width;
-    float top = 0.0f;
-    bool odd = false;
     u32x4 v[C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = load_eight(row, (i * 64 + lane) * 8, K);
+    for (int i = 0; i < C; ++i) v[i] = load_eight(row, (i * THREADS + tid) * 8, K);
+    Largest top;
 #pragma unroll
-    for (int i = 0; i < C; ++i) top = largest<T>(v[i], top, &odd);
-    for (int k = (C * 64 + lane) * 8; k < K; k += 512) top = largest<T>(load_eight(row, k, K), top, &odd);
-    const float s = i8_scale(__any(odd) ? INFINITY : wave_largest(top)), inverse = 1.0f / s;
-    if (lane == 0) scale[m] = s;
+    for (int i = 0; i < C; ++i) top.take(v[i]);
+    for (int k = (C * THREADS + tid) * 8; k < K; k += THREADS * 8) top.take(load_eight(row, k, K));
+    uint32_t bits = wave_largest(top.bits());
+    if constexpr (WAVES > 1) {
+      if ((threadIdx.x & 63) == 0) tops[turn][wave] = bits;
+      __syncthreads();  // one a turn: the next one's values go to the other half
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) bits = tops[turn][w] > bits ? tops[turn][w] : bits;
+    }
+    const float s = i8_scale_of<T>(bits), inverse = 1.0f / s;
+    if (tid == 0) scale[m] = s;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int k = (i * 64 + lane) * 8;
+      const int k = (i * THREADS + tid) * 8;
       if (k < width) *reinterpret_cast<u32x2 *>(to + k) = i8_packed<T>(v[i], s, inverse);
     }
-    for (int k = (C * 64 + lane) * 8; k < width; k += 512)
+    for (int k = (C * THREADS + tid) * 8; k < width; k += THREADS * 8)
       *reinterpret_cast<u32x2 *>(to + k) = i8_packed<T>(load_eight(row, k, K), s, inverse);
   }
 }
@@ -172,25 +226,24 @@ __global__ void __launch_bounds__(WAVES * 64) i8_few_kernel(I8Args a) {
     compiler_fence();  // the tokens first: waiting for them is then not waiting for the weights
     if (wave < blocks) job.begin(at);
     compiler_fence();
-    float *tops = reinterpret_cast<float *>(sums);  // [tokens][waves]
+    uint32_t *tops = reinterpret_cast<uint32_t *>(sums);  // [tokens][waves]
 #pragma unroll
     for (int m = 0; m < kI8OwnTokens; ++m) {
       if (m >= a.M) continue;
-      float top = 0.0f;
-      bool odd = false;
+      Largest top;
 #pragma unroll
-      for (int i = 0; i < C; ++i) top = largest<T>(v[m][i], top, &odd);
-      top = __any(odd) ? INFINITY : wave_largest(top);
-      if (lane == 0) tops[m * WAVES + wave] = top;
+      for (int i = 0; i < C; ++i) top.take(v[m][i]);
+      const uint32_t bits = wave_largest(top.bits());
+      if (lane == 0) tops[m * WAVES + wave] = bits;
     }
     lds_barrier();
 #pragma unroll
     for (int m = 0; m < kI8OwnTokens; ++m) {
       if (m >= a.M) continue;
-      float top = 0.0f;
+      uint32_t bits = 0;
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, tops[m * WAVES + w]);
-      const float s = i8_scale(top), inverse = 1.0f / s;
+      for (int w = 0; w < WAVES; ++w) bits = tops[m * WAVES + w] > bits ? tops[m * WAVES + w] : bits;
+      const float s = i8_scale_of<T>(bits), inverse = 1.0f / s;
       if (tid == 0) scales[m] = s;
 #pragma unroll
       for (int i = 0; i < C; ++i) {

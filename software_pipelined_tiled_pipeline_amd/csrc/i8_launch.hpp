@@ -10,14 +10,17 @@ namespace launch_detail {
 template <typename T>
 pgemm_status quant_rows(const uint16_t *x, int8_t *q, float *scale, int64_t M, int64_t K, hipStream_t stream) {
   if (M == 0) return PGEMM_OK;
-  const unsigned grid = row_grid(M * 64);
   const int k = (int)K, width = (int)i8_width(K);
-  if (K <= 1024)
-    hipLaunchKernelGGL((quant_rows_kernel<T, 2>), dim3(grid), dim3(256), 0, stream, x, q, scale, M, k, width);
+  const int64_t groups = K <= 1024 ? per(M, 4) : M;
+  const dim3 grid((unsigned)(groups < 16384 ? groups : 16384));
+  if (K < 8) {
+    hipLaunchKernelGGL(quant_short_kernel<T>, dim3(row_grid(M)), dim3(256), 0, stream, x, q, scale, M, k);
+  } else if (K <= 1024)
+    hipLaunchKernelGGL((quant_rows_kernel<T, 1, 2>), grid, dim3(256), 0, stream, x, q, scale, M, k, width);
   else if (K <= 4096)
-    hipLaunchKernelGGL((quant_rows_kernel<T, 8>), dim3(grid), dim3(256), 0, stream, x, q, scale, M, k, width);
+    hipLaunchKernelGGL((quant_rows_kernel<T, 4, 2>), grid, dim3(256), 0, stream, x, q, scale, M, k, width);
   else
-    hipLaunchKernelGGL((quant_rows_kernel<T, 16>), dim3(grid), dim3(256), 0, stream, x, q, scale, M, k, width);
+    hipLaunchKernelGGL((quant_rows_kernel<T, 4, 4>), grid, dim3(256), 0, stream, x, q, scale, M, k, width);
   return launched();
 }
 

@@ -9,8 +9,7 @@
 // Logits of 16 bits have few values, so that every such sum is one over values
 // and not over tokens: a row is counted by value, and a value's share is its
 // count times one exponential.  Counts do not depend on the order of their
-// atomics, and all sums are in 64 bits.  LDS holds the counts of kWindow values
-// in order, from the largest down; rows that reach further take the next window.
+// atomics, and all sums are in 64 bits.
 #pragma once
 
 #include "fused_launch.hpp"
@@ -30,248 +29,509 @@ struct SampleArgs {
 };
 
 constexpr int kSampleThreads = 1024, kSampleWaves = kSampleThreads / 64;
-constexpr int kSampleGroups = 576;                 // of 64 values each
-constexpr int kWindow = kSampleGroups * 64;        // 144 KiB of counts
+// LDS holds the counts of all values there are, two of 16 bits in a dword: a
+// thread has a block of 64 values that lie together, whose first and second
+// halves share 32 dwords.  These are in an order of the block's own, so that a
+// wave's reads fall on different banks.  A row with more than 65535 logits of
+// one value is counted in 32 bits instead, in windows of 32 values a thread.
+constexpr int kWindow = 32 * kSampleThreads;  // 128 KiB
 struct SampleShared {
   uint32_t count[kWindow];
-  double mass[kSampleGroups];   // sums up to and with the group
-  uint32_t held[kSampleGroups];
+  double mass[kSampleThreads];  // sums up to and with the thread's values
+  uint32_t held[kSampleThreads];
+  double root[32];              // 2^(i / 32)
+  double wave_mass[kSampleWaves];
   uint32_t waves[kSampleWaves], more[kSampleWaves];
+  int first[kSampleWaves];
   double answer_mass;
   int64_t answer_n, below;
-  uint32_t answer_key, answer_in;
+  int answer_key;
+  uint32_t answer_in, found;
 };
 
-// A logit's place in the order of its type's values: 16 bits, 0 for a NaN.
-template <typename T>
-__device__ __forceinline__ uint32_t sample_key(uint32_t bits) {
-  constexpr uint32_t INF = std::is_same_v<T, _Float16> ? 0x7C00u : 0x7F80u;
-  if ((bits & 0x7FFFu) > INF) return 0;
-  if (bits == 0x8000u) bits = 0;
-  return bits & 0x8000u ? 0xFFFFu - bits : bits | 0x8000u;
+// Sums over the lanes up to each one, by moves within a row of 16 lanes and
+// from a row's last lane to the rows after it.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t lane_move(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double lane_move(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = lane_move<CTRL, ROWS>((uint32_t)b), hi = lane_move<CTRL, ROWS>((uint32_t)(b >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double read_lane(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <typename U>
+__device__ __forceinline__ U wave_scan(U v) {
+  v += lane_move<0x111, 0xf>(v);
+  v += lane_move<0x112, 0xf>(v);
+  v += lane_move<0x114, 0xf>(v);
+  v += lane_move<0x118, 0xf>(v);
+  v += lane_move<0x142, 0xa>(v);
+  v += lane_move<0x143, 0xc>(v);
+  return v;
+}
+
+// e^d for d <= 0 in 64 bits: 2^(n/32) from a table times a polynomial of what
+// is left, |r| <= ln 2 / 64 (P. T. P. Tang, "Table-driven implementation of the
+// exponential function in IEEE floating-point arithmetic", 1989).
+__device__ __forceinline__ double sample_exp(double d, const double *root) {
+  if (!(d >= -744.0)) return 0.0;  // a NaN too: no share
+  const double n = __builtin_rint(d * 46.166241308446828384);         // 32 / ln 2
+  double r = __builtin_fma(n, -0x1.62e42fefp-6, d);                   // ln 2 / 32: its first 33 bits,
+  r = __builtin_fma(n, -0x1.473de6af278edp-39, r);                    // and the rest
+  double p = 1.0 / 120.0;  // up to r^5: 2^-48 of the result
+  p = __builtin_fma(p, r, 1.0 / 24.0);
+  p = __builtin_fma(p, r, 1.0 / 6.0);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  const int i = (int)n;
+  const double f = root[i & 31];
+  return __builtin_ldexp(__builtin_fma(f * r, p, f), i >> 5);
+}
+
+// A logit's place in the order of its type's values is its magnitude's bits, or
+// less them; minus zero has zero's.  Two logits a dword.
+typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ i16x2 sample_keys(uint32_t two) {
+  const i16x2 v = __builtin_bit_cast(i16x2, two), sign = v >> 15;
+  return (__builtin_bit_cast(i16x2, two & 0x7FFF7FFFu) ^ sign) - sign;
 }
 template <typename T>
-__device__ __forceinline__ double sample_value(uint32_t key) {
-  const uint32_t bits = key & 0x8000u ? key & 0x7FFFu : 0xFFFFu - key;
-  return (double)widen<T>((uint16_t)bits);
+__device__ __forceinline__ double sample_value(int key) {
+  return (double)widen<T>((uint16_t)(key < 0 ? 0x8000 - key : key));
 }
-// minus infinity's
+// minus infinity's, which is the lowest where there is no NaN
 template <typename T>
-constexpr uint32_t kLowestKey = std::is_same_v<T, _Float16> ? 0xFFFFu - 0xFC00u : 0xFFFFu - 0xFF80u;
+constexpr int kLowestKey = std::is_same_v<T, _Float16> ? -0x7C00 : -0x7F80;
+
+struct SampleSettings {
+  float u, top_p, min_p;
+  int k;
+};
 
 template <typename T>
 struct Sampler {
   SampleShared &s;
   const uint16_t *row;
   int V, tid, lane, wave;
-  uint32_t top;      // the largest logit's key
+  int top;                // the largest logit's key
   double largest, slope;  // its value; 1 / temperature
-  int window;        // which one is counted
+  int window;             // which one is counted
 
-  // f(key, index) of all logits, 16 bytes a thread at a time.
-  template <typename F>
-  __device__ __forceinline__ void each(F &&f) const {
-    for (int base = tid * 8; base < V; base += kSampleThreads * 8) {
-      if (base + 8 <= V) {
-        const u32x4 v = *reinterpret_cast<const u32x4_any *>(row + base);
+  // Eight logits from an index on; minus infinity past the row's end.
+  __device__ __forceinline__ u32x4 eight(int base) const {
+    constexpr uint32_t LOW = std::is_same_v<T, _Float16> ? 0xFC00FC00u : 0xFF80FF80u;
+    u32x4 v = {LOW, LOW, LOW, LOW};
+    if (base + 8 <= V) {
+      v = *reinterpret_cast<const u32x4_any *>(row + base);
+    } else if (base < V) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f(sample_key<T>((v[e / 2] >> (16 * (e % 2))) & 0xFFFFu), base + e);
-      } else {
-        for (int e = base; e < V; ++e) f(sample_key<T>(row[e]), e);
-      }
+      for (int e = 0; e < 8; ++e)
+        if (base + e < V) v[e / 2] = e % 2 ? (v[e / 2] & 0xFFFFu) | (uint32_t)row[base + e] << 16 : (v[e / 2] & 0xFFFF0000u) | row[base + e];
+    }
+    return v;
+  }
+  // f of eight logits and their first one's index, over a run of the row by threads `first`, first + step, ..;
+  // U loads are on the way at once.
+  template <int U, typename F>
+  __device__ __forceinline__ void each(int from, int to, int first, int step, F &&f) const {
+    for (int base = from + first * 8; base < to; base += U * step * 8) {
+      u32x4 v[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) v[i] = eight(base + i * step * 8 < to ? base + i * step * 8 : V);
+#pragma unroll
+      for (int i = 0; i < U; ++i) f(v[i], base + i * step * 8);
     }
   }
 
-  __device__ __forceinline__ double share(uint32_t key) const {
-    const double v = sample_value<T>(key);
-    if (v == largest) return 1.0;
-    const double d = (v - largest) * slope;
-    return d < 0.0 ? exp(d) : d == 0.0 ? 1.0 : 0.0;  // a NaN: an infinite largest one, at an infinite temperature
+  __device__ __forceinline__ double share(int key) const {
+    if (key >= top) return 1.0;  // (above it there is no logit)
+    const double d = (sample_value<T>(key) - largest) * slope;
+    return d < 0.0 ? sample_exp(d, s.root) : d == 0.0 ? 1.0 : 0.0;  // a NaN: an infinite largest one, at an infinite temperature
   }
-  // the key of place i of the counted window; negative: past the last value
-  __device__ __forceinline__ int key_at(int i) const { return (int)top - window * kWindow - i; }
+  // How values lie in the counts: in blocks of `bins` a thread from `start` down.
+  bool packed;
+  int bins, start;
+  __device__ __forceinline__ int key_at(int block, int i) const { return start - block * bins - i; }
+  __device__ __forceinline__ uint32_t count_at(int block, int i) const {
+    const uint32_t v = s.count[block * 32 + ((i ^ block) & 31)];
+    return packed ? v >> (i >> 5 << 4) & 0xFFFFu : v;
+  }
 
-  // Counts window w and adds the shares of its groups up.
-  __device__ __forceinline__ void count(int w) {
-    window = w;
-    __syncthreads();
-    for (int i = tid; i < kWindow; i += kSampleThreads) s.count[i] = 0;
-    if (tid == 0) s.below = 0;
-    __syncthreads();
-    const int first = (int)top - w * kWindow;
-    uint32_t below = 0;
-    each([&](uint32_t key, int) {
-      const int i = first - (int)key;
-      if (key > kLowestKey<T> && i >= 0) {
-        if (i < kWindow)
-          atomicAdd(&s.count[i], 1u);
-        else
-          ++below;
-      }
-    });
+  __device__ __forceinline__ void clear() const {
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) below += (uint32_t)__shfl_xor((int)below, d);
-    if (lane == 0) s.more[wave] = below;
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<u32x4 *>(s.count + (i * kSampleThreads + tid) * 4) = u32x4{0u, 0u, 0u, 0u};
+  }
+
+  // Counts the whole row, whose counts are clear, in 16 bits, from the largest
+  // key there is down, and finds the largest logit; false if there is nothing to
+  // take, or a NaN.  Minus infinity, which may be most of a row, is left out.
+  __device__ __forceinline__ bool count_all() {
+    packed = true;
+    window = 0;
+    bins = 64;
+    start = 0x7FFF;
+    if (tid == 0) s.found = 0;
     __syncthreads();
-    for (int g = wave; g < kSampleGroups; g += kSampleWaves) {
-      uint32_t n = s.count[g * 64 + lane];
-      double m = 0.0;
-      if (__any(n != 0)) m = n ? (double)n * share((uint32_t)key_at(g * 64 + lane)) : 0.0;
+    uint32_t taken = 0;
+    each<8>(0, V, tid, kSampleThreads, [&](const u32x4 &v, int) {
+      i16x2 key[4], low = {0x7FFF, 0x7FFF};
 #pragma unroll
-      for (int d = 32; d > 0; d >>= 1) {
-        n += (uint32_t)__shfl_xor((int)n, d);
-        m += __shfl_xor(m, d);
+      for (int d = 0; d < 4; ++d) {
+        key[d] = sample_keys(v[d]);
+        low = __builtin_elementwise_min(low, key[d]);
       }
-      if (lane == 0) {
-        s.held[g] = n;
-        s.mass[g] = m;
-      }
-    }
-    __syncthreads();
-    if (wave == 0) {
-      constexpr int PER = kSampleGroups / 64;
-      uint32_t n = 0;
-      double m = 0.0;
+      const bool some = low[0] <= kLowestKey<T> || low[1] <= kLowestKey<T>;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        n += s.held[lane * PER + i];
-        m += s.mass[lane * PER + i];
-      }
-      uint32_t before = n;
-      double before_m = m;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t a = (uint32_t)__shfl_up((int)before, d);
-        const double b = __shfl_up(before_m, d);
-        if (lane >= d) {
-          before += a;
-          before_m += b;
+      for (int d = 0; d < 4; ++d) {
+        // two places p = 0x7FFF - key; their dwords, p / 64 * 32 + (p ^ p / 64) % 32; 16 for the second half
+        const u16x2 p = __builtin_bit_cast(u16x2, i16x2{0x7FFF, 0x7FFF} - key[d]);
+        const uint32_t mixed = __builtin_bit_cast(uint32_t, p ^ (p >> 6)), half = __builtin_bit_cast(uint32_t, p >> 1);
+        const uint32_t word = (mixed & 0x001F001Fu) | (half & 0x7FE07FE0u), shift = half & 0x00100010u;
+        if (!some || key[d][0] > kLowestKey<T>) atomicAdd(&s.count[word & 0xFFFFu], 1u << (shift & 31u));
+        if (!some || key[d][1] > kLowestKey<T>) atomicAdd(&s.count[word >> 16], 1u << (shift >> 16));
+        if (some) {
+          taken += (key[d][0] > kLowestKey<T>) + (key[d][1] > kLowestKey<T>);
+          if (key[d][0] < kLowestKey<T> || key[d][1] < kLowestKey<T>) s.found = 1;  // a NaN with a sign
         }
       }
-      n = before - n;
-      m = __shfl_up(before_m, 1);
-      if (lane == 0) m = 0.0;
+      if (!some) taken += 8;
+    });
+    __syncthreads();
+    uint32_t n = 0;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t c = s.count[tid * 32 + ((i ^ tid) & 31)];
+      n += (c & 0xFFFFu) + (c >> 16);
+    }
+    const uint64_t here = __ballot(n != 0);
+    if (lane == 0) s.first[wave] = here ? wave * 64 + __builtin_ctzll(here) : kSampleThreads;
+    __syncthreads();
+    int g = kSampleThreads;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        n += s.held[lane * PER + i];
-        m += s.mass[lane * PER + i];
-        s.held[lane * PER + i] = n;
-        s.mass[lane * PER + i] = m;
+    for (int i = 0; i < kSampleWaves; ++i) g = s.first[i] < g ? s.first[i] : g;
+    g = __builtin_amdgcn_readfirstlane(g);
+    if (g == kSampleThreads || s.found) return false;
+    const uint64_t held = __ballot(count_at(g, lane) != 0);
+    const int j0 = (int)__builtin_ctzll(held);  // (a count that ran over may have left a zero, but not in all of a block)
+    top = key_at(g, j0);
+    if (top > -kLowestKey<T>) return false;  // a NaN
+    largest = sample_value<T>(top);
+
+    // The shares of a block's values, equally far apart, as a polynomial of their
+    // ratio, a count and a product each.  (A block's keys are 64 q to 64 q + 63;
+    // binades begin at multiples of 64, and the last value before one, or the first
+    // of the next, is as far away as the others.)
+    double m = 0.0;
+    if (__any(n != 0)) {
+      const int key = key_at(tid, 0);
+      const double r = sample_exp((sample_value<T>(key - 1) - sample_value<T>(key)) * slope, s.root);
+      double far = 0.0, r32 = r;
+#pragma unroll 8
+      for (int i = 31; i >= 0; --i) {
+        const uint32_t c = s.count[tid * 32 + ((i ^ tid) & 31)];
+        m = __builtin_fma(m, r, (double)(c & 0xFFFFu));
+        far = __builtin_fma(far, r, (double)(c >> 16));
       }
-      if (lane == 0) {
-        int64_t all = 0;
-        for (int i = 0; i < kSampleWaves; ++i) all += s.more[i];
-        s.below = all;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) r32 *= r32;
+      m = __builtin_fma(far, r32, m);
+      // (the block of the largest logit may begin above it)
+      const double d = (sample_value<T>(key) - largest) * slope;
+      m = n ? m * (d == 0.0 ? 1.0 : sample_exp(d, s.root)) : 0.0;
+      if (wave == g >> 6 && !(read_lane(d, g & 63) < 600.0)) {  // where that leaves the range: one value a lane
+        const uint32_t c = count_at(g, lane);
+        const double of_g = read_lane(wave_scan(c ? (double)c * share(key_at(g, lane)) : 0.0), 63);
+        if (tid == g) m = of_g;
       }
     }
+    // A count that runs over takes 2^16 from itself and adds at most one elsewhere: the counts' sum is then too small,
+    // modulo 2^32 too, since a row has fewer logits.
+    add_up(n, m, taken - n);
+    if (V > 0xFFFF && s.below != 0) {
+      packed = false;
+      return find_top();
+    }
+    return true;
+  }
+
+  // The largest logit by reading the row; false as count_all.
+  __device__ __forceinline__ bool find_top() {
+    i16x2 most = {-0x7FFF, -0x7FFF};
+    u16x2 magnitude = {0, 0};
+    each<8>(0, V, tid, kSampleThreads, [&](const u32x4 &v, int) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        most = __builtin_elementwise_max(most, sample_keys(v[d]));
+        magnitude = __builtin_elementwise_max(magnitude, __builtin_bit_cast(u16x2, v[d] & 0x7FFF7FFFu));
+      }
+    });
+    int t = most[0] > most[1] ? most[0] : most[1];
+    if ((magnitude[0] > magnitude[1] ? magnitude[0] : magnitude[1]) > -kLowestKey<T>) t = 0x10000;  // a NaN
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      const int o = __shfl_xor(t, d);
+      t = o > t ? o : t;
+    }
     __syncthreads();
+    if (lane == 0) s.first[wave] = t;
+    __syncthreads();
+    for (int w = 0; w < kSampleWaves; ++w) t = s.first[w] > t ? s.first[w] : t;
+    top = __builtin_amdgcn_readfirstlane(t);
+    largest = sample_value<T>(top);
+    return top <= 0x7FFF && top > kLowestKey<T>;
+  }
+
+  __device__ __forceinline__ void add_up(uint32_t n, double m, uint32_t below) {
+    const uint32_t with = wave_scan(n);
+    const double with_m = wave_scan(m);
+    below = wave_scan(below);
+    if (lane == 63) {
+      s.waves[wave] = with;
+      s.wave_mass[wave] = with_m;
+      s.more[wave] = below;
+    }
+    __syncthreads();
+    const int i = lane < kSampleWaves ? lane : kSampleWaves - 1;
+    const uint32_t upto = wave_scan(s.waves[i]);
+    const double upto_m = wave_scan(s.wave_mass[i]);
+    int64_t more = 0;
+    if (wave == 0) {
+#pragma unroll
+      for (int w = 0; w < kSampleWaves; ++w) more += s.more[w];
+    }
+    const int last = wave > 0 ? wave - 1 : 0;
+    const uint32_t before = wave > 0 ? (uint32_t)__builtin_amdgcn_readlane((int)upto, last) : 0u;
+    const double before_m = wave > 0 ? read_lane(upto_m, last) : 0.0;
+    s.held[tid] = before + with;
+    s.mass[tid] = before_m + with_m;
+    if (tid == 0) s.below = packed ? (int64_t)(uint32_t)more : more;
+    __syncthreads();
+  }
+
+  // Counts window w in 32 bits.
+  __device__ __forceinline__ void count_window(int w) {
+    __syncthreads();
+    clear();
+    packed = false;
+    window = w;
+    bins = 32;
+    start = top - w * kWindow;
+    __syncthreads();
+    const uint32_t skip = (uint32_t)w * kWindow, all = (uint32_t)(top - kLowestKey<T>) - skip;
+    const uint32_t inside = all < (uint32_t)kWindow ? all : (uint32_t)kWindow;
+    const i16x2 tops = {(int16_t)top, (int16_t)top};
+    uint32_t below = 0;
+    each<4>(0, V, tid, kSampleThreads, [&](const u32x4 &v, int) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const uint32_t two = __builtin_bit_cast(uint32_t, tops - sample_keys(v[d]));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t i = (h ? two >> 16 : two & 0xFFFFu) - skip;
+          if (i < inside)
+            atomicAdd(&s.count[(i & ~31u) | ((i ^ i >> 5) & 31u)], 1u);
+          else if (i < all)  // (places of the windows before this one have wrapped to the far end)
+            ++below;
+        }
+      }
+    });
+    __syncthreads();
+    uint32_t n = 0;
+    double m = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t c = count_at(tid, i);
+      if (c) {
+        n += c;
+        m = __builtin_fma((double)c, share(key_at(tid, i)), m);
+      }
+    }
+    add_up(n, m, below);
   }
 
   struct Found {
     int64_t n;    // tokens up to and with it
     double mass;  // their sum
-    uint32_t key;
+    int key;
     uint32_t in;  // which of its value's tokens it is, from 1
   };
 
   enum class What { Count, Reaches, Passes, Under };
 
-  // The first token with n >= count, with S_n >= mass, with S_n > mass, or the
-  // last before the first with e_i < mass; the row's last one if there is none.
-  template <What W>
-  __device__ __forceinline__ Found find(int64_t want, double mass) {
-    int64_t n0 = 0;
-    double m0 = 0.0;
+  // In the counted window, after n0 tokens of sum m0: the first token with
+  // n >= want, with S_n >= mass, with S_n > mass, or the last before the first
+  // with e_i < mass.  False, with what the window holds added, if there is none.
+  // For one wave alone.
+  __device__ __forceinline__ bool search(What what, int64_t want, double mass, Found *f) const {
+    const int64_t n0 = f->n;
+    const double m0 = f->mass;
+    auto there = [&](int64_t n, double m, int key) {
+      if (what == What::Count) return n0 + n >= want;
+      if (what == What::Reaches) return m0 + m >= mass;
+      if (what == What::Passes) return m0 + m > mass;
+      return key <= kLowestKey<T> || share(key) < mass;
+    };
+    // blocks by sixteens, one of sixteen, one of its values
+    auto block_there = [&](int g) { return there(s.held[g], s.mass[g], key_at(g, bins - 1)); };
+    uint64_t hit = __ballot(block_there(lane * 16 + 15));
+    if (hit == 0) {
+      f->n = n0 + s.held[kSampleThreads - 1];
+      f->mass = m0 + s.mass[kSampleThreads - 1];
+      f->in = 0;
+      return false;
+    }
+    const int some = __builtin_ctzll(hit) * 16;
+    hit = __ballot(lane < 16 && block_there(some + (lane & 15)));
+    const int g = some + (hit ? __builtin_ctzll(hit) : 15);
+    const int key = key_at(g, lane);
+    const uint32_t c = lane < bins ? count_at(g, lane) : 0u;
+    const double e = c ? share(key) : 0.0;
+    const uint32_t n = wave_scan(c);
+    const double m = wave_scan((double)c * e);
+    const int64_t bn = g ? s.held[g - 1] : 0;
+    const double bm = g ? s.mass[g - 1] : 0.0;
+    hit = __ballot(lane < bins && there(bn + n, bm + m, key) && (c != 0 || what == What::Under));
+    // the block's sum and its values' may round to either side of the border: its last value then
+    const uint64_t any = __ballot(c != 0);
+    const int at = hit ? __builtin_ctzll(hit) : any ? 63 - __builtin_clzll(any) : bins - 1;
+    const uint32_t count = (uint32_t)__builtin_amdgcn_readlane((int)c, at);
+    const int64_t nb = n0 + bn + (uint32_t)__builtin_amdgcn_readlane((int)n, at) - count;  // tokens of the values before
+    const double one = read_lane(e, at);
+    const double mb = m0 + bm + read_lane(m, at) - (double)count * one;
+    uint32_t in = count;
+    if (what == What::Count) {
+      in = (uint32_t)(want - nb);
+    } else if (what == What::Under) {
+      in = 0;
+    } else if (one > 0.0) {
+      const double k = (mass - mb) / one;
+      const double r = what == What::Reaches ? ceil(k) : floor(k) + 1.0;
+      in = r < 1.0 ? 1u : r > (double)count ? count : (uint32_t)r;
+    }
+    *f = Found{nb + in, mb + (double)in * one, key_at(g, at), in};
+    return true;
+  }
+
+  // What top_k leaves, the whole row without it; what top_p, and min_p, leave of
+  // that; the token; and if rounding put it past what is kept, the last of that.
+  template <typename F>
+  __device__ __forceinline__ static Found choose(const SampleSettings &set, F &&find) {
+    Found kept{0, 0.0, 0, 0}, f{0, 0.0, 0, 0};
+    double all = 0.0;
+#pragma unroll 1
+    for (int step = 0; step < 5; ++step) {
+      if (step == 1 && !(set.top_p < 1.0f)) continue;
+      if (step == 2 && !(set.min_p > 0.0f)) continue;
+      if (step == 4 && f.in != 0 && f.n <= kept.n) break;
+      const What what = step == 1 ? What::Reaches : step == 2 ? What::Under : step == 3 ? What::Passes : What::Count;
+      const int64_t want = step == 4 ? kept.n : set.k > 0 ? set.k : INT64_MAX;
+      f = find(what, want, step == 1 ? (double)set.top_p * all : step == 2 ? (double)set.min_p : (double)set.u * kept.mass);
+      if (step == 0) all = f.mass;
+      if (step == 0 || (step < 3 && f.n < kept.n)) kept = f;
+    }
+    return f;
+  }
+
+  // The same over all windows, for the whole workgroup.
+  __device__ __forceinline__ Found find(What what, int64_t want, double mass) {
+    Found f{0, 0.0, 0, 0};
     for (int w = 0;; ++w) {
-      if (w != window) count(w);
+      if (w != window) count_window(w);
       if (wave == 0) {
-        auto there = [&](int64_t n, double m, int place) {
-          if (W == What::Count) return n0 + n >= want;
-          if (W == What::Reaches) return m0 + m >= mass;
-          if (W == What::Passes) return m0 + m > mass;
-          const int key = key_at(place);
-          return key <= (int)kLowestKey<T> || share((uint32_t)key) < mass;
-        };
-        int g = -1;
-        for (int base = 0; base < kSampleGroups && g < 0; base += 64) {
-          const uint64_t hit = __ballot(there(s.held[base + lane], s.mass[base + lane], (base + lane) * 64 + 63));
-          if (hit) g = base + __builtin_ctzll(hit);
-        }
-        Found f{n0 + s.held[kSampleGroups - 1], m0 + s.mass[kSampleGroups - 1], 0, 0};
-        if (g >= 0) {
-          const uint32_t c = s.count[g * 64 + lane];
-          const int key = key_at(g * 64 + lane);
-          const double e = c ? share((uint32_t)key) : 0.0;
-          uint32_t n = c;
-          double m = (double)c * e;
-#pragma unroll
-          for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t a = (uint32_t)__shfl_up((int)n, d);
-            const double b = __shfl_up(m, d);
-            if (lane >= d) {
-              n += a;
-              m += b;
-            }
-          }
-          const int64_t bn = g ? s.held[g - 1] : 0;
-          const double bm = g ? s.mass[g - 1] : 0.0;
-          const uint64_t hit = __ballot(there(bn + n, bm + m, g * 64 + lane) && (c != 0 || W == What::Under));
-          // the group's sum and its values' may round to either side of the border: its last value then
-          const uint64_t any = __ballot(c != 0);
-          const int at = hit ? __builtin_ctzll(hit) : any ? 63 - __builtin_clzll(any) : 63;
-          const uint32_t here = (uint32_t)__shfl((int)c, at);
-          const int64_t nb = n0 + bn + (uint32_t)__shfl((int)n, at) - here;  // tokens of the values before
-          const double one = __shfl(e, at);
-          const double mb = m0 + bm + __shfl(m, at) - (double)here * one;
-          uint32_t in = here;
-          if (W == What::Count) {
-            in = (uint32_t)(want - nb);
-          } else if (W == What::Under) {
-            in = 0;
-          } else if (one > 0.0) {
-            const double k = (mass - mb) / one;
-            const double r = W == What::Reaches ? ceil(k) : floor(k) + 1.0;
-            in = r < 1.0 ? 1u : r > (double)here ? here : (uint32_t)r;
-          }
-          f = Found{nb + in, mb + (double)in * one, (uint32_t)__shfl(key, at), in};
-        }
+        const bool found = search(what, want, mass, &f);
         if (lane == 0) {
           s.answer_n = f.n;
           s.answer_mass = f.mass;
           s.answer_key = f.key;
-          s.answer_in = g >= 0 ? f.in + 1 : 0;
+          s.answer_in = f.in;
+          s.found = found;
         }
       }
       __syncthreads();
-      const Found f{s.answer_n, s.answer_mass, s.answer_key, s.answer_in ? s.answer_in - 1 : 0};
-      const bool over = s.answer_in != 0 || s.below == 0;
+      f = Found{s.answer_n, s.answer_mass, s.answer_key, s.answer_in};
+      const bool over = s.found != 0 || s.below == 0;
       __syncthreads();
       if (over) return f;
-      n0 = f.n;
-      m0 = f.mass;
     }
   }
 
-  // The index of the `which`-th logit with a key, from 1.
-  __device__ __forceinline__ int place_of(uint32_t key, uint32_t which) {
-    const int share = (V + kSampleWaves * 64 - 1) / (kSampleWaves * 64) * 64;  // a wave's run
-    const int from = wave * share, to = from + share < V ? from + share : V;
-    uint32_t n = 0;
-    for (int base = from; base < to; base += 64)
-      n += (uint32_t)__popcll(__ballot(base + lane < to && sample_key<T>(row[base + lane]) == key));
+  // The index of the `which`-th logit with a key, from 1.  The logits with it are
+  // listed in the order of their atomics, and the one that has which - 1 of them
+  // before it is taken; more than a thread has room for are counted by runs of the row
+  // instead.
+  __device__ __forceinline__ int place_of(int key, uint32_t which) {
+    uint32_t *list = s.count;  // done with
+    const uint32_t bits = (uint32_t)(key < 0 ? 0x8000 - key : key) * 0x10001u;
+    const uint32_t mask = key == 0 ? 0x7FFF7FFFu : 0xFFFFFFFFu;  // either zero
     __syncthreads();
-    if (lane == 0) s.waves[wave] = n;
-    if (tid == 0) s.answer_n = -1;
+    if (tid == 0) s.found = 0;
+    __syncthreads();
+    each<8>(0, V, tid, kSampleThreads, [&](const u32x4 &v, int base) {
+      uint32_t t[4];
+      u16x2 least = {0xFFFF, 0xFFFF};
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        t[d] = (v[d] ^ bits) & mask;
+        least = __builtin_elementwise_min(least, __builtin_bit_cast(u16x2, t[d]));
+      }
+      if (least[0] == 0 || least[1] == 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (((t[e / 2] >> (16 * (e % 2))) & 0xFFFFu) == 0 && base + e < V) {
+            const uint32_t at = atomicAdd(&s.found, 1u);
+            if (at < kSampleThreads) list[at] = (uint32_t)(base + e);
+          }
+      }
+    });
+    __syncthreads();
+    const uint32_t n = s.found;
+    if (n <= kSampleThreads) {
+      if (n == 1) return (int)list[0];
+      if (tid < (int)n) {
+        const uint32_t mine = list[tid];
+        uint32_t before = 0;
+        for (uint32_t i = 0; i < n; ++i) before += list[i] < mine;
+        if (before + 1 == which) s.answer_n = mine;
+      }
+      __syncthreads();
+      return (int)s.answer_n;
+    }
+    const int run = (V + kSampleWaves * 512 - 1) / (kSampleWaves * 512) * 512;  // a wave's, below 2^27
+    const int from = wave * run, to = V - from < run ? V : from + run;
+    auto matches = [&](const u32x4 &v, int base, int e) {
+      return (((v[e / 2] ^ bits) & mask) >> (16 * (e % 2)) & 0xFFFFu) == 0 && base + e < to;
+    };
+    uint32_t ours = 0;
+    each<8>(from, to, lane, 64, [&](const u32x4 &v, int base) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ours += matches(v, base, e);
+    });
+    ours = wave_scan(ours);
+    if (lane == 63) s.waves[wave] = ours;
     __syncthreads();
     uint32_t before = 0;
     for (int w = 0; w < wave; ++w) before += s.waves[w];
-    if (before < which && which <= before + n) {
-      for (int base = from; base < to; base += 64) {
-        const bool is = base + lane < to && sample_key<T>(row[base + lane]) == key;
-        const uint64_t who = __ballot(is);
-        const uint32_t mine = before + (uint32_t)__popcll(who & ((2ull << lane) - 1));
-        if (is && mine == which) s.answer_n = base + lane;
-        before += (uint32_t)__popcll(who);
+    if (before < which && which <= before + s.waves[wave]) {
+      for (int base = from + lane * 8; base - lane * 8 < to; base += 512) {
+        const u32x4 v = eight(base);
+        uint32_t mine = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mine += matches(v, base, e);
+        const uint32_t with = wave_scan(mine);
+        uint32_t at = before + with - mine;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (matches(v, base, e) && ++at == which) s.answer_n = base + e;
+        before += (uint32_t)__shfl((int)with, 63);
       }
     }
     __syncthreads();
@@ -279,11 +539,27 @@ struct Sampler {
   }
 };
 
+// A row whose counts do not fit 16 bits, for the whole workgroup; a function of
+// its own, so that its registers are not the other rows' too.
+template <typename T>
+__device__ __attribute__((noinline)) void sample_wide(SampleShared &s, const uint16_t *logits, int V, int top, double slope,
+                                                      SampleSettings set) {
+  const int tid = threadIdx.x;
+  Sampler<T> row{s, logits, V, tid, tid & 63, tid >> 6, top, sample_value<T>(top), slope, -1, false, 0, 0};
+  const auto f = row.choose(set, [&](auto what, int64_t want, double mass) { return row.find(what, want, mass); });
+  if (tid == 0) {
+    s.answer_key = f.key;
+    s.answer_in = f.in;
+  }
+  __syncthreads();
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kSampleThreads) sample_kernel(SampleArgs a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   SampleShared &s = *reinterpret_cast<SampleShared *>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (tid < 32) s.root[tid] = exp2((double)tid / 32.0);
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     auto at = [&](int bit) { return a.shared & bit ? 0 : m; };
     const float u = a.u[m];
@@ -292,52 +568,46 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(SampleArgs a) {
     const float top_p = a.top_p ? a.top_p[at(PGEMM_SAMPLE_TOP_P)] : 1.0f;
     const float min_p = a.min_p ? a.min_p[at(PGEMM_SAMPLE_MIN_P)] : 0.0f;
 
-    Sampler<T> row{s, a.logits + m * a.V, a.V, tid, lane, wave, 0, 0.0, 1.0, -1};
-    uint32_t top = 0, odd = 0;
-    row.each([&](uint32_t key, int) {
-      top = key > top ? key : top;
-      odd |= key == 0;
-    });
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-      const uint32_t o = (uint32_t)__shfl_xor((int)top, d);
-      top = o > top ? o : top;
+    Sampler<T> row{s, a.logits + m * a.V, a.V, tid, lane, wave, 0, 0.0, 1.0, -1, false, 0, 0};
+    const bool first = t == 0.0f || top_p <= 0.0f || min_p > 1.0f || k == 1;  // nothing to choose
+    row.slope = 1.0 / (double)t;
+    bool good = t >= 0.0f && top_p == top_p && min_p == min_p && u == u;
+    if (good) {
+      if (first) {
+        good = row.find_top();
+      } else {
+        row.clear();
+        good = row.count_all();
+      }
     }
-    __syncthreads();
-    if (__any(odd)) top = 0x10000u;
-    if (lane == 0) s.waves[wave] = top;
-    __syncthreads();
-    top = 0;
-    for (int w = 0; w < kSampleWaves; ++w) top = s.waves[w] > top ? s.waves[w] : top;
-    const bool none = top > 0xFFFFu || top <= kLowestKey<T> || !(t >= 0.0f) || top_p != top_p || min_p != min_p || u != u;
-    if (none) {
+    if (!good) {
       if (tid == 0) a.token[m] = -1;
       __syncthreads();
       continue;
     }
-    row.top = top;
-    row.largest = sample_value<T>(top);
-    uint32_t key = top, in = 1;
-    if (t > 0.0f && !(top_p <= 0.0f) && !(min_p > 1.0f) && k != 1) {
-      row.slope = 1.0 / (double)t;
-      using What = typename Sampler<T>::What;
-      // what top_k leaves; without it the whole row
-      typename Sampler<T>::Found kept = row.template find<What::Count>(k > 0 ? k : INT64_MAX, 0.0);
-      const auto last = kept;
-      if (top_p < 1.0f) kept = row.template find<What::Reaches>(0, (double)top_p * last.mass);
-      if (min_p > 0.0f) {
-        const auto f = row.template find<What::Under>(0, (double)min_p);
-        if (f.n < kept.n) kept = f;
+    const SampleSettings set{u, top_p, min_p, k};
+    int key = row.top;
+    uint32_t in = 1;
+    if (!first) {
+      typename Sampler<T>::Found f{0, 0.0, 0, 0};
+      if (row.packed) {  // one window holds the row
+        if (wave == 0) {
+          f = row.choose(set, [&](auto what, int64_t want, double mass) __attribute__((always_inline)) {
+            typename Sampler<T>::Found g{0, 0.0, 0, 0};
+            row.search(what, want, mass, &g);
+            return g;
+          });
+          if (lane == 0) {
+            s.answer_key = f.key;
+            s.answer_in = f.in;
+          }
+        }
+        __syncthreads();
+      } else {
+        sample_wide<T>(s, row.row, row.V, row.top, row.slope, set);
       }
-      const auto f = row.template find<What::Passes>(0, (double)u * kept.mass);
-      if (f.in != 0 && f.n <= kept.n) {
-        key = f.key;
-        in = f.in;
-      } else {  // the last that is kept
-        const auto e = row.template find<What::Count>(kept.n, 0.0);
-        key = e.key;
-        in = e.in;
-      }
+      key = s.answer_key;
+      in = s.answer_in;
     }
     const int place = row.place_of(key, in);
     if (tid == 0) a.token[m] = place;

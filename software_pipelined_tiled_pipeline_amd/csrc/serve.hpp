@@ -27,7 +27,7 @@ inline I8Plan plan_i8(int64_t M, int64_t N, int64_t K, bool gated, bool quantize
   Carver c;
   const int64_t width = up_to(K, 16);
   p.few = M <= kI8FewRows;
-  p.own = p.few && !quantized && M <= 4 && K <= 8192;
+  p.own = p.few && !quantized && M <= 4 && K >= 8 && K <= 8192;
   if (!quantized && !p.own) {
     p.q = c.take(M * width);
     p.s = c.take(M * 4);
