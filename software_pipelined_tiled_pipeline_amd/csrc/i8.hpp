@@ -200,14 +200,15 @@ __global__ void __launch_bounds__(WAVES * 64) i8_few_kernel(I8Args a) {
   Stream job;
   job.init(lane, a.width / 2);
   typename Stream::Place at, next;
-  const int64_t rows = GATED ? 2 * (int64_t)a.N : a.N;
 #pragma unroll
   for (int b = 0; b < NT; ++b) {
-    const int r = n0 + (GATED ? 0 : 16 * b) + (lane >> 2);
-    at.w[b] = row_of(a.w, GATED ? (int64_t)(r < a.N ? r : a.N - 1) + (int64_t)b * a.N : r, rows, a.width);
+    const int row0 = n0 + (GATED ? 0 : 16 * b);
+    at.w[b] = block_start(a.w + (GATED && b ? (int64_t)a.N * a.width : 0), row0, a.N, a.width);
+    at.wo[b] = block_row(row0, lane >> 2, a.N, a.width);
   }
+  at.x = XL ? nullptr : block_start(a.q, m0, a.M, a.width);
 #pragma unroll
-  for (int m = 0; m < MT; ++m) at.x[m] = XL ? nullptr : row_of(a.q, m0 + 16 * m + (lane >> 2), a.M, a.width);
+  for (int m = 0; m < MT; ++m) at.xo[m] = block_row(m0, 16 * m + (lane >> 2), a.M, a.width);
   const int blocks = job.blocks(), turn = first_turn(blockIdx.x, blocks);
   auto block = [&](int i) { return i + turn < blocks ? i + turn : i + turn - blocks; };
   next = at;

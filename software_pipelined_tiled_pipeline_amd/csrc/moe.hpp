@@ -11,6 +11,7 @@
 // choice of an expert.
 #pragma once
 
+#include "lane_ops.hpp"
 #include "row_stream.hpp"
 #include "serve.hpp"
 
@@ -26,6 +27,9 @@ struct MoeArgs {
   uint32_t *tops;      // [M k] largest |h|, f16 only
   uint32_t *counts;    // [chunks][slots] choices of the slot's expert, and the expert << 8
   uint16_t *lists;     // [chunks][slots][64] which choices of the chunk they are
+  float *partial;      // [splits][M][D] sums of y, if there are several
+  uint32_t *arrived;   // [chunks][groups of 16 columns] workgroups of moe_down_kernel that are done
+  int groups, splits;  // all of these groups; workgroups that share one
   int M, E, D, F, k, slots;
   bool by_choice;      // slots are choices
   int act;
@@ -42,32 +46,48 @@ constexpr bool kWideHidden = std::is_same_v<T, _Float16>;
 // ------------------------------------------------------------ the choice ---
 
 // Logits in 64 bits: which experts a token gets must not depend on the order
-// of the sum.  A wave takes two experts, eight values a lane at a time.
-template <typename T>
+// of the sum.  A workgroup has one expert and up to TB tokens, a thread eight
+// values of K at a time, two loads ahead.
+template <typename T, int TB>
 __global__ void __launch_bounds__(256) moe_logits_kernel(MoeArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int m = blockIdx.y, e0 = (blockIdx.x * 4 + wave) * 2;
-  if (e0 >= a.E) return;
-  const uint16_t *x = a.x + (int64_t)m * a.D;
-  const uint16_t *r[2] = {a.router + (int64_t)e0 * a.D, a.router + (int64_t)(e0 + 1 < a.E ? e0 + 1 : e0) * a.D};
-  double sum[2] = {0.0, 0.0};
-  for (int k = lane * 8; k < a.D; k += 512) {
-    const u32x4 xv = k + 8 <= a.D ? *reinterpret_cast<const u32x4_any *>(x + k) : load_tail(x, k, a.D);
+  __shared__ double sums[4][TB];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int e = blockIdx.x, m0 = blockIdx.y * TB;
+  const uint16_t *r = a.router + (int64_t)e * a.D;
+  double sum[TB];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const u32x4 rv = k + 8 <= a.D ? *reinterpret_cast<const u32x4_any *>(r[i] + k) : load_tail(r[i], k, a.D);
+  for (int i = 0; i < TB; ++i) sum[i] = 0.0;
+  auto eight = [&](const uint16_t *row, int k) {
+    if (k + 8 <= a.D) return (u32x4)*reinterpret_cast<const u32x4_any *>(row + k);
+    return k < a.D ? load_tail(row, k, a.D) : u32x4{0u, 0u, 0u, 0u};
+  };
+  for (int k0 = 0; k0 < a.D; k0 += 4096) {
+    u32x4 rv[2], xv[2][TB];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        sum[i] = __builtin_fma((double)widen<T>((uint16_t)(xv[e / 2] >> (16 * (e % 2)))),
-                               (double)widen<T>((uint16_t)(rv[e / 2] >> (16 * (e % 2)))), sum[i]);
+    for (int j = 0; j < 2; ++j) {
+      const int k = k0 + j * 2048 + tid * 8;
+      rv[j] = eight(r, k);
+#pragma unroll
+      for (int i = 0; i < TB; ++i) xv[j][i] = eight(a.x + (int64_t)(m0 + i < a.M ? m0 + i : a.M - 1) * a.D, k);
     }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const double w = (double)widen<T>((uint16_t)(rv[j][n / 2] >> (16 * (n % 2))));
+#pragma unroll
+        for (int i = 0; i < TB; ++i)
+          sum[i] = __builtin_fma((double)widen<T>((uint16_t)(xv[j][i][n / 2] >> (16 * (n % 2)))), w, sum[i]);
+      }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum[i] += __shfl_xor(sum[i], d);
-    if (lane == 0 && e0 + i < a.E) a.logits[(int64_t)m * a.E + e0 + i] = sum[i];
+  for (int i = 0; i < TB; ++i) {
+    sum[i] = wave_scan(sum[i]);
+    if (lane == 63) sums[wave][i] = sum[i];
   }
+  __syncthreads();
+  if (tid < TB && m0 + tid < a.M)
+    a.logits[(int64_t)(m0 + tid) * a.E + e] = (sums[0][tid] + sums[1][tid]) + (sums[2][tid] + sums[3][tid]);
 }
 
 // Numbers as integers of the same order; a NaN is behind minus infinity.
@@ -83,53 +103,48 @@ __device__ __forceinline__ double moe_value(uint64_t o) {
 
 constexpr int kMoeExperts = 1024, kMoeTop = 32, kMoeChunk = 64;
 
-// A wave a token: top_k times the largest logit that is left, the lowest index
-// of equal ones.
-static __global__ void __launch_bounds__(64) moe_choose_kernel(MoeArgs a) {
-  constexpr int PER = kMoeExperts / 64;
+// A wave a token, up to 64 PER experts: top_k times the largest logit that is
+// left, the lowest index of equal ones.
+template <int PER>
+__global__ void __launch_bounds__(64) moe_choose_kernel(MoeArgs a) {
   const int lane = threadIdx.x, m = blockIdx.x;
+  for (int i = m * 64 + lane; i < a.groups; i += a.M * 64) a.arrived[i] = 0;
   const double *l = a.logits + (int64_t)m * a.E;
   uint64_t left[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) left[i] = i * 64 + lane < a.E ? moe_order(l[i * 64 + lane]) : 0;
-  double first = 0.0, total = 0.0, mine = 0.0;
+  double first = 0.0, mine = -INFINITY;
   int my_expert = 0;
   for (int j = 0; j < a.k; ++j) {
     uint64_t best = left[0];
-    int at = lane;
 #pragma unroll
     for (int i = 1; i < PER; ++i)
-      if (i * 64 < a.E && left[i] > best) {
-        best = left[i];
-        at = i * 64 + lane;
-      }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-      const uint64_t other = __shfl_xor((unsigned long long)best, d);
-      const int where = __shfl_xor(at, d);
-      if (other > best || (other == best && where < at)) {
-        best = other;
-        at = where;
-      }
-    }
+      if (i * 64 < a.E && left[i] > best) best = left[i];
+    best = wave_most(best);
+    int at = -1;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (at == i * 64 + lane) left[i] = 0;
+      if (i * 64 < a.E && at < 0) {
+        const uint64_t has = __ballot(left[i] == best);
+        if (has) {
+          at = i * 64 + __builtin_ctzll(has);
+          if (lane == __builtin_ctzll(has)) left[i] = 0;
+        }
+      }
     const double v = moe_value(best);
     if (j == 0) first = v;
-    const double e = exp(v - first);
-    total += e;
     if (lane == j) {
-      mine = e;
+      mine = v;
       my_expert = at;
     }
   }
-  if (!a.normalize) {
-    total = 0.0;
+  mine = exp(mine - first);
+  double total = 0.0;
+  if (a.normalize)
+    total = lane < a.k ? mine : 0.0;
+  else
     for (int e = lane; e < a.E; e += 64) total += exp(l[e] - first);
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) total += __shfl_xor(total, d);
-  }
+  total = read_lane(wave_scan(total), 63);
   if (lane < a.k) {
     const int64_t at = (int64_t)m * a.k + lane;
     a.experts[at] = my_expert;
@@ -143,8 +158,9 @@ static __global__ void __launch_bounds__(64) moe_choose_kernel(MoeArgs a) {
 // A workgroup has an expert's 16 gate rows and the same 16 up rows; its waves
 // take blocks of K in turn and join their sums in LDS.  More than 16 MT tokens
 // of an expert take another pass over these weights.
-template <typename T, int MT, int WAVES>
-__global__ void __launch_bounds__(WAVES * 64) moe_gated_kernel(MoeArgs a) {
+// SHORT: D is below eight.
+template <typename T, int MT, int WAVES, bool SHORT>
+__global__ void __launch_bounds__(WAVES * 64, MT < 4 ? 4 : 2) moe_gated_kernel(MoeArgs a) {
   constexpr int NT = 2, VALS = MT * NT * 4;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   uint16_t *list = reinterpret_cast<uint16_t *>(smem);  // [64]
@@ -160,6 +176,25 @@ __global__ void __launch_bounds__(WAVES * 64) moe_gated_kernel(MoeArgs a) {
     return;
   }
   const int expert = a.by_choice ? __builtin_amdgcn_readfirstlane(experts[slot]) : slot;
+  using Stream = RowStream<Frag8<T>, MT, NT>;
+  Stream job;
+  job.init(lane, a.D);
+  typename Stream::Place at, next;
+  const int blocks = job.blocks(), turn = first_turn(blockIdx.x + slot * 7, blocks);
+  auto block = [&](int i) { return i + turn < blocks ? i + turn : i + turn - blocks; };
+  const uint16_t *w = a.w + (int64_t)expert * 2 * a.F * a.D;
+  const int64_t pitch = (int64_t)a.D * 2;
+#pragma unroll
+  for (int b = 0; b < NT; ++b) {
+    at.w[b] = block_start(w + (int64_t)b * a.F * a.D, f0, a.F, pitch);
+    at.wo[b] = block_row(f0, lane >> 2, a.F, pitch);
+  }
+  at.x = reinterpret_cast<const char *>(a.x + (int64_t)t0 * a.D);
+  at.kb = wave < blocks ? block(wave) : 0;
+  const bool streams = !SHORT && wave < blocks;
+  // weights are on the way while the expert's tokens are found (a slot of a choice has some, but for a second choice of
+  // its expert)
+  if (a.by_choice && streams) job.begin_weights(at);
   if (wave == 0) {
     int n = 0;
     bool taken = false;  // an earlier choice has this expert's slot
@@ -183,30 +218,21 @@ __global__ void __launch_bounds__(WAVES * 64) moe_gated_kernel(MoeArgs a) {
   }
   if (n == 0) return;
 
-  using Stream = RowStream<Frag8<T>, MT, NT>;
-  Stream job;
-  job.init(lane, a.D);
-  typename Stream::Place at, next;
-  const int blocks = job.blocks(), turn = first_turn(blockIdx.x + slot * 7, blocks);
-  auto block = [&](int i) { return i + turn < blocks ? i + turn : i + turn - blocks; };
-  const uint16_t *w = a.w + (int64_t)expert * 2 * a.F * a.D;
-  const int64_t pitch = (int64_t)a.D * 2;
   const int c = lane & 15, q = lane >> 4;
-#pragma unroll
-  for (int b = 0; b < NT; ++b) at.w[b] = row_of(w + (int64_t)b * a.F * a.D, f0 + (lane >> 2), a.F, pitch);
   for (int first = 0; first < n; first += 16 * MT) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int i = first + 16 * m + (lane >> 2);
-      at.x[m] = row_of(a.x, t0 + list[i < n ? i : n - 1] / a.k, a.M, pitch);
+      at.xo[m] = (uint32_t)(list[i < n ? i : n - 1] / a.k * pitch);
     }
     next = at;
     job.clear();
-    if (a.D < 8) {
+    if constexpr (SHORT) {
       if (wave == 0 && a.D > 0) job.short_rows(at);
-    } else if (wave < blocks) {
+    } else if (streams) {
       at.kb = block(wave);
-      job.begin(at);
+      if (!a.by_choice || first > 0) job.begin_weights(at);
+      job.begin_tokens(at);
       for (int i = wave + WAVES; i < blocks; i += WAVES) {
         next.kb = block(i);
         job.template block<true>(at, next);
@@ -265,45 +291,51 @@ __host__ __device__ constexpr int up_even(int n) { return (n + 1) & ~1; }
 // LDS of moe_down_kernel
 inline int moe_down_lds(int waves, int tokens, int k, int slots) {
   const int choices = tokens * k;
-  return waves * tokens * 64 + choices * 12 + up_even(choices) * 2 + slots * 4 + 4 + choices;
+  return waves * tokens * 64 + choices * 12 + up_even(choices) * 2 + slots * 4 + 8 + choices;
 }
 
-// A workgroup has 16 columns of y and all experts of a chunk.  Their blocks of
-// K, one expert's after the other's, are dealt to the waves in runs of the same
-// length; where a run leaves an expert (or 16 MT of its tokens), the wave adds
-// its sums, times the choices' weights, to its own copy of the chunk's rows,
-// and the copies are added up in order at the end.
-template <typename T, int MT, int WAVES>
-__global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(MoeArgs a) {
-  constexpr int THREADS = WAVES * 64;
+// A workgroup has 16 columns of y and all experts of a chunk, or, with few
+// columns, one of `splits` shares of them.  Their blocks of K, one expert's after
+// the other's, are dealt to the waves in runs of the same length; where a run
+// leaves an expert (or 16 MT of its tokens), the wave adds its sums, times the
+// choices' weights, to its own copy of the chunk's rows.  The copies are added up
+// in order at the end, and the shares by the workgroup that is done last.
+// SHORT: F is below eight.
+template <typename T, int MT, int WAVES, bool SHORT>
+__global__ void __launch_bounds__(WAVES * 64, MT < 4 ? 4 : 2) moe_down_kernel(MoeArgs a) {
+  constexpr int THREADS = WAVES * 64, AHEAD = 2;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int chunk = blockIdx.y, d0 = blockIdx.x * 16;
+  const int chunk = blockIdx.y, d0 = blockIdx.x * 16, split = blockIdx.z;
   const int t0 = chunk * kMoeChunk, tokens = a.M - t0 < kMoeChunk ? a.M - t0 : kMoeChunk;
   const int choices = tokens * a.k;
   float *rows = reinterpret_cast<float *>(smem);                        // [WAVES][tokens][16]
-  float *weight = rows + WAVES * tokens * 16;                           // [choices], by slot
+  float *weight = rows + WAVES * tokens * 16;                           // [choices]
   uint32_t *part = reinterpret_cast<uint32_t *>(weight + choices);      // [choices] of a part: first place in the list, how many << 16; expert
   uint16_t *list = reinterpret_cast<uint16_t *>(part + 2 * choices);    // [choices], by slot
   uint32_t *from_slot = reinterpret_cast<uint32_t *>(list + up_even(choices));  // [slots] first place in the list, how many << 16
-  int *parts_found = reinterpret_cast<int *>(from_slot + a.slots);
-  int8_t *power = reinterpret_cast<int8_t *>(parts_found + 1);  // [choices] exponents (f16)
+  int *parts_found = reinterpret_cast<int *>(from_slot + a.slots), *last_one = parts_found + 1;
+  int8_t *power = reinterpret_cast<int8_t *>(parts_found + 2);  // [choices] exponents (f16)
 
+  // everything that is read here is on the way at once: the slots' lists before it is known how long they are
+  const int blocks = (a.F + 127) / 128, quads = a.slots * (kMoeChunk / 4);  // four entries of the lists each
+  const uint64_t *lists = reinterpret_cast<const uint64_t *>(a.lists + (int64_t)chunk * a.slots * kMoeChunk);
+  uint64_t entries[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) entries[i] = tid + i * THREADS < quads && blocks > 0 ? lists[tid + i * THREADS] : 0;
+  for (int i = tid; i < choices; i += THREADS) {
+    const int64_t choice = (int64_t)t0 * a.k + i;
+    weight[i] = a.weights[choice];
+    if constexpr (kWideHidden<T>) power[i] = (int8_t)moe_exponent(blocks > 0 ? a.tops[choice] : 0);
+  }
   for (int i = tid; i < WAVES * tokens * 16; i += THREADS) rows[i] = 0.0f;
-  const int blocks = (a.F + 127) / 128;
   if (wave == 0) {
     int at = 0, parts = 0;
     for (int base = 0; base < a.slots; base += 64) {
       const int s = base + lane;
       const uint32_t v = s < a.slots && blocks > 0 ? a.counts[(int64_t)chunk * a.slots + s] : 0u;
       const int n = (int)(v & 0xffu), mine = (n + 16 * MT - 1) / (16 * MT);
-      int before = n, parts_before = mine;  // sums over the lanes up to this one
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int u = __shfl_up(before, d), p = __shfl_up(parts_before, d);
-        before += lane >= d ? u : 0;
-        parts_before += lane >= d ? p : 0;
-      }
+      const int before = (int)wave_scan((uint32_t)n), parts_before = (int)wave_scan((uint32_t)mine);
       const int to = at + before - n;
       if (s < a.slots) from_slot[s] = (uint32_t)to | (uint32_t)n << 16;
       for (int i = 0; i < mine; ++i) {
@@ -312,23 +344,23 @@ __global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(MoeArgs a) {
         part[2 * p] = (uint32_t)(to + i * 16 * MT) | (uint32_t)(left < 16 * MT ? left : 16 * MT) << 16;
         part[2 * p + 1] = v >> 8;
       }
-      at += __shfl(before, 63);
-      parts += __shfl(parts_before, 63);
+      at += __builtin_amdgcn_readlane(before, 63);
+      parts += __builtin_amdgcn_readlane(parts_before, 63);
     }
     if (lane == 0) *parts_found = parts;
   }
   __syncthreads();
-  for (int i = tid; i < a.slots * kMoeChunk; i += THREADS) {
-    const uint32_t v = from_slot[i / kMoeChunk];
-    if (i % kMoeChunk < (int)(v >> 16))
-      list[(v & 0xffffu) + i % kMoeChunk] = a.lists[(int64_t)chunk * a.slots * kMoeChunk + i];
-  }
-  __syncthreads();
   const int parts = __builtin_amdgcn_readfirstlane(*parts_found);
-  for (int i = tid; i < choices && parts > 0; i += THREADS) {
-    const int64_t choice = (int64_t)t0 * a.k + list[i];
-    weight[i] = a.weights[choice];
-    if constexpr (kWideHidden<T>) power[i] = (int8_t)moe_exponent(a.tops[choice]);
+  for (int i = 0; i * THREADS < quads && parts > 0; ++i) {
+    const int quad = tid + i * THREADS;
+    if (quad >= quads) break;
+    const uint32_t v = from_slot[quad / (kMoeChunk / 4)];
+    const int first = quad % (kMoeChunk / 4) * 4, n = (int)(v >> 16);
+    if (first >= n) continue;
+    const uint64_t e = i == 0 ? entries[0] : i == 1 ? entries[1] : lists[quad];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (first + j < n) list[(v & 0xffffu) + first + j] = (uint16_t)(e >> (16 * j));
   }
   __syncthreads();
 
@@ -337,19 +369,21 @@ __global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(MoeArgs a) {
   job.init(lane, a.F);
   const int64_t pitch = (int64_t)a.F * 2, total = (int64_t)parts * blocks;
   const int c = lane & 15, q = lane >> 4;
-  int64_t i = total * wave / WAVES;
-  const int64_t end = total * (wave + 1) / WAVES;
+  const int share = split * WAVES + wave, shares = a.splits * WAVES;
+  int64_t i = total * share / shares;
+  const int64_t end = total * (share + 1) / shares;
   auto place = [&](typename Stream::Place &p, int g, int kb) __attribute__((always_inline)) {
     const uint32_t v = part[2 * g];
     const int from = (int)(v & 0xffffu), n = (int)(v >> 16), expert = __builtin_amdgcn_readfirstlane((int)part[2 * g + 1]);
     p.kb = kb;
-    p.w[0] = row_of(a.down + (int64_t)expert * a.D * a.F, d0 + (lane >> 2), a.D, pitch);
+    p.x = a.h + (int64_t)t0 * a.k * a.F * (kWideHidden<T> ? 4 : 2);
+    p.w[0] = block_start(a.down + (int64_t)expert * a.D * a.F, d0, a.D, pitch);
+    p.wo[0] = block_row(d0, lane >> 2, a.D, pitch);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int j = 16 * m + (lane >> 2), which = from + (j < n ? j : n - 1);
-      const int64_t choice = (int64_t)t0 * a.k + list[which];
-      p.x[m] = a.h + choice * a.F * (kWideHidden<T> ? 4 : 2);
-      p.scale[m] = kWideHidden<T> ? ldexpf(1.0f, power[which]) : 1.0f;
+      p.xo[m] = (uint32_t)list[which] * (uint32_t)a.F * (kWideHidden<T> ? 4u : 2u);
+      p.scale[m] = kWideHidden<T> ? ldexpf(1.0f, power[list[which]]) : 1.0f;
     }
   };
   auto add = [&](int g) __attribute__((always_inline)) {
@@ -361,23 +395,23 @@ __global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(MoeArgs a) {
       for (int r = 0; r < 4; ++r) {
         const int j = 16 * m + 4 * q + r;
         if (j >= n) continue;
-        const int token = list[from + j] / a.k;
+        const int choice = list[from + j];
         float s = job.tot[m][0][r];
-        if constexpr (kWideHidden<T>) s = ldexpf(s, -power[from + j]);
-        rows[(wave * tokens + token) * 16 + c] += weight[from + j] * s;
+        if constexpr (kWideHidden<T>) s = ldexpf(s, -power[choice]);
+        rows[(wave * tokens + choice / a.k) * 16 + c] += weight[choice] * s;
       }
     job.clear();
   };
-  if (i < end) {
+  if constexpr (SHORT) {
+    typename Stream::Place at;
+    for (; i < end; ++i) {
+      place(at, (int)i, 0);
+      job.short_rows(at);
+      add((int)i);
+    }
+  } else if (i < end) {
     int g = __builtin_amdgcn_readfirstlane((int)(i / blocks)), kb = __builtin_amdgcn_readfirstlane((int)(i % blocks));
     typename Stream::Place at, next;
-    if (a.F < 8) {
-      for (; i < end; ++i) {
-        place(at, (int)i, 0);
-        job.short_rows(at);
-        add((int)i);
-      }
-    } else {
     place(at, g, kb);
     job.begin(at);
     for (++i; i < end; ++i) {
@@ -396,7 +430,6 @@ __global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(MoeArgs a) {
     }
     job.template block<false>(at, at);
     add(g);
-    }
   }
   __syncthreads();
   for (int j = tid; j < tokens * 16; j += THREADS) {
@@ -405,7 +438,33 @@ __global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(MoeArgs a) {
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) v += rows[w * tokens * 16 + j];
-    a.y[(int64_t)(t0 + j / 16) * a.D + col] = __builtin_bit_cast(uint16_t, (T)v);
+    const int64_t to = (int64_t)(t0 + j / 16) * a.D + col;
+    if (a.splits == 1)
+      a.y[to] = __builtin_bit_cast(uint16_t, (T)v);
+    else
+      __hip_atomic_store(a.partial + (int64_t)split * a.M * a.D + to, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (a.splits == 1) return;
+  // The sums are stored and loaded by device-wide accesses, which no cache keeps to itself; each thread waits for its stores before the
+  // workgroup arrives, and a share's loads come after all arrivals.  (Fences would write the whole of an L2 back: 150 us
+  // instead of 20.)
+  wait_vmcnt<0>();
+  compiler_fence();
+  __syncthreads();
+  if (tid == 0)
+    *last_one = __hip_atomic_fetch_add(a.arrived + chunk * gridDim.x + blockIdx.x, 1u, __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)a.splits - 1;
+  __syncthreads();
+  if (!*last_one) return;
+  compiler_fence();
+  for (int j = tid; j < tokens * 16; j += THREADS) {
+    const int col = d0 + j % 16;
+    if (col >= a.D) continue;
+    const int64_t to = (int64_t)(t0 + j / 16) * a.D + col;
+    float v = 0.0f;
+    for (int i = 0; i < a.splits; ++i)
+      v += __hip_atomic_load(a.partial + (int64_t)i * a.M * a.D + to, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    a.y[to] = __builtin_bit_cast(uint16_t, (T)v);
   }
 }
 

@@ -7,32 +7,32 @@
 namespace pgemm {
 namespace launch_detail {
 
-template <typename T, int MT, int WAVES>
+template <typename T, int MT, int WAVES, bool SHORT = false>
 pgemm_status launch_moe_gated(const MoeArgs &a, int64_t chunks, hipStream_t stream) {
   constexpr int LDS = 144 + WAVES * MT * 2 * 4 * 256;
   static_assert(LDS <= 65536, "what a kernel may use without asking");
-  auto kern = moe_gated_kernel<T, MT, WAVES>;
+  auto kern = moe_gated_kernel<T, MT, WAVES, SHORT>;
   hipLaunchKernelGGL(kern, dim3((unsigned)per(a.F, 16), (unsigned)a.slots, (unsigned)chunks), dim3(WAVES * 64), LDS, stream, a);
   return launched();
 }
 
-template <typename T, int MT, int WAVES>
+template <typename T, int MT, int WAVES, bool SHORT = false>
 pgemm_status launch_moe_down(const MoeArgs &a, int64_t chunks, hipStream_t stream, int dev) {
   static std::atomic<uint64_t> lds_set{0};
   constexpr int kMost = 160 * 1024;
-  auto kern = moe_down_kernel<T, MT, WAVES>;
+  auto kern = moe_down_kernel<T, MT, WAVES, SHORT>;
   const int lds = moe_down_lds(WAVES, a.M < kMoeChunk ? a.M : kMoeChunk, a.k, a.slots);
   if (lds > 65536) {
     pgemm_status st = allow_lds(kern, kMost, dev, lds_set);
     if (st != PGEMM_OK) return st;
   }
-  hipLaunchKernelGGL(kern, dim3((unsigned)per(a.D, 16), (unsigned)chunks), dim3(WAVES * 64), lds, stream, a);
+  hipLaunchKernelGGL(kern, dim3((unsigned)per(a.D, 16), (unsigned)chunks, (unsigned)a.splits), dim3(WAVES * 64), lds, stream, a);
   return launched();
 }
 
 template <typename T>
 pgemm_status moe_layer(const MoeCall &c) {
-  const MoePlan p = plan_moe(c.M, c.E, c.F, c.top_k);
+  const MoePlan p = plan_moe(c.M, c.E, c.D, c.F, c.top_k);
   const int64_t chunks = per(c.M, kMoeChunkTokens);
   MoeArgs a{};
   a.x = c.x;
@@ -53,25 +53,37 @@ pgemm_status moe_layer(const MoeCall &c) {
   a.F = (int)c.F;
   a.k = (int)c.top_k;
   a.slots = (int)p.slots;
+  a.splits = (int)p.splits;
+  a.groups = (int)p.groups;
+  a.partial = reinterpret_cast<float *>(c.workspace + p.partial);
+  a.arrived = reinterpret_cast<uint32_t *>(c.workspace + p.arrived);
   a.by_choice = p.by_choice;
   a.act = c.act;
   a.normalize = c.normalize;
-  hipLaunchKernelGGL(moe_logits_kernel<T>, dim3((unsigned)per(c.E, 8), (unsigned)c.M), dim3(256), 0, c.stream, a);
+  if (c.M <= 4)
+    hipLaunchKernelGGL((moe_logits_kernel<T, 1>), dim3((unsigned)c.E, (unsigned)c.M), dim3(256), 0, c.stream, a);
+  else
+    hipLaunchKernelGGL((moe_logits_kernel<T, 4>), dim3((unsigned)c.E, (unsigned)per(c.M, 4)), dim3(256), 0, c.stream, a);
   pgemm_status st = launched();
   if (st != PGEMM_OK) return st;
-  hipLaunchKernelGGL(moe_choose_kernel, dim3((unsigned)c.M), dim3(64), 0, c.stream, a);
+  auto choose = c.E <= 64 ? moe_choose_kernel<1> : c.E <= 256 ? moe_choose_kernel<4> : moe_choose_kernel<16>;
+  hipLaunchKernelGGL(choose, dim3((unsigned)c.M), dim3(64), 0, c.stream, a);
   st = launched();
   if (st != PGEMM_OK || c.D == 0) return st;
   // tokens an expert has on average
   const int64_t mean = (c.M < kMoeChunkTokens ? c.M : kMoeChunkTokens) * c.top_k / c.E;
   if (c.F > 0) {
-    st = mean <= 8 ? launch_moe_gated<T, 1, 8>(a, chunks, c.stream)
-                   : mean <= 24 ? launch_moe_gated<T, 2, 8>(a, chunks, c.stream) : launch_moe_gated<T, 4, 4>(a, chunks, c.stream);
+    const bool many = per(c.F, 16) * p.slots * chunks > 512;
+    st = c.D < 8     ? launch_moe_gated<T, 1, 8, true>(a, chunks, c.stream)
+         : mean > 24 ? launch_moe_gated<T, 4, 4>(a, chunks, c.stream)
+         : mean > 8 ? many ? launch_moe_gated<T, 2, 4>(a, chunks, c.stream) : launch_moe_gated<T, 2, 8>(a, chunks, c.stream)
+                    : many ? launch_moe_gated<T, 1, 4>(a, chunks, c.stream) : launch_moe_gated<T, 1, 8>(a, chunks, c.stream);
     if (st != PGEMM_OK) return st;
   }
-  return mean <= 8 ? launch_moe_down<T, 1, 8>(a, chunks, c.stream, c.dev)
-                   : mean <= 24 ? launch_moe_down<T, 2, 8>(a, chunks, c.stream, c.dev)
-                                : launch_moe_down<T, 4, 8>(a, chunks, c.stream, c.dev);
+  return c.F < 8     ? launch_moe_down<T, 1, 8, true>(a, chunks, c.stream, c.dev)
+         : mean <= 8 ? launch_moe_down<T, 1, 8>(a, chunks, c.stream, c.dev)
+                     : mean <= 24 ? launch_moe_down<T, 2, 8>(a, chunks, c.stream, c.dev)
+                                  : launch_moe_down<T, 4, 8>(a, chunks, c.stream, c.dev);
 }
 
 }  // namespace launch_detail

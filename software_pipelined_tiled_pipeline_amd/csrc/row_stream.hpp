@@ -33,13 +33,15 @@ enum class Tokens { Rows, Lds, Wide };
 
 template <class F, int MT, int NT, Tokens X = Tokens::Rows, typename T = void>
 struct RowStream {
-  static constexpr int XD = MT == 1 ? 4 : 2;  // steps that tokens are loaded ahead
+  static constexpr int XD = MT == 1 && X != Tokens::Wide ? 4 : 2;  // steps that tokens are loaded ahead
   static constexpr int XP = X == Tokens::Wide ? 2 : 1;  // 16-byte pieces of a token's share
 
-  // A block's place: this lane's rows (of its token and weight blocks row l / 4,
-  // at the row's start) and the block of K.
+  // A block's place: where the tokens and each block of weight rows start, the
+  // same for the wave; this lane's rows (row l / 4 of each block) from there,
+  // below 2^31 bytes; the block of K.
   struct Place {
-    const char *x[MT], *w[NT];
+    const char *x, *w[NT];
+    uint32_t xo[MT], wo[NT];
     float scale[MT];  // Wide: of x's rows
     int kb;
   };
@@ -68,10 +70,10 @@ struct RowStream {
 
   // Eight units of a row for step s of block kb.  In the block that K ends in
   // the row's last eight, put in place when they are used.
-  __device__ __forceinline__ u32x4 load(const char *row, int kb, int s) const {
-    if (kb < full) return *reinterpret_cast<const u32x4_any *>(row + (int64_t)kb * 256 + s * 64 + piece * 16);
+  __device__ __forceinline__ u32x4 load(const char *base, uint32_t row, int kb, int s) const {
+    if (kb < full) return load_at<u32x4_any>(base + ((int64_t)kb * 256 + s * 64), row + 16u * piece);
     const int k = kb * 128 + 32 * s + 8 * piece;
-    return *reinterpret_cast<const u32x4_any *>(row + (int64_t)(k < K - 8 ? k : K - 8) * 2);
+    return load_at<u32x4_any>(base, row + 2u * (k < K - 8 ? k : K - 8));
   }
   __device__ __forceinline__ u32x4 used(u32x4 v, int kb, int s) const {
     if (kb >= full) {
@@ -86,24 +88,29 @@ struct RowStream {
     for (int m = 0; m < MT; ++m) {
       if constexpr (X == Tokens::Wide) {
         const int k = p.kb * 128 + 32 * s + 8 * piece;
-        const float *row = reinterpret_cast<const float *>(p.x[m]);
-        const float *at = row + (p.kb < full || k < K - 8 ? k : K - 8);
-        xr[slot][m][0] = *reinterpret_cast<const u32x4_any *>(at);
-        xr[slot][m][1] = *reinterpret_cast<const u32x4_any *>(at + 4);
+        const uint32_t at = p.xo[m] + 4u * (p.kb < full || k < K - 8 ? k : K - 8);
+        xr[slot][m][0] = load_at<u32x4_any>(p.x, at);
+        xr[slot][m][1] = load_at<u32x4_any>(p.x, at + 16u);
       } else {
-        xr[slot][m][0] = load(p.x[m], p.kb, s);
+        xr[slot][m][0] = load(p.x, p.xo[m], p.kb, s);
       }
     }
   }
   __device__ __forceinline__ void load_w(const Place &p, int s) {
 #pragma unroll
-    for (int b = 0; b < NT; ++b) wr[s][b] = load(p.w[b], p.kb, s);
+    for (int b = 0; b < NT; ++b) wr[s][b] = load(p.w[b], p.wo[b], p.kb, s);
   }
-  __device__ __forceinline__ void begin(const Place &p) {
+  __device__ __forceinline__ void begin_weights(const Place &p) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) load_w(p, s);
+  }
+  __device__ __forceinline__ void begin_tokens(const Place &p) {
 #pragma unroll
     for (int s = 0; s < XD; ++s) load_x(p, s, s);
+  }
+  __device__ __forceinline__ void begin(const Place &p) {
+    begin_weights(p);
+    begin_tokens(p);
   }
 
   // All of rows shorter than eight units, value by value (not from LDS).
@@ -114,21 +121,21 @@ struct RowStream {
       u32x4 v = {0u, 0u, 0u, 0u};
       if constexpr (X == Tokens::Wide) {
         if (piece == 0) {
-          const float *row = reinterpret_cast<const float *>(p.x[m]);
+          const float *row = reinterpret_cast<const float *>(p.x + p.xo[m]);
 #pragma unroll
           for (int e = 0; e < 7; ++e) {
             if (e < K) v[e / 2] |= Mfma<T>::pack4(row[e] * p.scale[m], 0.0f, 0.0f, 0.0f)[0] << (16 * (e % 2));
           }
         }
       } else {
-        if (piece == 0) v = load_tail(reinterpret_cast<const uint16_t *>(p.x[m]), 0, K);
+        if (piece == 0) v = load_tail(reinterpret_cast<const uint16_t *>(p.x + p.xo[m]), 0, K);
       }
       x[m] = to_rows(v, from);
     }
 #pragma unroll
     for (int b = 0; b < NT; ++b) {
       u32x4 v = {0u, 0u, 0u, 0u};
-      if (piece == 0) v = load_tail(reinterpret_cast<const uint16_t *>(p.w[b]), 0, K);
+      if (piece == 0) v = load_tail(reinterpret_cast<const uint16_t *>(p.w[b] + p.wo[b]), 0, K);
       v = to_rows(v, from);
 #pragma unroll
       for (int m = 0; m < MT; ++m) tot[m][b] = F::mma(x[m], v, tot[m][b]);
@@ -177,9 +184,13 @@ struct RowStream {
 // (Widths below eight units, in which load_tail reads a row value by value, are
 // left out of the loop: its loads took 70 registers.)
 
-// The start of row r (of `rows`, the last one repeated) of a matrix with rows of `pitch` bytes.
-__device__ __forceinline__ const char *row_of(const void *base, int64_t r, int64_t rows, int64_t pitch) {
-  return static_cast<const char *>(base) + (r < rows ? r : rows - 1) * pitch;
+// Row r of a block of rows from row0 on, the last of `rows` repeated: its
+// distance from where block_start says that the block starts.
+__device__ __forceinline__ const char *block_start(const void *base, int64_t row0, int64_t rows, int64_t pitch) {
+  return static_cast<const char *>(base) + (row0 < rows ? row0 : rows - 1) * pitch;
+}
+__device__ __forceinline__ uint32_t block_row(int64_t row0, int r, int64_t rows, int64_t pitch) {
+  return (uint32_t)(((row0 + r < rows ? row0 + r : rows - 1) - (row0 < rows ? row0 : rows - 1)) * pitch);
 }
 
 // Where a workgroup starts along K: rows are often a multiple of the memory

@@ -13,6 +13,7 @@
 #pragma once
 
 #include "fused_launch.hpp"
+#include "lane_ops.hpp"
 #include "serve.hpp"
 
 namespace pgemm {
@@ -48,35 +49,6 @@ struct SampleShared {
   int answer_key;
   uint32_t answer_in, found;
 };
-
-// Sums over the lanes up to each one, by moves within a row of 16 lanes and
-// from a row's last lane to the rows after it.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t lane_move(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
-}
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double lane_move(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = lane_move<CTRL, ROWS>((uint32_t)b), hi = lane_move<CTRL, ROWS>((uint32_t)(b >> 32));
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ double read_lane(double v, int lane) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-template <typename U>
-__device__ __forceinline__ U wave_scan(U v) {
-  v += lane_move<0x111, 0xf>(v);
-  v += lane_move<0x112, 0xf>(v);
-  v += lane_move<0x114, 0xf>(v);
-  v += lane_move<0x118, 0xf>(v);
-  v += lane_move<0x142, 0xa>(v);
-  v += lane_move<0x143, 0xc>(v);
-  return v;
-}
 
 // e^d for d <= 0 in 64 bits: 2^(n/32) from a table times a polynomial of what
 // is left, |r| <= ln 2 / 64 (P. T. P. Tang, "Table-driven implementation of the

@@ -62,7 +62,7 @@ pgemm_status i8(Launch launch, const void *x, const float *xs, const int8_t *w, 
 }
 
 pgemm_status check_moe(int64_t M, int64_t E, int64_t D, int64_t F, int64_t top_k) {
-  if (M < 0 || M >= kMoeMaxTokens || E < 1 || E > kMoeMaxExperts || !pitch(D) || !pitch(F < 0 ? F : 2 * F) || top_k < 1 ||
+  if (M < 0 || M >= kMoeMaxTokens || E < 1 || E > kMoeMaxExperts || !pitch(D) || F < 0 || F > kMoeMaxHidden || top_k < 1 ||
       top_k > kMoeMaxTop || top_k > E)
     return PGEMM_ERR_SHAPE;
   return PGEMM_OK;
@@ -81,7 +81,7 @@ pgemm_status moe(Launch launch, const uint16_t *x, const uint16_t *router, const
     return PGEMM_ERR_ALIGN;
   if (M == 0) return PGEMM_OK;
   Site s;
-  st = s.open(stream, plan_moe(M, E, F, top_k).bytes);
+  st = s.open(stream, plan_moe(M, E, D, F, top_k).bytes);
   if (st != PGEMM_OK) return st;
   MoeCall c{};
   c.x = x;
@@ -135,7 +135,7 @@ pgemm_status pgemm_moe_workspace(int64_t M, int64_t E, int64_t D, int64_t F, int
   if (!bytes) return PGEMM_ERR_NULL;
   pgemm_status st = check_moe(M, E, D, F, top_k);
   if (st != PGEMM_OK) return st;
-  *bytes = M == 0 ? 0 : plan_moe(M, E, F, top_k).bytes;
+  *bytes = M == 0 ? 0 : plan_moe(M, E, D, F, top_k).bytes;
   return PGEMM_OK;
 }
 
