@@ -181,6 +181,11 @@ struct I8Args {
 constexpr int kI8OwnTokens = 4;     // tokens that a workgroup makes integers of itself,
 constexpr int kI8OwnWidth = 8192;   // of at most so many values
 
+// LDS of a workgroup's sums, and of its waves' blocks before
+constexpr int i8_sums(int mt, int waves, bool own) {
+  return waves * (mt * 2048 > stream_bytes(own ? 0 : mt) ? mt * 2048 : stream_bytes(own ? 0 : mt));
+}
+
 // A workgroup has 32 weight rows (16 of the gate and the same 16 of the up
 // projection) and all of K; its waves take blocks of 256 bytes in turn and add
 // their sums up in LDS.  XL: tokens of 16 bits are made integers by every
@@ -194,29 +199,32 @@ __global__ void __launch_bounds__(WAVES * 64) i8_few_kernel(I8Args a) {
   const int n0 = blockIdx.x * (GATED ? 16 : 32), m0 = blockIdx.y * MT * 16;
   float *scales = reinterpret_cast<float *>(smem);  // XL: the tokens' scales
   int *sums = reinterpret_cast<int *>(smem + (XL ? 64 : 0));
-  char *tokens = smem + 64 + WAVES * VALS * 256;
+  constexpr int STREAM = stream_bytes(XL ? 0 : MT), SUMS = i8_sums(MT, WAVES, XL);  // and the waves' blocks before
+  char *tokens = smem + 64 + SUMS;
 
   using Stream = RowStream<Int8Step, MT, NT, XL ? Tokens::Lds : Tokens::Rows>;
   Stream job;
-  job.init(lane, a.width / 2);
-  typename Stream::Place at, next;
+  job.init(lane, a.width / 2, reinterpret_cast<char *>(sums) + wave * STREAM - (XL ? MT * kBlockBytes : 0));
 #pragma unroll
   for (int b = 0; b < NT; ++b) {
     const int row0 = n0 + (GATED ? 0 : 16 * b);
-    at.w[b] = block_start(a.w + (GATED && b ? (int64_t)a.N * a.width : 0), row0, a.N, a.width);
-    at.wo[b] = block_row(row0, lane >> 2, a.N, a.width);
-  }
-  at.x = XL ? nullptr : block_start(a.q, m0, a.M, a.width);
+    job.w[b] = block_start(a.w + (GATED && b ? (int64_t)a.N * a.width : 0), row0, a.N, a.width);
 #pragma unroll
-  for (int m = 0; m < MT; ++m) at.xo[m] = block_row(m0, 16 * m + (lane >> 2), a.M, a.width);
+    for (int i = 0; i < 4; ++i) job.wo[b][i] = block_row(row0, 4 * i + (lane >> 4), a.N, a.width);
+  }
+  job.have = a.M - m0;
+  job.x = XL ? nullptr : block_start(a.q, m0, a.M, a.width);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) job.xo[m][i] = block_row(m0, 16 * m + 4 * i + (lane >> 4), a.M, a.width);
   const int blocks = job.blocks(), turn = first_turn(blockIdx.x, blocks);
   auto block = [&](int i) { return i + turn < blocks ? i + turn : i + turn - blocks; };
-  next = at;
-  at.kb = wave < blocks ? block(wave) : 0;
+  int kb = wave < blocks ? block(wave) : 0;
 
   if constexpr (XL) {
     constexpr int C = kI8OwnWidth / (THREADS * 8);
-    static_assert(C * THREADS * 8 == kI8OwnWidth && WAVES * kI8OwnTokens * 4 <= WAVES * VALS * 256, "");
+    static_assert(C * THREADS * 8 == kI8OwnWidth && kI8OwnTokens * 4 <= kBlockBytes, "");
     const int pitch = blocks * 256 + 16;
     u32x4 v[kI8OwnTokens][C];
 #pragma unroll
@@ -225,7 +233,7 @@ __global__ void __launch_bounds__(WAVES * 64) i8_few_kernel(I8Args a) {
       for (int i = 0; i < C; ++i)
         v[m][i] = m < a.M ? load_eight(a.x + (int64_t)m * a.K, (i * THREADS + tid) * 8, a.K) : u32x4{0u, 0u, 0u, 0u};
     compiler_fence();  // the tokens first: waiting for them is then not waiting for the weights
-    if (wave < blocks) job.begin(at);
+    if (wave < blocks) job.begin_weights(kb);
     compiler_fence();
     uint32_t *tops = reinterpret_cast<uint32_t *>(sums);  // [tokens][waves]
 #pragma unroll
@@ -256,16 +264,21 @@ __global__ void __launch_bounds__(WAVES * 64) i8_few_kernel(I8Args a) {
     const int row = lane & 15;
     job.xl = tokens + (row < a.M ? row : a.M - 1) * pitch + 16 * (lane >> 4);
   } else {
-    if (wave < blocks) job.begin(at);
+    if (wave < blocks) {
+      job.begin_weights(kb);
+      job.load_x(kb);
+    }
   }
+  auto same = []() {};
   if (wave < blocks) {
     for (int i = wave + WAVES; i < blocks; i += WAVES) {
-      next.kb = block(i);
-      job.template block<true>(at, next);
-      at.kb = next.kb;
+      const int next = block(i);
+      job.template block<true>(kb, next, same);
+      kb = next;
     }
-    job.template block<false>(at, at);
+    job.template block<false>(kb, kb, same);
   }
+  __syncthreads();
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll

@@ -25,30 +25,34 @@ pgemm_status quant_rows(const uint16_t *x, int8_t *q, float *scale, int64_t M, i
 }
 
 template <typename T, bool GATED, int MT, int WAVES, bool XL>
-pgemm_status launch_i8_few_one(const I8Args &a, hipStream_t stream) {
-  constexpr int SUMS = (XL ? 64 : 0) + WAVES * MT * 2 * 4 * 256;
-  constexpr int TOKENS = XL ? kI8OwnTokens * (kI8OwnWidth + 16) : 0;
-  static_assert(SUMS + TOKENS <= 65536, "what a kernel may use without asking");
+pgemm_status launch_i8_few_one(const I8Args &a, hipStream_t stream, int dev) {
+  static std::atomic<uint64_t> lds_set{0};
+  constexpr int SUMS = (XL ? 64 : 0) + i8_sums(MT, WAVES, XL), MOST = SUMS + (XL ? kI8OwnTokens * (kI8OwnWidth + 16) : 0);
+  static_assert(MOST <= 160 * 1024, "LDS of a CU");
   const int lds = SUMS + (XL ? (int)(a.M * (up_to(a.width, 256) + 16)) : 0);
   auto kern = i8_few_kernel<T, GATED, MT, WAVES, XL>;
+  if (lds > 65536) {
+    pgemm_status st = allow_lds(kern, MOST, dev, lds_set);
+    if (st != PGEMM_OK) return st;
+  }
   hipLaunchKernelGGL(kern, dim3((unsigned)per(a.N, GATED ? 16 : 32), (unsigned)per(a.M, 16 * MT)), dim3(WAVES * 64), lds,
                      stream, a);
   return launched();
 }
 
 template <typename T, bool GATED, int MT, bool XL>
-pgemm_status launch_i8_waves(const I8Args &a, hipStream_t stream) {
+pgemm_status launch_i8_waves(const I8Args &a, hipStream_t stream, int dev) {
   const int64_t groups = per(a.N, GATED ? 16 : 32) * per(a.M, 16 * MT);
-  if (groups <= 512) return launch_i8_few_one<T, GATED, MT, 8, XL>(a, stream);
-  return launch_i8_few_one<T, GATED, MT, 4, XL>(a, stream);
+  if (groups <= 512) return launch_i8_few_one<T, GATED, MT, 8, XL>(a, stream, dev);
+  return launch_i8_few_one<T, GATED, MT, 4, XL>(a, stream, dev);
 }
 
 template <typename T, bool GATED>
-pgemm_status launch_i8_few(const I8Args &a, bool own, hipStream_t stream) {
-  if (own) return launch_i8_waves<T, GATED, 1, true>(a, stream);
-  if (a.M <= 16) return launch_i8_waves<T, GATED, 1, false>(a, stream);
-  if (a.M <= 32) return launch_i8_waves<T, GATED, 2, false>(a, stream);
-  return launch_i8_waves<T, GATED, 4, false>(a, stream);
+pgemm_status launch_i8_few(const I8Args &a, bool own, hipStream_t stream, int dev) {
+  if (own) return launch_i8_waves<T, GATED, 1, true>(a, stream, dev);
+  if (a.M <= 16) return launch_i8_waves<T, GATED, 1, false>(a, stream, dev);
+  if (a.M <= 32) return launch_i8_waves<T, GATED, 2, false>(a, stream, dev);
+  return launch_i8_waves<T, GATED, 4, false>(a, stream, dev);
 }
 
 template <typename T>
@@ -103,7 +107,7 @@ pgemm_status i8_product(const I8Call &c) {
   a.K = (int)c.K;
   a.width = (int)i8_width(c.K);
   a.act = c.act;
-  return c.gated ? launch_i8_few<T, true>(a, p.own, c.stream) : launch_i8_few<T, false>(a, p.own, c.stream);
+  return c.gated ? launch_i8_few<T, true>(a, p.own, c.stream, c.dev) : launch_i8_few<T, false>(a, p.own, c.stream, c.dev);
 }
 
 }  // namespace launch_detail

@@ -28,7 +28,7 @@ struct MoeArgs {
   uint32_t *counts;    // [chunks][slots] choices of the slot's expert, and the expert << 8
   uint16_t *lists;     // [chunks][slots][64] which choices of the chunk they are
   float *partial;      // [splits][M][D] sums of y, if there are several
-  uint32_t *arrived;   // [chunks][groups of 16 columns] workgroups of moe_down_kernel that are done
+  uint32_t *arrived;   // [chunks][groups of 32 columns] workgroups of moe_down_kernel that are done
   int groups, splits;  // all of these groups; workgroups that share one
   int M, E, D, F, k, slots;
   bool by_choice;      // slots are choices
@@ -101,7 +101,7 @@ __device__ __forceinline__ double moe_value(uint64_t o) {
   return __builtin_bit_cast(double, o >> 63 ? o ^ 1ull << 63 : ~o);
 }
 
-constexpr int kMoeExperts = 1024, kMoeTop = 32, kMoeChunk = 64;
+constexpr int kMoeChunk = kMoeChunkTokens, kMoeColumns = kMoeDownColumns;
 
 // A wave a token, up to 64 PER experts: top_k times the largest logit that is
 // left, the lowest index of equal ones.
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(64) moe_choose_kernel(MoeArgs a) {
 // of an expert take another pass over these weights.
 // SHORT: D is below eight.
 template <typename T, int MT, int WAVES, bool SHORT>
-__global__ void __launch_bounds__(WAVES * 64, MT < 4 ? 4 : 2) moe_gated_kernel(MoeArgs a) {
+__global__ void __launch_bounds__(WAVES * 64, MT == 1 ? 4 : MT == 2 ? 3 : 2) moe_gated_kernel(MoeArgs a) {
   constexpr int NT = 2, VALS = MT * NT * 4;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   uint16_t *list = reinterpret_cast<uint16_t *>(smem);  // [64]
@@ -178,23 +178,22 @@ __global__ void __launch_bounds__(WAVES * 64, MT < 4 ? 4 : 2) moe_gated_kernel(M
   const int expert = a.by_choice ? __builtin_amdgcn_readfirstlane(experts[slot]) : slot;
   using Stream = RowStream<Frag8<T>, MT, NT>;
   Stream job;
-  job.init(lane, a.D);
-  typename Stream::Place at, next;
+  job.init(lane, a.D, reinterpret_cast<char *>(sums) + wave * stream_bytes(MT));
   const int blocks = job.blocks(), turn = first_turn(blockIdx.x + slot * 7, blocks);
   auto block = [&](int i) { return i + turn < blocks ? i + turn : i + turn - blocks; };
   const uint16_t *w = a.w + (int64_t)expert * 2 * a.F * a.D;
   const int64_t pitch = (int64_t)a.D * 2;
 #pragma unroll
   for (int b = 0; b < NT; ++b) {
-    at.w[b] = block_start(w + (int64_t)b * a.F * a.D, f0, a.F, pitch);
-    at.wo[b] = block_row(f0, lane >> 2, a.F, pitch);
+    job.w[b] = block_start(w + (int64_t)b * a.F * a.D, f0, a.F, pitch);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) job.wo[b][i] = block_row(f0, 4 * i + (lane >> 4), a.F, pitch);
   }
-  at.x = reinterpret_cast<const char *>(a.x + (int64_t)t0 * a.D);
-  at.kb = wave < blocks ? block(wave) : 0;
+  job.x = reinterpret_cast<const char *>(a.x + (int64_t)t0 * a.D);
   const bool streams = !SHORT && wave < blocks;
   // weights are on the way while the expert's tokens are found (a slot of a choice has some, but for a second choice of
   // its expert)
-  if (a.by_choice && streams) job.begin_weights(at);
+  if (a.by_choice && streams) job.begin_weights(block(wave));
   if (wave == 0) {
     int n = 0;
     bool taken = false;  // an earlier choice has this expert's slot
@@ -219,27 +218,31 @@ __global__ void __launch_bounds__(WAVES * 64, MT < 4 ? 4 : 2) moe_gated_kernel(M
   if (n == 0) return;
 
   const int c = lane & 15, q = lane >> 4;
+  auto same = []() {};
   for (int first = 0; first < n; first += 16 * MT) {
+    job.have = n - first;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int i = first + 16 * m + (lane >> 2);
-      at.xo[m] = (uint32_t)(list[i < n ? i : n - 1] / a.k * pitch);
-    }
-    next = at;
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = first + 16 * m + 4 * r + (lane >> 4);
+        job.xo[m][r] = (uint32_t)(list[i < n ? i : n - 1] / a.k * pitch);
+      }
     job.clear();
     if constexpr (SHORT) {
-      if (wave == 0 && a.D > 0) job.short_rows(at);
+      if (wave == 0 && a.D > 0) job.short_rows();
     } else if (streams) {
-      at.kb = block(wave);
-      if (!a.by_choice || first > 0) job.begin_weights(at);
-      job.begin_tokens(at);
+      int kb = block(wave);
+      if (!a.by_choice || first > 0) job.begin_weights(kb);
+      job.load_x(kb);
       for (int i = wave + WAVES; i < blocks; i += WAVES) {
-        next.kb = block(i);
-        job.template block<true>(at, next);
-        at.kb = next.kb;
+        const int next = block(i);
+        job.template block<true>(kb, next, same);
+        kb = next;
       }
-      job.template block<false>(at, at);
+      job.template block<false>(kb, kb, same);
     }
+    __syncthreads();
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -289,12 +292,12 @@ __device__ __forceinline__ int moe_exponent(uint32_t top) {
 
 __host__ __device__ constexpr int up_even(int n) { return (n + 1) & ~1; }
 // LDS of moe_down_kernel
-inline int moe_down_lds(int waves, int tokens, int k, int slots) {
+inline int moe_down_lds(int mt, int waves, int tokens, int k, int slots) {
   const int choices = tokens * k;
-  return waves * tokens * 64 + choices * 12 + up_even(choices) * 2 + slots * 4 + 8 + choices;
+  return waves * (stream_bytes(mt) + tokens * kMoeColumns * 4) + choices * 12 + up_even(choices) * 2 + slots * 4 + 8 + choices;
 }
 
-// A workgroup has 16 columns of y and all experts of a chunk, or, with few
+// A workgroup has 32 columns of y and all experts of a chunk, or, with few
 // columns, one of `splits` shares of them.  Their blocks of K, one expert's after
 // the other's, are dealt to the waves in runs of the same length; where a run
 // leaves an expert (or 16 MT of its tokens), the wave adds its sums, times the
@@ -302,15 +305,15 @@ inline int moe_down_lds(int waves, int tokens, int k, int slots) {
 // in order at the end, and the shares by the workgroup that is done last.
 // SHORT: F is below eight.
 template <typename T, int MT, int WAVES, bool SHORT>
-__global__ void __launch_bounds__(WAVES * 64, MT < 4 ? 4 : 2) moe_down_kernel(MoeArgs a) {
-  constexpr int THREADS = WAVES * 64, AHEAD = 2;
+__global__ void __launch_bounds__(WAVES * 64, MT == 1 ? 4 : MT == 2 ? 3 : 2) moe_down_kernel(MoeArgs a) {
+  constexpr int THREADS = WAVES * 64, AHEAD = 2, NT = kMoeColumns / 16;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int chunk = blockIdx.y, d0 = blockIdx.x * 16, split = blockIdx.z;
+  const int chunk = blockIdx.y, d0 = blockIdx.x * kMoeColumns, split = blockIdx.z;
   const int t0 = chunk * kMoeChunk, tokens = a.M - t0 < kMoeChunk ? a.M - t0 : kMoeChunk;
   const int choices = tokens * a.k;
-  float *rows = reinterpret_cast<float *>(smem);                        // [WAVES][tokens][16]
-  float *weight = rows + WAVES * tokens * 16;                           // [choices]
+  float *rows = reinterpret_cast<float *>(smem + WAVES * stream_bytes(MT));  // [WAVES][tokens][32]
+  float *weight = rows + WAVES * tokens * kMoeColumns;                  // [choices]
   uint32_t *part = reinterpret_cast<uint32_t *>(weight + choices);      // [choices] of a part: first place in the list, how many << 16; expert
   uint16_t *list = reinterpret_cast<uint16_t *>(part + 2 * choices);    // [choices], by slot
   uint32_t *from_slot = reinterpret_cast<uint32_t *>(list + up_even(choices));  // [slots] first place in the list, how many << 16
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(WAVES * 64, MT < 4 ? 4 : 2) moe_down_kernel(Mo
     weight[i] = a.weights[choice];
     if constexpr (kWideHidden<T>) power[i] = (int8_t)moe_exponent(blocks > 0 ? a.tops[choice] : 0);
   }
-  for (int i = tid; i < WAVES * tokens * 16; i += THREADS) rows[i] = 0.0f;
+  for (int i = tid; i < WAVES * tokens * kMoeColumns; i += THREADS) rows[i] = 0.0f;
   if (wave == 0) {
     int at = 0, parts = 0;
     for (int base = 0; base < a.slots; base += 64) {
@@ -364,27 +367,35 @@ __global__ void __launch_bounds__(WAVES * 64, MT < 4 ? 4 : 2) moe_down_kernel(Mo
   }
   __syncthreads();
 
-  using Stream = RowStream<Frag8<T>, MT, 1, kWideHidden<T> ? Tokens::Wide : Tokens::Rows, T>;
+  using Stream = RowStream<Frag8<T>, MT, NT, kWideHidden<T> ? Tokens::Wide : Tokens::Rows, T>;
   Stream job;
-  job.init(lane, a.F);
+  job.init(lane, a.F, smem + wave * stream_bytes(MT));
   const int64_t pitch = (int64_t)a.F * 2, total = (int64_t)parts * blocks;
   const int c = lane & 15, q = lane >> 4;
   const int share = split * WAVES + wave, shares = a.splits * WAVES;
   int64_t i = total * share / shares;
   const int64_t end = total * (share + 1) / shares;
-  auto place = [&](typename Stream::Place &p, int g, int kb) __attribute__((always_inline)) {
-    const uint32_t v = part[2 * g];
-    const int from = (int)(v & 0xffffu), n = (int)(v >> 16), expert = __builtin_amdgcn_readfirstlane((int)part[2 * g + 1]);
-    p.kb = kb;
-    p.x = a.h + (int64_t)t0 * a.k * a.F * (kWideHidden<T> ? 4 : 2);
-    p.w[0] = block_start(a.down + (int64_t)expert * a.D * a.F, d0, a.D, pitch);
-    p.wo[0] = block_row(d0, lane >> 2, a.D, pitch);
+  job.x = a.h + (int64_t)t0 * a.k * a.F * (kWideHidden<T> ? 4 : 2);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int j = 16 * m + (lane >> 2), which = from + (j < n ? j : n - 1);
-      p.xo[m] = (uint32_t)list[which] * (uint32_t)a.F * (kWideHidden<T> ? 4u : 2u);
-      p.scale[m] = kWideHidden<T> ? ldexpf(1.0f, power[list[which]]) : 1.0f;
-    }
+  for (int b = 0; b < NT; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) job.wo[b][r] = block_row(d0 + 16 * b, 4 * r + (lane >> 4), a.D, pitch);
+  auto part_rows = [&](int g) __attribute__((always_inline)) {  // a part's rows
+    const uint32_t v = part[2 * g];
+    const int from = (int)(v & 0xffffu), n = __builtin_amdgcn_readfirstlane((int)(v >> 16));
+    const int expert = __builtin_amdgcn_readfirstlane((int)part[2 * g + 1]);
+    job.have = n;
+    const uint16_t *down = a.down + (int64_t)expert * a.D * a.F;
+#pragma unroll
+    for (int b = 0; b < NT; ++b) job.w[b] = block_start(down, d0 + 16 * b, a.D, pitch);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int j = 16 * m + 4 * r + (lane >> 4), choice = list[from + (j < n ? j : n - 1)];
+        job.xo[m][r] = (uint32_t)choice * (uint32_t)a.F * (kWideHidden<T> ? 4u : 2u);
+        job.scale[m][r] = kWideHidden<T> ? ldexpf(1.0f, power[choice]) : 1.0f;
+      }
   };
   auto add = [&](int g) __attribute__((always_inline)) {
     const uint32_t v = part[2 * g];
@@ -396,49 +407,47 @@ __global__ void __launch_bounds__(WAVES * 64, MT < 4 ? 4 : 2) moe_down_kernel(Mo
         const int j = 16 * m + 4 * q + r;
         if (j >= n) continue;
         const int choice = list[from + j];
-        float s = job.tot[m][0][r];
-        if constexpr (kWideHidden<T>) s = ldexpf(s, -power[choice]);
-        rows[(wave * tokens + choice / a.k) * 16 + c] += weight[choice] * s;
+#pragma unroll
+        for (int b = 0; b < NT; ++b) {
+          float s = job.tot[m][b][r];
+          if constexpr (kWideHidden<T>) s = ldexpf(s, -power[choice]);
+          rows[(wave * tokens + choice / a.k) * kMoeColumns + 16 * b + c] += weight[choice] * s;
+        }
       }
     job.clear();
   };
   if constexpr (SHORT) {
-    typename Stream::Place at;
     for (; i < end; ++i) {
-      place(at, (int)i, 0);
-      job.short_rows(at);
+      part_rows((int)i);
+      job.short_rows();
       add((int)i);
     }
   } else if (i < end) {
     int g = __builtin_amdgcn_readfirstlane((int)(i / blocks)), kb = __builtin_amdgcn_readfirstlane((int)(i % blocks));
-    typename Stream::Place at, next;
-    place(at, g, kb);
-    job.begin(at);
+    auto same = []() {};
+    part_rows(g);
+    job.begin_weights(kb);
+    job.load_x(kb);
     for (++i; i < end; ++i) {
-      if (kb + 1 < blocks) {
-        next = at;
-        next.kb = ++kb;
-        job.template block<true>(at, next);
-      } else {
-        kb = 0;
-        place(next, g + 1, 0);
-        job.template block<true>(at, next);
-        add(g);
-        ++g;
-      }
-      at = next;
+      const bool leaves = kb + 1 == blocks;
+      const int to = leaves ? 0 : kb + 1;
+      job.template block<true>(kb, to, [&]() {
+        if (leaves) part_rows(g + 1);
+      });
+      if (leaves) add(g++);
+      kb = to;
     }
-    job.template block<false>(at, at);
+    job.template block<false>(kb, kb, same);
     add(g);
   }
   __syncthreads();
-  for (int j = tid; j < tokens * 16; j += THREADS) {
-    const int col = d0 + j % 16;
+  for (int j = tid; j < tokens * kMoeColumns; j += THREADS) {
+    const int col = d0 + j % kMoeColumns;
     if (col >= a.D) continue;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) v += rows[w * tokens * 16 + j];
-    const int64_t to = (int64_t)(t0 + j / 16) * a.D + col;
+    for (int w = 0; w < WAVES; ++w) v += rows[w * tokens * kMoeColumns + j];
+    const int64_t to = (int64_t)(t0 + j / kMoeColumns) * a.D + col;
     if (a.splits == 1)
       a.y[to] = __builtin_bit_cast(uint16_t, (T)v);
     else
@@ -457,10 +466,10 @@ __global__ void __launch_bounds__(WAVES * 64, MT < 4 ? 4 : 2) moe_down_kernel(Mo
   __syncthreads();
   if (!*last_one) return;
   compiler_fence();
-  for (int j = tid; j < tokens * 16; j += THREADS) {
-    const int col = d0 + j % 16;
+  for (int j = tid; j < tokens * kMoeColumns; j += THREADS) {
+    const int col = d0 + j % kMoeColumns;
     if (col >= a.D) continue;
-    const int64_t to = (int64_t)(t0 + j / 16) * a.D + col;
+    const int64_t to = (int64_t)(t0 + j / kMoeColumns) * a.D + col;
     float v = 0.0f;
     for (int i = 0; i < a.splits; ++i)
       v += __hip_atomic_load(a.partial + (int64_t)i * a.M * a.D + to, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

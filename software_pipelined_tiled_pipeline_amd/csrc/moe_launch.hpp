@@ -7,11 +7,18 @@
 namespace pgemm {
 namespace launch_detail {
 
+constexpr int kMoeLds = 160 * 1024;  // a CU's
+
 template <typename T, int MT, int WAVES, bool SHORT = false>
-pgemm_status launch_moe_gated(const MoeArgs &a, int64_t chunks, hipStream_t stream) {
-  constexpr int LDS = 144 + WAVES * MT * 2 * 4 * 256;
-  static_assert(LDS <= 65536, "what a kernel may use without asking");
+pgemm_status launch_moe_gated(const MoeArgs &a, int64_t chunks, hipStream_t stream, int dev) {
+  static std::atomic<uint64_t> lds_set{0};
+  constexpr int LDS = 144 + WAVES * stream_bytes(MT);
+  static_assert(stream_bytes(MT) >= MT * 2048 && LDS <= 160 * 1024, "the sums take the blocks' place");
   auto kern = moe_gated_kernel<T, MT, WAVES, SHORT>;
+  if (LDS > 65536) {
+    pgemm_status st = allow_lds(kern, LDS, dev, lds_set);
+    if (st != PGEMM_OK) return st;
+  }
   hipLaunchKernelGGL(kern, dim3((unsigned)per(a.F, 16), (unsigned)a.slots, (unsigned)chunks), dim3(WAVES * 64), LDS, stream, a);
   return launched();
 }
@@ -19,14 +26,13 @@ pgemm_status launch_moe_gated(const MoeArgs &a, int64_t chunks, hipStream_t stre
 template <typename T, int MT, int WAVES, bool SHORT = false>
 pgemm_status launch_moe_down(const MoeArgs &a, int64_t chunks, hipStream_t stream, int dev) {
   static std::atomic<uint64_t> lds_set{0};
-  constexpr int kMost = 160 * 1024;
   auto kern = moe_down_kernel<T, MT, WAVES, SHORT>;
-  const int lds = moe_down_lds(WAVES, a.M < kMoeChunk ? a.M : kMoeChunk, a.k, a.slots);
+  const int lds = moe_down_lds(MT, WAVES, a.M < kMoeChunk ? a.M : kMoeChunk, a.k, a.slots);
   if (lds > 65536) {
-    pgemm_status st = allow_lds(kern, kMost, dev, lds_set);
+    pgemm_status st = allow_lds(kern, kMoeLds, dev, lds_set);
     if (st != PGEMM_OK) return st;
   }
-  hipLaunchKernelGGL(kern, dim3((unsigned)per(a.D, 16), (unsigned)chunks, (unsigned)a.splits), dim3(WAVES * 64), lds, stream, a);
+  hipLaunchKernelGGL(kern, dim3((unsigned)per(a.D, kMoeColumns), (unsigned)chunks, (unsigned)a.splits), dim3(WAVES * 64), lds, stream, a);
   return launched();
 }
 
@@ -74,16 +80,19 @@ pgemm_status moe_layer(const MoeCall &c) {
   const int64_t mean = (c.M < kMoeChunkTokens ? c.M : kMoeChunkTokens) * c.top_k / c.E;
   if (c.F > 0) {
     const bool many = per(c.F, 16) * p.slots * chunks > 512;
-    st = c.D < 8     ? launch_moe_gated<T, 1, 8, true>(a, chunks, c.stream)
-         : mean > 24 ? launch_moe_gated<T, 4, 4>(a, chunks, c.stream)
-         : mean > 8 ? many ? launch_moe_gated<T, 2, 4>(a, chunks, c.stream) : launch_moe_gated<T, 2, 8>(a, chunks, c.stream)
-                    : many ? launch_moe_gated<T, 1, 4>(a, chunks, c.stream) : launch_moe_gated<T, 1, 8>(a, chunks, c.stream);
+    st = c.D < 8     ? launch_moe_gated<T, 1, 8, true>(a, chunks, c.stream, c.dev)
+         : mean > 24 ? launch_moe_gated<T, 4, 4>(a, chunks, c.stream, c.dev)
+         : mean > 8 ? many ? launch_moe_gated<T, 2, 4>(a, chunks, c.stream, c.dev) : launch_moe_gated<T, 2, 8>(a, chunks, c.stream, c.dev)
+                    : many ? launch_moe_gated<T, 1, 4>(a, chunks, c.stream, c.dev) : launch_moe_gated<T, 1, 8>(a, chunks, c.stream, c.dev);
     if (st != PGEMM_OK) return st;
   }
-  return c.F < 8     ? launch_moe_down<T, 1, 8, true>(a, chunks, c.stream, c.dev)
-         : mean <= 8 ? launch_moe_down<T, 1, 8>(a, chunks, c.stream, c.dev)
-                     : mean <= 24 ? launch_moe_down<T, 2, 8>(a, chunks, c.stream, c.dev)
-                                  : launch_moe_down<T, 4, 8>(a, chunks, c.stream, c.dev);
+  // eight waves where their rows of y find room in LDS
+  const bool wide = moe_down_lds(1, 8, a.M < kMoeChunk ? a.M : kMoeChunk, a.k, a.slots) <= kMoeLds;
+  return c.F < 8      ? launch_moe_down<T, 1, 4, true>(a, chunks, c.stream, c.dev)
+         : mean > 24  ? launch_moe_down<T, 4, 4>(a, chunks, c.stream, c.dev)
+         : mean > 8   ? launch_moe_down<T, 2, 4>(a, chunks, c.stream, c.dev)
+         : wide       ? launch_moe_down<T, 1, 8>(a, chunks, c.stream, c.dev)
+                      : launch_moe_down<T, 1, 4>(a, chunks, c.stream, c.dev);
 }
 
 }  // namespace launch_detail

@@ -4,11 +4,14 @@
 // A wave multiplies MT blocks of 16 tokens with NT blocks of 16 weight rows,
 // block of K by block of K.  Widths count units of two bytes: a 16-bit value or
 // two 8-bit ones; a block is 128 of them, 256 bytes of a row, in four MFMA
-// steps.  Four lanes load 64 bytes of a row, so that a load is 16 requests and
-// not one a lane; the values change lanes to where the MFMAs want them, row
-// l % 16, with ds_bpermute (skinny.hpp has what that is worth).  The next
-// block's loads are issued step by step while this one is multiplied, also
-// where the next block belongs to other rows.
+// steps.  Sixteen lanes load a row's 256 bytes, four rows a load, so that rows
+// that start on no cache line cost few lines twice; the block goes through 4 KiB
+// of LDS of the wave's own to where the MFMAs want it, row l % 16.  (With four
+// lanes to 64 bytes of a row, and the lanes changed by ds_bpermute as in
+// skinny.hpp, experts of 2050 x 1001 values took 109 and 84 us instead of 88 and
+// 76 for their two products, where they are reached by 37 tokens four times each.)  The next block's
+// loads are on the way while this one is multiplied, also where the next block
+// belongs to other rows.
 //   lane l, register r of an accumulator: token 4 (l / 16) + r, weight row l % 16.
 #pragma once
 
@@ -31,33 +34,39 @@ struct Int8Step {
 // l / 16); or in memory in fp32, to be rounded to T after a factor of their row.
 enum class Tokens { Rows, Lds, Wide };
 
+constexpr int kBlockBytes = 4096;  // of 16 rows
+// LDS of a wave: each block of tokens, and a block of weights
+constexpr int stream_bytes(int mt) { return (mt + 1) * kBlockBytes; }
+
 template <class F, int MT, int NT, Tokens X = Tokens::Rows, typename T = void>
 struct RowStream {
-  static constexpr int XD = MT == 1 && X != Tokens::Wide ? 4 : 2;  // steps that tokens are loaded ahead
   static constexpr int XP = X == Tokens::Wide ? 2 : 1;  // 16-byte pieces of a token's share
 
-  // A block's place: where the tokens and each block of weight rows start, the
-  // same for the wave; this lane's rows (row l / 4 of each block) from there,
-  // below 2^31 bytes; the block of K.
-  struct Place {
-    const char *x, *w[NT];
-    uint32_t xo[MT], wo[NT];
-    float scale[MT];  // Wide: of x's rows
-    int kb;
-  };
+  // Where the tokens and each block of weight rows start, the same for the wave,
+  // and this lane's rows (4 i + l / 16 of each block) from there, below 2^31 bytes.
+  const char *x, *w[NT];
+  uint32_t xo[MT][4], wo[NT][4];
+  float scale[MT][4];  // Wide: of x's rows
+  // Tokens there are.  The rows of a block past them are neither loaded nor put
+  // into LDS: what they hold there reaches no token's sums.
+  int have;
 
   int K, full;  // units of a row; whole blocks
-  int from;     // the lane its fragments come from, in bytes
-  int piece;    // which 16 bytes of a step it loads
+  int piece;    // which 16 bytes of a row's block it loads
+  char *put_at, *get_at;  // this lane's row in the wave's LDS, as it loads and as it multiplies
+  int row, part;          // that row, and 16-byte piece
   f32x4 tot[MT][NT];
-  u32x4 xr[XD][MT][XP], wr[4][NT];
+  u32x4 xr[MT][4][XP], wr[NT][4];
   const char *xl;
 
-  __device__ __forceinline__ void init(int lane, int units) {
+  __device__ __forceinline__ void init(int lane, int units, char *lds) {
     K = units;
     full = units / 128;
-    from = (4 * (lane & 15) + (lane >> 4)) * 4;
-    piece = lane & 3;
+    piece = lane & 15;
+    put_at = lds + (lane >> 4) * 256;
+    row = lane & 15;
+    part = lane >> 4;
+    get_at = lds + row * 256;
     clear();
   }
   __device__ __forceinline__ void clear() {
@@ -68,119 +77,144 @@ struct RowStream {
   }
   __device__ __forceinline__ int blocks() const { return (K + 127) / 128; }
 
-  // Eight units of a row for step s of block kb.  In the block that K ends in
-  // the row's last eight, put in place when they are used.
-  __device__ __forceinline__ u32x4 load(const char *base, uint32_t row, int kb, int s) const {
-    if (kb < full) return load_at<u32x4_any>(base + ((int64_t)kb * 256 + s * 64), row + 16u * piece);
-    const int k = kb * 128 + 32 * s + 8 * piece;
-    return load_at<u32x4_any>(base, row + 2u * (k < K - 8 ? k : K - 8));
+  // A lane's eight units of a row's block.  In the block that K ends in the
+  // row's last eight, put in place when they are used.
+  __device__ __forceinline__ int unit(int kb) const {
+    const int k = kb * 128 + 8 * piece;
+    return kb < full || k < K - 8 ? k : K - 8;
   }
-  __device__ __forceinline__ u32x4 used(u32x4 v, int kb, int s) const {
+  __device__ __forceinline__ u32x4 in_place(u32x4 v, int kb) const {
     if (kb >= full) {
-      const int past = kb * 128 + 32 * s + 8 * piece - (K - 8);
+      const int past = kb * 128 + 8 * piece - (K - 8);
       v = drop_values(v, past > 0 ? past : 0);
     }
-    return to_rows(v, from);
+    return v;
   }
-  __device__ __forceinline__ void load_x(const Place &p, int slot, int s) {
+  // Row 4 i + l / 16 of the wave's LDS: pieces in an order of the row's own, so
+  // that the sixteen rows that a read touches lie on different banks.
+  // Block `which` is the weights' at MT, else tokens'.
+  __device__ __forceinline__ void put(int which, int i, u32x4 v) const {
+    *reinterpret_cast<u32x4 *>(put_at + which * kBlockBytes + i * 1024 + ((piece ^ (4 * i + part)) * 16)) = v;
+  }
+  __device__ __forceinline__ u32x4 get(int which, int s) const {
+    return *reinterpret_cast<const u32x4 *>(get_at + which * kBlockBytes + (((4 * s + part) ^ row) * 16));
+  }
+
+  __device__ __forceinline__ void load_x(int kb) {
     if constexpr (X == Tokens::Lds) return;
+    const int k = unit(kb);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if constexpr (X == Tokens::Wide) {
-        const int k = p.kb * 128 + 32 * s + 8 * piece;
-        const uint32_t at = p.xo[m] + 4u * (p.kb < full || k < K - 8 ? k : K - 8);
-        xr[slot][m][0] = load_at<u32x4_any>(p.x, at);
-        xr[slot][m][1] = load_at<u32x4_any>(p.x, at + 16u);
-      } else {
-        xr[slot][m][0] = load(p.x, p.xo[m], p.kb, s);
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (16 * m + 4 * i >= have) break;
+        if constexpr (X == Tokens::Wide) {
+          xr[m][i][0] = load_at<u32x4_any>(x, xo[m][i] + 4u * k);
+          xr[m][i][1] = load_at<u32x4_any>(x, xo[m][i] + 4u * k + 16u);
+        } else {
+          xr[m][i][0] = load_at<u32x4_any>(x, xo[m][i] + 2u * k);
+        }
       }
+  }
+  __device__ __forceinline__ void load_w(int b, int kb) {
+    const int k = unit(kb);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wr[b][i] = load_at<u32x4_any>(w[b], wo[b][i] + 2u * k);
+  }
+  __device__ __forceinline__ void begin_weights(int kb) {
+#pragma unroll
+    for (int b = 0; b < NT; ++b) load_w(b, kb);
+  }
+
+  __device__ __forceinline__ u32x4 token_piece(int m, int i) const {
+    if constexpr (X == Tokens::Wide) {
+      u32x4 v;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const f32x4 f = __builtin_bit_cast(f32x4, xr[m][i][e]) * scale[m][i];
+        const u32x2 two = Mfma<T>::pack4(f[0], f[1], f[2], f[3]);
+        v[2 * e] = two[0];
+        v[2 * e + 1] = two[1];
+      }
+      return v;
+    } else {
+      return xr[m][i][0];
     }
-  }
-  __device__ __forceinline__ void load_w(const Place &p, int s) {
-#pragma unroll
-    for (int b = 0; b < NT; ++b) wr[s][b] = load(p.w[b], p.wo[b], p.kb, s);
-  }
-  __device__ __forceinline__ void begin_weights(const Place &p) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s) load_w(p, s);
-  }
-  __device__ __forceinline__ void begin_tokens(const Place &p) {
-#pragma unroll
-    for (int s = 0; s < XD; ++s) load_x(p, s, s);
-  }
-  __device__ __forceinline__ void begin(const Place &p) {
-    begin_weights(p);
-    begin_tokens(p);
   }
 
   // All of rows shorter than eight units, value by value (not from LDS).
-  __device__ __forceinline__ void short_rows(const Place &p) {
-    u32x4 x[MT];
+  __device__ __forceinline__ void short_rows() {
+    u32x4 xs[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      u32x4 v = {0u, 0u, 0u, 0u};
-      if constexpr (X == Tokens::Wide) {
-        if (piece == 0) {
-          const float *row = reinterpret_cast<const float *>(p.x + p.xo[m]);
 #pragma unroll
-          for (int e = 0; e < 7; ++e) {
-            if (e < K) v[e / 2] |= Mfma<T>::pack4(row[e] * p.scale[m], 0.0f, 0.0f, 0.0f)[0] << (16 * (e % 2));
+      for (int i = 0; i < 4; ++i) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (piece == 0) {
+          if constexpr (X == Tokens::Wide) {
+            const float *from = reinterpret_cast<const float *>(x + xo[m][i]);
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+              if (e < K) v[e / 2] |= Mfma<T>::pack4(from[e] * scale[m][i], 0.0f, 0.0f, 0.0f)[0] << (16 * (e % 2));
+          } else {
+            v = load_tail(reinterpret_cast<const uint16_t *>(x + xo[m][i]), 0, K);
           }
         }
-      } else {
-        if (piece == 0) v = load_tail(reinterpret_cast<const uint16_t *>(p.x + p.xo[m]), 0, K);
+        put(0, i, v);
       }
-      x[m] = to_rows(v, from);
+      xs[m] = get(0, 0);
     }
 #pragma unroll
     for (int b = 0; b < NT; ++b) {
-      u32x4 v = {0u, 0u, 0u, 0u};
-      if (piece == 0) v = load_tail(reinterpret_cast<const uint16_t *>(p.w[b] + p.wo[b]), 0, K);
-      v = to_rows(v, from);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) tot[m][b] = F::mma(x[m], v, tot[m][b]);
+      for (int i = 0; i < 4; ++i) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (piece == 0) v = load_tail(reinterpret_cast<const uint16_t *>(w[b] + wo[b][i]), 0, K);
+        put(MT, i, v);
+      }
+      const u32x4 ws = get(MT, 0);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) tot[m][b] = F::mma(xs[m], ws, tot[m][b]);
     }
   }
 
-  // Block `at`, while block `next` loads (rows of eight units and more).
-  template <bool MORE>
-  __device__ __forceinline__ void block(const Place &at, const Place &next) {
+  // Block kb, while block next loads (rows of eight units and more); `move`
+  // sets the rows that it is of, if they are others.
+  template <bool MORE, typename Move>
+  __device__ __forceinline__ void block(int kb, int next, Move &&move) {
+    if constexpr (X != Tokens::Lds) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      u32x4 x[MT];
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        if constexpr (X == Tokens::Lds) {
-          x[m] = *reinterpret_cast<const u32x4 *>(xl + at.kb * 256 + s * 64);
-        } else if constexpr (X == Tokens::Wide) {
-          u32x4 v;
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            const f32x4 f = __builtin_bit_cast(f32x4, xr[s % XD][m][e / 4]) * at.scale[m];
-            const u32x2 p = Mfma<T>::pack4(f[0], f[1], f[2], f[3]);
-            v[e / 2] = p[0];
-            v[e / 2 + 1] = p[1];
-          }
-          x[m] = used(v, at.kb, s);
-        } else {
-          x[m] = used(xr[s % XD][m][0], at.kb, s);
+        for (int i = 0; i < 4; ++i) {
+          if (16 * m + 4 * i >= have) break;
+          put(m, i, in_place(token_piece(m, i), kb));
         }
-      }
+    }
+    if (MORE) {
+      move();
+      load_x(next);
+    }
 #pragma unroll
-      for (int b = 0; b < NT; ++b) {
-        const u32x4 w = used(wr[s][b], at.kb, s);
+    for (int b = 0; b < NT; ++b) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) tot[m][b] = F::mma(x[m], w, tot[m][b]);
+      for (int i = 0; i < 4; ++i) put(MT, i, in_place(wr[b][i], kb));
+      if (MORE) load_w(b, next);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const u32x4 ws = get(MT, s);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const u32x4 xs = X == Tokens::Lds ? *reinterpret_cast<const u32x4 *>(xl + kb * 256 + s * 64) : get(m, s);
+          tot[m][b] = F::mma(xs, ws, tot[m][b]);
+        }
+        if (s == 1) __builtin_amdgcn_sched_barrier(0);  // two steps' fragments at a time
       }
-      if (MORE) load_w(next, s);
-      // the slot of step s takes step s + XD
-      if (s + XD < 4)
-        load_x(at, s % XD, s + XD);
-      else if (MORE)
-        load_x(next, s % XD, s + XD - 4);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 };
+
 // (Widths below eight units, in which load_tail reads a row value by value, are
 // left out of the loop: its loads took 70 registers.)
 
