@@ -103,13 +103,10 @@ __device__ __forceinline__ double moe_value(uint64_t o) {
 
 constexpr int kMoeChunk = kMoeChunkTokens, kMoeColumns = kMoeDownColumns;
 
-// A wave a token, up to 64 PER experts: top_k times the largest logit that is
-// left, the lowest index of equal ones.
+// Top_k times the largest logit l that is left, the lowest index of equal ones, by
+// one wave, for up to 64 PER experts; the sums' weights.
 template <int PER>
-__global__ void __launch_bounds__(64) moe_choose_kernel(MoeArgs a) {
-  const int lane = threadIdx.x, m = blockIdx.x;
-  for (int i = m * 64 + lane; i < a.groups; i += a.M * 64) a.arrived[i] = 0;
-  const double *l = a.logits + (int64_t)m * a.E;
+__device__ __forceinline__ void moe_choose(const MoeArgs &a, const double *l, int m, int lane) {
   uint64_t left[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) left[i] = i * 64 + lane < a.E ? moe_order(l[i * 64 + lane]) : 0;
@@ -151,6 +148,54 @@ __global__ void __launch_bounds__(64) moe_choose_kernel(MoeArgs a) {
     a.weights[at] = (float)(mine / total);
     if (a.tops) a.tops[at] = 0;
   }
+}
+
+// A wave a token.
+template <int PER>
+__global__ void __launch_bounds__(64) moe_choose_kernel(MoeArgs a) {
+  const int lane = threadIdx.x, m = blockIdx.x;
+  for (int i = m * 64 + lane; i < a.groups; i += a.M * 64) a.arrived[i] = 0;
+  moe_choose<PER>(a, a.logits + (int64_t)m * a.E, m, lane);
+}
+
+// Both for a token in one workgroup, where the router is small: its logits, an
+// expert a wave at a time, and then the choice.  One launch less: with 8 experts
+// of 1024 values 3.5 us instead of 2.7 and 2.5.
+constexpr int kMoeRouteExperts = 64, kMoeRouteValues = 65536;
+template <typename T>
+__global__ void __launch_bounds__(1024) moe_route_kernel(MoeArgs a) {
+  __shared__ double logits[kMoeRouteExperts];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = blockIdx.x;
+  for (int i = m * 1024 + tid; i < a.groups; i += a.M * 1024) a.arrived[i] = 0;
+  const uint16_t *x = a.x + (int64_t)m * a.D;
+  auto eight = [&](const uint16_t *row, int k) {
+    if (k + 8 <= a.D) return (u32x4)*reinterpret_cast<const u32x4_any *>(row + k);
+    return k < a.D ? load_tail(row, k, a.D) : u32x4{0u, 0u, 0u, 0u};
+  };
+  for (int e = wave; e < a.E; e += 16) {
+    const uint16_t *r = a.router + (int64_t)e * a.D;
+    double sum = 0.0;
+    for (int k0 = 0; k0 < a.D; k0 += 2048) {
+      u32x4 xv[4], rv[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + j * 512 + lane * 8;
+        xv[j] = eight(x, k);
+        rv[j] = eight(r, k);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+          sum = __builtin_fma((double)widen<T>((uint16_t)(xv[j][n / 2] >> (16 * (n % 2)))),
+                              (double)widen<T>((uint16_t)(rv[j][n / 2] >> (16 * (n % 2)))), sum);
+    }
+    sum = wave_scan(sum);
+    if (lane == 63) logits[e] = sum;
+  }
+  __syncthreads();
+  if (wave == 0) moe_choose<1>(a, logits, m, lane);
 }
 
 // ---------------------------------------------------------- gated blocks ---

@@ -66,15 +66,21 @@ pgemm_status moe_layer(const MoeCall &c) {
   a.by_choice = p.by_choice;
   a.act = c.act;
   a.normalize = c.normalize;
-  if (c.M <= 4)
-    hipLaunchKernelGGL((moe_logits_kernel<T, 1>), dim3((unsigned)c.E, (unsigned)c.M), dim3(256), 0, c.stream, a);
-  else
-    hipLaunchKernelGGL((moe_logits_kernel<T, 4>), dim3((unsigned)c.E, (unsigned)per(c.M, 4)), dim3(256), 0, c.stream, a);
-  pgemm_status st = launched();
-  if (st != PGEMM_OK) return st;
-  auto choose = c.E <= 64 ? moe_choose_kernel<1> : c.E <= 256 ? moe_choose_kernel<4> : moe_choose_kernel<16>;
-  hipLaunchKernelGGL(choose, dim3((unsigned)c.M), dim3(64), 0, c.stream, a);
-  st = launched();
+  pgemm_status st;
+  if (c.E <= kMoeRouteExperts && c.E * c.D <= kMoeRouteValues) {
+    hipLaunchKernelGGL(moe_route_kernel<T>, dim3((unsigned)c.M), dim3(1024), 0, c.stream, a);
+    st = launched();
+  } else {
+    if (c.M <= 4)
+      hipLaunchKernelGGL((moe_logits_kernel<T, 1>), dim3((unsigned)c.E, (unsigned)c.M), dim3(256), 0, c.stream, a);
+    else
+      hipLaunchKernelGGL((moe_logits_kernel<T, 4>), dim3((unsigned)c.E, (unsigned)per(c.M, 4)), dim3(256), 0, c.stream, a);
+    st = launched();
+    if (st != PGEMM_OK) return st;
+    auto choose = c.E <= 64 ? moe_choose_kernel<1> : c.E <= 256 ? moe_choose_kernel<4> : moe_choose_kernel<16>;
+    hipLaunchKernelGGL(choose, dim3((unsigned)c.M), dim3(64), 0, c.stream, a);
+    st = launched();
+  }
   if (st != PGEMM_OK || c.D == 0) return st;
   // tokens an expert has on average
   const int64_t mean = (c.M < kMoeChunkTokens ? c.M : kMoeChunkTokens) * c.top_k / c.E;

@@ -10,8 +10,25 @@ namespace pgemm {
 // The largest K whose sums of products of two 8-bit integers stay in int32.
 constexpr int64_t kI8MaxK = ((int64_t)1 << 17) - 16;
 
-// How an 8-bit product runs: by few_rows kernels up to 64 tokens, else in tiles.
-constexpr int64_t kI8FewRows = 64;
+// An 8-bit product of up to 256 tokens by the kernel for few of them, or in
+// tiles, whichever takes less: microseconds, by what a workgroup's 256 bytes of K
+// were measured to take with 16, 32 or 64 tokens, where at least half of the CUs
+// have one, and by plan_tiles, or the weights' way from memory where that is
+// longer.  Measured, tiles and few tokens, for tokens x columns x K:
+//   8 x 4096 x 4096   10.1  6.8     64 x 12288 x 4096  20.5 22.5     128 x 4096 x 4096   15.7 10.4
+//   8 x 8192 x 8192   17.5 14.1     64 x 8192 x 8192   25.1 21.1     128 x 8192 x 8192   29.8 36.9
+//   8 x 28672 x 4096  29.4 23.1     64 x 28672 x 4096  30.4 40.0     128 x 28672 x 4096  31.9 64.4
+// and gated
+//   32 x 12288 x 4096  26.9 22.1    64 x 12288 x 4096  27.5 33.0     64 x 1024 x 8192    25.8 15.0
+constexpr int64_t kI8FewRows = 256;
+inline double i8_few_us(int64_t M, int64_t groups, int64_t width) {
+  const double mine = M <= 16 ? 0.36 : M <= 32 ? 0.42 : 0.6;
+  return 3.5 + mine * (double)per(width, 256) * (groups > 128 ? (double)groups : 128.0) / 256.0;
+}
+inline double i8_tiles_us(const Tiling &t, int64_t rows, int64_t width) {
+  const double bytes = 4.0 + (double)rows * (double)width / 4.6e6;
+  return t.us > bytes ? t.us : bytes;
+}
 
 struct I8Plan {
   bool few;
@@ -26,14 +43,15 @@ inline I8Plan plan_i8(int64_t M, int64_t N, int64_t K, bool gated, bool quantize
   I8Plan p{};
   Carver c;
   const int64_t width = up_to(K, 16);
-  p.few = M <= kI8FewRows;
+  p.tiles = plan_tiles(M, N, width / 2, gated, Cuts{!gated, true});
+  const int64_t groups = per(N, gated ? 16 : 32) * per(M, M <= 16 ? 16 : M <= 32 ? 32 : 64);
+  p.few = M <= kI8FewRows && i8_few_us(M, groups, width) < i8_tiles_us(p.tiles, gated ? 2 * N : N, width);
   p.own = p.few && !quantized && M <= 4 && K >= 8 && K <= 8192;
   if (!quantized && !p.own) {
     p.q = c.take(M * width);
     p.s = c.take(M * 4);
   }
   if (!p.few) {
-    p.tiles = plan_tiles(M, N, width / 2, gated, Cuts{!gated, true});
     p.part = c.take(piece_bytes(p.tiles, M, N));
   }
   p.bytes = c.bytes;
