@@ -7,33 +7,34 @@
 namespace pgemm {
 namespace launch_detail {
 
-constexpr int kMoeLds = 160 * 1024;  // a CU's
-
-template <typename T, int MT, int WAVES, bool SHORT = false>
-pgemm_status launch_moe_gated(const MoeArgs &a, int64_t chunks, hipStream_t stream, int dev) {
+template <typename T, int MT, int WAVES, bool DOWN, bool SHORT>
+pgemm_status launch_moe_rows_one(const MoeArgs &a, int64_t chunks, hipStream_t stream, int dev) {
   static std::atomic<uint64_t> lds_set{0};
   constexpr int LDS = 144 + WAVES * stream_bytes(MT);
   static_assert(stream_bytes(MT) >= MT * 2048 && LDS <= 160 * 1024, "the sums take the blocks' place");
-  auto kern = moe_gated_kernel<T, MT, WAVES, SHORT>;
+  auto kern = moe_rows_kernel<T, MT, WAVES, DOWN, SHORT>;
   if (LDS > 65536) {
     pgemm_status st = allow_lds(kern, LDS, dev, lds_set);
     if (st != PGEMM_OK) return st;
   }
-  hipLaunchKernelGGL(kern, dim3((unsigned)per(a.F, 16), (unsigned)a.slots, (unsigned)chunks), dim3(WAVES * 64), LDS, stream, a);
+  const int64_t groups = DOWN ? per(a.D, 32) : per(a.F, 16);
+  hipLaunchKernelGGL(kern, dim3((unsigned)groups, (unsigned)a.slots, (unsigned)chunks), dim3(WAVES * 64), LDS, stream, a);
   return launched();
 }
 
-template <typename T, int MT, int WAVES, bool SHORT = false>
-pgemm_status launch_moe_down(const MoeArgs &a, int64_t chunks, hipStream_t stream, int dev) {
-  static std::atomic<uint64_t> lds_set{0};
-  auto kern = moe_down_kernel<T, MT, WAVES, SHORT>;
-  const int lds = moe_down_lds(MT, WAVES, a.M < kMoeChunk ? a.M : kMoeChunk, a.k, a.slots);
-  if (lds > 65536) {
-    pgemm_status st = allow_lds(kern, kMoeLds, dev, lds_set);
-    if (st != PGEMM_OK) return st;
-  }
-  hipLaunchKernelGGL(kern, dim3((unsigned)per(a.D, kMoeColumns), (unsigned)chunks, (unsigned)a.splits), dim3(WAVES * 64), lds, stream, a);
-  return launched();
+// Blocks of 16 tokens by how many an expert has on average; waves along K so
+// that all workgroups together give each CU about sixteen.
+template <typename T, bool DOWN>
+pgemm_status launch_moe_rows(const MoeArgs &a, int64_t chunks, hipStream_t stream, int dev) {
+  if ((DOWN ? a.F : a.D) < 8) return launch_moe_rows_one<T, 1, 8, DOWN, true>(a, chunks, stream, dev);
+  const int64_t mean = (a.M < kMoeChunk ? a.M : kMoeChunk) * a.k / a.E;
+  const bool many = (DOWN ? per(a.D, 32) : per(a.F, 16)) * a.slots * chunks > 512;
+  if (mean > 24) return launch_moe_rows_one<T, 4, 4, DOWN, false>(a, chunks, stream, dev);
+  if (mean > 8)
+    return many ? launch_moe_rows_one<T, 2, 4, DOWN, false>(a, chunks, stream, dev)
+                : launch_moe_rows_one<T, 2, 8, DOWN, false>(a, chunks, stream, dev);
+  return many ? launch_moe_rows_one<T, 1, 4, DOWN, false>(a, chunks, stream, dev)
+              : launch_moe_rows_one<T, 1, 8, DOWN, false>(a, chunks, stream, dev);
 }
 
 template <typename T>
@@ -51,23 +52,18 @@ pgemm_status moe_layer(const MoeCall &c) {
   a.logits = reinterpret_cast<double *>(c.workspace + p.logits);
   a.h = c.workspace + p.h;
   a.tops = kWideHidden<T> ? reinterpret_cast<uint32_t *>(c.workspace + p.tops) : nullptr;
-  a.counts = reinterpret_cast<uint32_t *>(c.workspace + p.counts);
-  a.lists = reinterpret_cast<uint16_t *>(c.workspace + p.lists);
+  a.products = reinterpret_cast<float *>(c.workspace + p.products);
   a.M = (int)c.M;
   a.E = (int)c.E;
   a.D = (int)c.D;
   a.F = (int)c.F;
   a.k = (int)c.top_k;
   a.slots = (int)p.slots;
-  a.splits = (int)p.splits;
-  a.groups = (int)p.groups;
-  a.partial = reinterpret_cast<float *>(c.workspace + p.partial);
-  a.arrived = reinterpret_cast<uint32_t *>(c.workspace + p.arrived);
   a.by_choice = p.by_choice;
   a.act = c.act;
   a.normalize = c.normalize;
   pgemm_status st;
-  if (c.E <= kMoeRouteExperts && c.E * c.D <= kMoeRouteValues) {
+  if (c.E <= kMoeRouteExperts && c.D <= kMoeRouteValues) {
     hipLaunchKernelGGL(moe_route_kernel<T>, dim3((unsigned)c.M), dim3(1024), 0, c.stream, a);
     st = launched();
   } else {
@@ -82,23 +78,14 @@ pgemm_status moe_layer(const MoeCall &c) {
     st = launched();
   }
   if (st != PGEMM_OK || c.D == 0) return st;
-  // tokens an expert has on average
-  const int64_t mean = (c.M < kMoeChunkTokens ? c.M : kMoeChunkTokens) * c.top_k / c.E;
   if (c.F > 0) {
-    const bool many = per(c.F, 16) * p.slots * chunks > 512;
-    st = c.D < 8     ? launch_moe_gated<T, 1, 8, true>(a, chunks, c.stream, c.dev)
-         : mean > 24 ? launch_moe_gated<T, 4, 4>(a, chunks, c.stream, c.dev)
-         : mean > 8 ? many ? launch_moe_gated<T, 2, 4>(a, chunks, c.stream, c.dev) : launch_moe_gated<T, 2, 8>(a, chunks, c.stream, c.dev)
-                    : many ? launch_moe_gated<T, 1, 4>(a, chunks, c.stream, c.dev) : launch_moe_gated<T, 1, 8>(a, chunks, c.stream, c.dev);
+    st = launch_moe_rows<T, false>(a, chunks, c.stream, c.dev);
     if (st != PGEMM_OK) return st;
   }
-  // eight waves where their rows of y find room in LDS
-  const bool wide = moe_down_lds(1, 8, a.M < kMoeChunk ? a.M : kMoeChunk, a.k, a.slots) <= kMoeLds;
-  return c.F < 8      ? launch_moe_down<T, 1, 4, true>(a, chunks, c.stream, c.dev)
-         : mean > 24  ? launch_moe_down<T, 4, 4>(a, chunks, c.stream, c.dev)
-         : mean > 8   ? launch_moe_down<T, 2, 4>(a, chunks, c.stream, c.dev)
-         : wide       ? launch_moe_down<T, 1, 8>(a, chunks, c.stream, c.dev)
-                      : launch_moe_down<T, 1, 4>(a, chunks, c.stream, c.dev);
+  st = launch_moe_rows<T, true>(a, chunks, c.stream, c.dev);
+  if (st != PGEMM_OK || c.top_k == 1) return st;
+  hipLaunchKernelGGL(moe_sum_kernel<T>, dim3(row_grid(c.M * per(c.D, 4) * 4)), dim3(64), 0, c.stream, a);
+  return launched();
 }
 
 }  // namespace launch_detail

@@ -82,42 +82,29 @@ struct I8Call {
 };
 
 // The mixture of experts takes tokens in chunks.
-constexpr int64_t kMoeChunkTokens = 64, kMoeMaxExperts = 1024, kMoeMaxTop = 32, kMoeMaxTokens = 32768, kMoeMaxSplits = 8;
-constexpr int64_t kMoeDownColumns = 32;  // of a workgroup of the second products
+constexpr int64_t kMoeChunkTokens = 64, kMoeMaxExperts = 1024, kMoeMaxTop = 32, kMoeMaxTokens = 32768;
 // hidden values, so that those of a chunk's choices stay below 2^31 bytes
 constexpr int64_t kMoeMaxHidden = (int64_t)1 << 17;
 
 struct MoePlan {
   int64_t slots;    // experts a chunk may reach, or, if fewer, its choices
   bool by_choice;
-  int64_t splits;   // workgroups that share 32 columns of y
-  int64_t groups;   // such columns of all chunks
-  int64_t logits, experts, weights, h, tops, counts, lists, partial, arrived;  // workspace offsets
+  int64_t logits, experts, weights, h, tops, products;  // workspace offsets
   int64_t bytes;
 };
 
 inline MoePlan plan_moe(int64_t M, int64_t E, int64_t D, int64_t F, int64_t top_k) {
   MoePlan p{};
   Carver c;
-  const int64_t chunks = per(M, kMoeChunkTokens), most = (M < kMoeChunkTokens ? M : kMoeChunkTokens) * top_k;
+  const int64_t most = (M < kMoeChunkTokens ? M : kMoeChunkTokens) * top_k;
   p.by_choice = most < E;
   p.slots = p.by_choice ? most : E;
-  // The second products run in as many workgroups as give each CU two, but none with less than two blocks of K a wave
-  // (eight of them) where every choice is of another expert.
-  p.groups = per(D, kMoeDownColumns) * chunks;
-  const int64_t blocks = (M * top_k < E ? M * top_k : E) * per(F, 128);
-  p.splits = p.groups > 0 ? 512 / p.groups : 1;
-  if (p.splits > blocks / 16) p.splits = blocks / 16;
-  p.splits = p.splits < 1 ? 1 : p.splits > kMoeMaxSplits ? kMoeMaxSplits : p.splits;
   p.logits = c.take(M * E * 8);
   p.experts = c.take(M * top_k * 4);
   p.weights = c.take(M * top_k * 4);
   p.h = c.take(M * top_k * F * 4);
   p.tops = c.take(M * top_k * 4);
-  p.counts = c.take(chunks * p.slots * 4);
-  p.lists = c.take(chunks * p.slots * kMoeChunkTokens * 2);
-  p.arrived = c.take(p.groups * 4);
-  if (p.splits > 1) p.partial = c.take(p.splits * M * D * 4);
+  if (top_k > 1) p.products = c.take(M * top_k * D * 4);
   p.bytes = c.bytes;
   return p;
 }
