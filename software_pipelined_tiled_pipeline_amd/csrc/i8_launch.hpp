@@ -83,10 +83,12 @@ pgemm_status i8_tiles(const I8Call &c, const I8Plan &p, const int8_t *q, const f
 
 template <typename T>
 pgemm_status i8_product(const I8Call &c) {
-  const I8Plan p = plan_i8(c.M, c.N, c.K, c.gated, c.x == nullptr);
+  // scales tell the kinds of tokens apart: rows of no values may have no address
+  const bool quantized = c.xs != nullptr;
+  const I8Plan p = plan_i8(c.M, c.N, c.K, c.gated, quantized);
   const int8_t *q = c.q;
   const float *xs = c.xs;
-  if (c.x && !p.own) {
+  if (!quantized && !p.own) {
     int8_t *to = reinterpret_cast<int8_t *>(c.workspace + p.q);
     float *scale = reinterpret_cast<float *>(c.workspace + p.s);
     pgemm_status st = quant_rows<T>(c.x, to, scale, c.M, c.K, c.stream);

@@ -191,9 +191,14 @@ struct Sampler {
 #pragma unroll
     for (int i = 0; i < kSampleWaves; ++i) g = s.first[i] < g ? s.first[i] : g;
     g = __builtin_amdgcn_readfirstlane(g);
-    if (g == kSampleThreads || s.found) return false;
+    if (s.found) return false;
+    if (g == kSampleThreads) {  // nothing, or a multiple of 2^16 of one value that left no carry
+      if (V <= 0xFFFF) return false;
+      packed = false;
+      return find_top();
+    }
     const uint64_t held = __ballot(count_at(g, lane) != 0);
-    const int j0 = (int)__builtin_ctzll(held);  // (a count that ran over may have left a zero, but not in all of a block)
+    const int j0 = (int)__builtin_ctzll(held);  // (if a count ran over, another key's: found below)
     top = key_at(g, j0);
     if (top > -kLowestKey<T>) return false;  // a NaN
     largest = sample_value<T>(top);
@@ -557,7 +562,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(SampleArgs a) {
       __syncthreads();
       continue;
     }
-    const SampleSettings set{u, top_p, min_p, k};
+    const SampleSettings set{u > 0.0f ? u : 0.0f, top_p, min_p, k};
     int key = row.top;
     uint32_t in = 1;
     if (!first) {
