@@ -1,6 +1,6 @@
-"""Trains a small next-token model on the fused operators, then serves it with 4-bit weights.
+"""Trains a small next-token model on the fused operators, then serves it with 4-bit or 8-bit weights.
 
-    python examples/gated_lm.py [--steps 60] [--vocab 4000]
+    python examples/gated_lm.py [--steps 60] [--vocab 4000] [--bits 8] [--temperature 0.7]
 
 The model is an embedding, one gated feed-forward block and a vocabulary head:
 
@@ -11,7 +11,9 @@ It learns a fixed successor of every token.  A training step runs the block
 its logits (pgemm_bf16_xent) and both gradients; the optimizer keeps fp32 weights.
 Serving quantizes the block and the head to 4 bits with a scale and a zero point
 per group of 32 and decodes token by token with pgemm_bf16_q4_gated and
-pgemm_bf16_q4.
+pgemm_bf16_q4; or to 8 bits with a scale per row (pgemm_bf16_quant_i8), for
+pgemm_bf16_i8_gated and pgemm_bf16_i8.  pgemm_bf16_sample takes the next token:
+the likeliest one at temperature 0.
 """
 import argparse
 import os
@@ -91,14 +93,25 @@ def train(vocab, width, hidden, tokens, steps, seed=0, report=10):
     return successor, embed, block, head, [x.item() for x in losses]
 
 
-def serve(embed, block, head, first, count):
-    """`count` tokens after each of `first`, the likeliest one every time."""
+def serve(embed, block, head, first, count, bits=4, temperature=0.0, seed=0):
+    """`count` tokens after each of `first`, the likeliest one every time at temperature 0."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    t = torch.tensor(temperature, device="cuda")
     e = embed.bfloat16()
-    b, h = quantize(block), quantize(head)
+    if bits == 4:
+        b, h = quantize(block), quantize(head)
+    else:
+        b, h = (pgemm.pgemm_bf16_quant_i8(w.bfloat16()) for w in (block, head))
     token, out = first, []
     for _ in range(count):
-        y = pgemm.pgemm_bf16_q4_gated(e[token], *b, group=GROUP)
-        token = pgemm.pgemm_bf16_q4(y, *h, group=GROUP).float().argmax(1)
+        if bits == 4:
+            y = pgemm.pgemm_bf16_q4_gated(e[token], *b, group=GROUP)
+            z = pgemm.pgemm_bf16_q4(y, *h, group=GROUP)
+        else:
+            y = pgemm.pgemm_bf16_i8_gated(e[token], *b)
+            z = pgemm.pgemm_bf16_i8(y, *h)
+        u = torch.rand(len(token), generator=gen, device="cuda")
+        token = pgemm.pgemm_bf16_sample(z, u, temperature=t)
         out.append(token)
     return torch.stack(out, 1)
 
@@ -110,17 +123,19 @@ def main(argv=None):
     ap.add_argument("--hidden", type=int, default=512)
     ap.add_argument("--tokens", type=int, default=2048)
     ap.add_argument("--steps", type=int, default=60)
+    ap.add_argument("--bits", type=int, choices=(4, 8), default=4)
+    ap.add_argument("--temperature", type=float, default=0.0)
     a = ap.parse_args(argv)
     successor, embed, block, head, losses = train(a.vocab, a.width, a.hidden, a.tokens, a.steps)
     first = torch.arange(8, device="cuda") * (a.vocab // 8)
     with torch.no_grad():
-        got = serve(embed, block, head, first, 16)
+        got = serve(embed, block, head, first, 16, a.bits, a.temperature)
     want, token = [], first
     for _ in range(16):
         token = successor[token]
         want.append(token)
     right = (got == torch.stack(want, 1)).float().mean().item()
-    print(f"loss {losses[0]:.3f} -> {losses[-1]:.3f}; 4-bit decoding: {100 * right:.0f} % of the tokens right")
+    print(f"loss {losses[0]:.3f} -> {losses[-1]:.3f}; {a.bits}-bit decoding: {100 * right:.0f} % of the tokens right")
     return losses, right
 
 

@@ -191,16 +191,12 @@ struct Sampler {
 #pragma unroll
     for (int i = 0; i < kSampleWaves; ++i) g = s.first[i] < g ? s.first[i] : g;
     g = __builtin_amdgcn_readfirstlane(g);
-    if (s.found) return false;
-    if (g == kSampleThreads) {  // nothing, or a multiple of 2^16 of one value that left no carry
-      if (V <= 0xFFFF) return false;
-      packed = false;
-      return find_top();
-    }
-    const uint64_t held = __ballot(count_at(g, lane) != 0);
+    const bool none = g == kSampleThreads;  // nothing, or a multiple of 2^16 of one value that left no carry
+    if (s.found || (none && V <= 0xFFFF)) return false;
+    const uint64_t held = none ? 1 : __ballot(count_at(g, lane) != 0);
     const int j0 = (int)__builtin_ctzll(held);  // (if a count ran over, another key's: found below)
     top = key_at(g, j0);
-    if (top > -kLowestKey<T>) return false;  // a NaN
+    if (!none && top > -kLowestKey<T>) return false;  // a NaN
     largest = sample_value<T>(top);
 
     // The shares of a block's values, equally far apart, as a polynomial of their
@@ -233,7 +229,7 @@ struct Sampler {
     // A count that runs over takes 2^16 from itself and adds at most one elsewhere: the counts' sum is then too small,
     // modulo 2^32 too, since a row has fewer logits.
     add_up(n, m, taken - n);
-    if (V > 0xFFFF && s.below != 0) {
+    if (V > 0xFFFF && (none || s.below != 0)) {
       packed = false;
       return find_top();
     }

@@ -575,3 +575,16 @@ def test_graph(pg, fmt, M):
                 assert torch.equal(a, b)
         del junk
     pg.release_workspace(side)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("temperature", [0.0, 0.7])
+def test_example_serves(pg, bits, temperature):
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import gated_lm
+    gen = torch.Generator().manual_seed(60)
+    embed, block, head = (randn(gen, n, k, scale=k ** -0.5).cuda() for n, k in ((300, 64), (192, 64), (300, 96)))
+    first = torch.arange(7, device="cuda")
+    got = gated_lm.serve(embed, block, head, first, 5, bits, temperature)
+    assert got.shape == (7, 5) and got.dtype == torch.int64 and ((got >= 0) & (got < 300)).all()
+    assert torch.equal(got, gated_lm.serve(embed, block, head, first, 5, bits, temperature))
