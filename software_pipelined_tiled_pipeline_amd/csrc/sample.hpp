@@ -30,11 +30,15 @@ struct SampleArgs {
 };
 
 constexpr int kSampleThreads = 1024, kSampleWaves = kSampleThreads / 64;
-// LDS holds the counts of all values there are, two of 16 bits in a dword: a
-// thread has a block of 64 values that lie together, whose first and second
-// halves share 32 dwords.  These are in an order of the block's own, so that a
-// wave's reads fall on different banks.  A row with more than 65535 logits of
+// LDS holds the counts of all values there are, two of 16 bits in a dword: 64
+// values whose bits follow each other share 32 dwords, which are in an order of
+// their block's own, so that a wave's reads fall on different banks.  The
+// place is made of a logit's bits as they are, which takes 13 instructions for
+// two of them (21 with the values in their order; counting is bound by them,
+// not by its atomics).  Thread t has the t-th block from the largest values
+// down: positive ones from their end on.  A row with more than 65535 logits of
 // one value is counted in 32 bits instead, in windows of 32 values a thread.
+constexpr int kPositive = kSampleThreads / 2;  // blocks of positive values
 constexpr int kWindow = 32 * kSampleThreads;  // 128 KiB
 struct SampleShared {
   uint32_t count[kWindow];
@@ -129,13 +133,17 @@ struct Sampler {
     const double d = (sample_value<T>(key) - largest) * slope;
     return d < 0.0 ? sample_exp(d, s.root) : d == 0.0 ? 1.0 : 0.0;  // a NaN: an infinite largest one, at an infinite temperature
   }
-  // How values lie in the counts: in blocks of `bins` a thread from `start` down.
+  // How values lie in the counts: in blocks of `bins` a thread, from `start` down in a window, else from the largest
+  // there is, with zero in two places, the second one empty.
   bool packed;
   int bins, start;
-  __device__ __forceinline__ int key_at(int block, int i) const { return start - block * bins - i; }
+  __device__ __forceinline__ int key_at(int block, int i) const {
+    return start - block * bins - i + (packed && block >= kPositive);
+  }
   __device__ __forceinline__ uint32_t count_at(int block, int i) const {
-    const uint32_t v = s.count[block * 32 + ((i ^ block) & 31)];
-    return packed ? v >> (i >> 5 << 4) & 0xFFFFu : v;
+    const int of = packed && block < kPositive ? block ^ (kPositive - 1) : block;
+    const uint32_t v = s.count[of * 32 + ((i ^ block) & 31)];
+    return packed ? v >> (((i >> 5) ^ (block < kPositive)) << 4) & 0xFFFFu : v;
   }
 
   __device__ __forceinline__ void clear() const {
@@ -153,35 +161,41 @@ struct Sampler {
     start = 0x7FFF;
     if (tid == 0) s.found = 0;
     __syncthreads();
+    constexpr uint32_t LOW = 0x10000u - (0x8000u + kLowestKey<T>);  // minus infinity's bits; above them, NaN with a sign
     uint32_t taken = 0;
     each<8>(0, V, tid, kSampleThreads, [&](const u32x4 &v, int) {
-      i16x2 key[4], low = {0x7FFF, 0x7FFF};
+      u16x2 most = {0, 0};
+#pragma unroll
+      for (int d = 0; d < 4; ++d) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, +v[d]));
+      const bool some = most[0] >= LOW || most[1] >= LOW;
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
-        key[d] = sample_keys(v[d]);
-        low = __builtin_elementwise_min(low, key[d]);
-      }
-      const bool some = low[0] <= kLowestKey<T> || low[1] <= kLowestKey<T>;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        // two places p = 0x7FFF - key; their dwords, p / 64 * 32 + (p ^ p / 64) % 32; 16 for the second half
-        const u16x2 p = __builtin_bit_cast(u16x2, i16x2{0x7FFF, 0x7FFF} - key[d]);
+        // dwords p / 64 * 32 + (p ^ p / 64) % 32; 16 for the second half
+        const u16x2 p = __builtin_bit_cast(u16x2, +v[d]);  // (without the +, element 0 whatever d)
         const uint32_t mixed = __builtin_bit_cast(uint32_t, p ^ (p >> 6)), half = __builtin_bit_cast(uint32_t, p >> 1);
-        const uint32_t word = (mixed & 0x001F001Fu) | (half & 0x7FE07FE0u), shift = half & 0x00100010u;
-        if (!some || key[d][0] > kLowestKey<T>) atomicAdd(&s.count[word & 0xFFFFu], 1u << (shift & 31u));
-        if (!some || key[d][1] > kLowestKey<T>) atomicAdd(&s.count[word >> 16], 1u << (shift >> 16));
+        const uint32_t word = (mixed & 0x001F001Fu) | (half & ~0x001F001Fu), shift = half & 0x00100010u;
+        if (!some || p[0] < LOW) atomicAdd(&s.count[word & 0xFFFFu], 1u << (shift & 31u));
+        if (!some || p[1] < LOW) atomicAdd(&s.count[word >> 16], 1u << (shift >> 16));
         if (some) {
-          taken += (key[d][0] > kLowestKey<T>) + (key[d][1] > kLowestKey<T>);
-          if (key[d][0] < kLowestKey<T> || key[d][1] < kLowestKey<T>) s.found = 1;  // a NaN with a sign
+          taken += (p[0] < LOW) + (p[1] < LOW);
+          if (p[0] > LOW || p[1] > LOW) s.found = 1;
         }
       }
       if (!some) taken += 8;
     });
     __syncthreads();
+    if (tid == 0) {  // minus zero is zero
+      constexpr int minus = kPositive * 32;
+      const uint32_t zeros = s.count[minus] & 0xFFFFu;
+      s.count[minus] -= zeros;
+      s.count[0] += zeros;
+    }
+    __syncthreads();
+    const uint32_t *mine = s.count + (tid < kPositive ? tid ^ (kPositive - 1) : tid) * 32;
     uint32_t n = 0;
 #pragma unroll 8
     for (int i = 0; i < 32; ++i) {
-      const uint32_t c = s.count[tid * 32 + ((i ^ tid) & 31)];
+      const uint32_t c = mine[(i ^ tid) & 31];
       n += (c & 0xFFFFu) + (c >> 16);
     }
     const uint64_t here = __ballot(n != 0);
@@ -199,18 +213,17 @@ struct Sampler {
     if (!none && top > -kLowestKey<T>) return false;  // a NaN
     largest = sample_value<T>(top);
 
-    // The shares of a block's values, equally far apart, as a polynomial of their
-    // ratio, a count and a product each.  (A block's keys are 64 q to 64 q + 63;
-    // binades begin at multiples of 64, and the last value before one, or the first
-    // of the next, is as far away as the others.)
+    // The shares of a block's values, equally far apart since binades begin at
+    // multiples of 64, as a polynomial of their ratio, a count and a product each.
     double m = 0.0;
     if (__any(n != 0)) {
       const int key = key_at(tid, 0);
       const double r = sample_exp((sample_value<T>(key - 1) - sample_value<T>(key)) * slope, s.root);
+      const int near = tid < kPositive ? 16 : 0;  // the first 32 values' counts
       double far = 0.0, r32 = r;
 #pragma unroll 8
       for (int i = 31; i >= 0; --i) {
-        const uint32_t c = s.count[tid * 32 + ((i ^ tid) & 31)];
+        const uint32_t v = mine[(i ^ tid) & 31], c = __builtin_rotateright32(v, near);
         m = __builtin_fma(m, r, (double)(c & 0xFFFFu));
         far = __builtin_fma(far, r, (double)(c >> 16));
       }
