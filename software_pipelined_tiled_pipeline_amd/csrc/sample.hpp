@@ -115,16 +115,34 @@ struct Sampler {
     }
     return v;
   }
-  // f of eight logits and their first one's index, over a run of the row by threads `first`, first + step, ..;
-  // U loads are on the way at once.
-  template <int U, typename F>
-  __device__ __forceinline__ void each(int from, int to, int first, int step, F &&f) const {
-    for (int base = from + first * 8; base < to; base += U * step * 8) {
+  // f of eight logits, over a run of the row by threads `first`, first + step, ..; U loads are on the way at once,
+  // without a branch between them.  Where f returns true, `rare` gets each two of them again and the first one's
+  // index: its code is there once, and not between the steps that are taken every time.
+  template <int U, typename F, typename R>
+  __device__ __forceinline__ void each(int from, int to, int first, int step, F &&f, R &&rare) const {
+    const int n = (to - from) / 8;
+    uint32_t again = 0;
+#pragma unroll 1
+    for (int i0 = first; i0 <= n; i0 += U * step) {
       u32x4 v[U];
+      if (i0 < n) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) v[i] = eight(base + i * step * 8 < to ? base + i * step * 8 : V);
+        for (int i = 0; i < U; ++i) v[i] = *reinterpret_cast<const u32x4_any *>(row + from + (i0 + i * step < n ? i0 + i * step : i0) * 8);
 #pragma unroll
-      for (int i = 0; i < U; ++i) f(v[i], base + i * step * 8);
+        for (int i = 0; i < U; ++i)
+          if (i0 + i * step < n && f(v[i])) again |= 1u << i;
+      }
+      if (from + n * 8 < to && (unsigned)(n - i0) % step == 0 && (n - i0) / step < U) again |= 1u << (n - i0) / step;
+      while (again) {
+        const int base = from + (i0 + __builtin_ctz(again) * step) * 8;
+        again &= again - 1;
+        u32x4 w = eight(base);
+#pragma unroll 1
+        for (int d = 0; d < 4; ++d) {
+          rare(w[0], base + 2 * d);
+          w = u32x4{w[1], w[2], w[3], 0u};
+        }
+      }
     }
   }
 
@@ -163,26 +181,36 @@ struct Sampler {
     __syncthreads();
     constexpr uint32_t LOW = 0x10000u - (0x8000u + kLowestKey<T>);  // minus infinity's bits; above them, NaN with a sign
     uint32_t taken = 0;
-    each<8>(0, V, tid, kSampleThreads, [&](const u32x4 &v, int) {
-      u16x2 most = {0, 0};
+    auto count = [&](uint32_t two, bool both, bool lo, bool hi) {
+      // dwords p / 64 * 32 + (p ^ p / 64) % 32; 16 for the second half
+      const u16x2 p = __builtin_bit_cast(u16x2, two);
+      const uint32_t mixed = __builtin_bit_cast(uint32_t, p ^ (p >> 6)), half = __builtin_bit_cast(uint32_t, p >> 1);
+      const uint32_t word = (mixed & 0x001F001Fu) | (half & ~0x001F001Fu), shift = half & 0x00100010u;
+      if (both || lo) atomicAdd(&s.count[word & 0xFFFFu], 1u << (shift & 31u));
+      if (both || hi) atomicAdd(&s.count[word >> 16], 1u << (shift >> 16));
+    };
+    each<4>(0, V, tid, kSampleThreads,
+            [&](const u32x4 &v) {
+              u16x2 most = {0, 0}, least = {0xFFFF, 0xFFFF};
 #pragma unroll
-      for (int d = 0; d < 4; ++d) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, +v[d]));
-      const bool some = most[0] >= LOW || most[1] >= LOW;
+              for (int d = 0; d < 4; ++d) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, +v[d]));
+              if (most[0] < LOW && most[1] < LOW) {
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        // dwords p / 64 * 32 + (p ^ p / 64) % 32; 16 for the second half
-        const u16x2 p = __builtin_bit_cast(u16x2, +v[d]);  // (without the +, element 0 whatever d)
-        const uint32_t mixed = __builtin_bit_cast(uint32_t, p ^ (p >> 6)), half = __builtin_bit_cast(uint32_t, p >> 1);
-        const uint32_t word = (mixed & 0x001F001Fu) | (half & ~0x001F001Fu), shift = half & 0x00100010u;
-        if (!some || p[0] < LOW) atomicAdd(&s.count[word & 0xFFFFu], 1u << (shift & 31u));
-        if (!some || p[1] < LOW) atomicAdd(&s.count[word >> 16], 1u << (shift >> 16));
-        if (some) {
-          taken += (p[0] < LOW) + (p[1] < LOW);
-          if (p[0] > LOW || p[1] > LOW) s.found = 1;
-        }
-      }
-      if (!some) taken += 8;
-    });
+                for (int d = 0; d < 4; ++d) count(v[d], true, true, true);
+                taken += 8;
+                return false;
+              }
+              // nothing but minus infinity?
+#pragma unroll
+              for (int d = 0; d < 4; ++d) least = __builtin_elementwise_min(least, __builtin_bit_cast(u16x2, +v[d]));
+              return most[0] != LOW || most[1] != LOW || least[0] != LOW || least[1] != LOW;
+            },
+            [&](uint32_t two, int) {
+              const uint32_t lo = two & 0xFFFFu, hi = two >> 16;
+              count(two, false, lo < LOW, hi < LOW);
+              taken += (lo < LOW) + (hi < LOW);
+              if (lo > LOW || hi > LOW) s.found = 1;
+            });
     __syncthreads();
     if (tid == 0) {  // minus zero is zero
       constexpr int minus = kPositive * 32;
@@ -253,13 +281,17 @@ struct Sampler {
   __device__ __forceinline__ bool find_top() {
     i16x2 most = {-0x7FFF, -0x7FFF};
     u16x2 magnitude = {0, 0};
-    each<8>(0, V, tid, kSampleThreads, [&](const u32x4 &v, int) {
+    auto two = [&](uint32_t v) {
+      most = __builtin_elementwise_max(most, sample_keys(v));
+      magnitude = __builtin_elementwise_max(magnitude, __builtin_bit_cast(u16x2, v & 0x7FFF7FFFu));
+    };
+    each<4>(0, V, tid, kSampleThreads,
+            [&](const u32x4 &v) {
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        most = __builtin_elementwise_max(most, sample_keys(v[d]));
-        magnitude = __builtin_elementwise_max(magnitude, __builtin_bit_cast(u16x2, v[d] & 0x7FFF7FFFu));
-      }
-    });
+              for (int d = 0; d < 4; ++d) two(v[d]);
+              return false;
+            },
+            [&](uint32_t v, int) { two(v); });
     int t = most[0] > most[1] ? most[0] : most[1];
     if ((magnitude[0] > magnitude[1] ? magnitude[0] : magnitude[1]) > -kLowestKey<T>) t = 0x10000;  // a NaN
 #pragma unroll
@@ -316,20 +348,24 @@ struct Sampler {
     const uint32_t inside = all < (uint32_t)kWindow ? all : (uint32_t)kWindow;
     const i16x2 tops = {(int16_t)top, (int16_t)top};
     uint32_t below = 0;
-    each<4>(0, V, tid, kSampleThreads, [&](const u32x4 &v, int) {
+    auto count = [&](uint32_t v) {
+      const uint32_t two = __builtin_bit_cast(uint32_t, tops - sample_keys(v));
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const uint32_t two = __builtin_bit_cast(uint32_t, tops - sample_keys(v[d]));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t i = (h ? two >> 16 : two & 0xFFFFu) - skip;
-          if (i < inside)
-            atomicAdd(&s.count[(i & ~31u) | ((i ^ i >> 5) & 31u)], 1u);
-          else if (i < all)  // (places of the windows before this one have wrapped to the far end)
-            ++below;
-        }
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t i = (h ? two >> 16 : two & 0xFFFFu) - skip;
+        if (i < inside)
+          atomicAdd(&s.count[(i & ~31u) | ((i ^ i >> 5) & 31u)], 1u);
+        else if (i < all)  // (places of the windows before this one have wrapped to the far end)
+          ++below;
       }
-    });
+    };
+    each<4>(0, V, tid, kSampleThreads,
+            [&](const u32x4 &v) {
+#pragma unroll
+              for (int d = 0; d < 4; ++d) count(v[d]);
+              return false;
+            },
+            [&](uint32_t v, int) { count(v); });
     __syncthreads();
     uint32_t n = 0;
     double m = 0.0;
@@ -461,23 +497,22 @@ struct Sampler {
     __syncthreads();
     if (tid == 0) s.found = 0;
     __syncthreads();
-    each<8>(0, V, tid, kSampleThreads, [&](const u32x4 &v, int base) {
-      uint32_t t[4];
-      u16x2 least = {0xFFFF, 0xFFFF};
+    each<4>(0, V, tid, kSampleThreads,
+            [&](const u32x4 &v) {
+              u16x2 least = {0xFFFF, 0xFFFF};
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        t[d] = (v[d] ^ bits) & mask;
-        least = __builtin_elementwise_min(least, __builtin_bit_cast(u16x2, t[d]));
-      }
-      if (least[0] == 0 || least[1] == 0) {
+              for (int d = 0; d < 4; ++d) least = __builtin_elementwise_min(least, __builtin_bit_cast(u16x2, (v[d] ^ bits) & mask));
+              return least[0] == 0 || least[1] == 0;
+            },
+            [&](uint32_t two, int base) {
+              const uint32_t t = (two ^ bits) & mask;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (((t[e / 2] >> (16 * (e % 2))) & 0xFFFFu) == 0 && base + e < V) {
-            const uint32_t at = atomicAdd(&s.found, 1u);
-            if (at < kSampleThreads) list[at] = (uint32_t)(base + e);
-          }
-      }
-    });
+              for (int e = 0; e < 2; ++e)
+                if ((t >> (16 * e) & 0xFFFFu) == 0 && base + e < V) {
+                  const uint32_t at = atomicAdd(&s.found, 1u);
+                  if (at < kSampleThreads) list[at] = (uint32_t)(base + e);
+                }
+            });
     __syncthreads();
     const uint32_t n = s.found;
     if (n <= kSampleThreads) {
@@ -493,14 +528,18 @@ struct Sampler {
     }
     const int run = (V + kSampleWaves * 512 - 1) / (kSampleWaves * 512) * 512;  // a wave's, below 2^27
     const int from = wave * run, to = V - from < run ? V : from + run;
-    auto matches = [&](const u32x4 &v, int base, int e) {
-      return (((v[e / 2] ^ bits) & mask) >> (16 * (e % 2)) & 0xFFFFu) == 0 && base + e < to;
+    auto matches = [&](uint32_t two, int base, int e) {
+      return (((two ^ bits) & mask) >> (16 * e) & 0xFFFFu) == 0 && base + e < to;
     };
     uint32_t ours = 0;
-    each<8>(from, to, lane, 64, [&](const u32x4 &v, int base) {
+    auto count = [&](uint32_t two, int base) { ours += matches(two, base, 0) + matches(two, base, 1); };
+    each<8>(from, to, lane, 64,
+            [&](const u32x4 &v) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ours += matches(v, base, e);
-    });
+              for (int d = 0; d < 4; ++d) count(v[d], from);
+              return false;
+            },
+            [&](uint32_t two, int base) { count(two, base); });
     ours = wave_scan(ours);
     if (lane == 63) s.waves[wave] = ours;
     __syncthreads();
@@ -511,12 +550,12 @@ struct Sampler {
         const u32x4 v = eight(base);
         uint32_t mine = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mine += matches(v, base, e);
+        for (int e = 0; e < 8; ++e) mine += matches(v[e / 2], base + (e & ~1), e % 2);
         const uint32_t with = wave_scan(mine);
         uint32_t at = before + with - mine;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (matches(v, base, e) && ++at == which) s.answer_n = base + e;
+          if (matches(v[e / 2], base + (e & ~1), e % 2) && ++at == which) s.answer_n = base + e;
         before += (uint32_t)__shfl((int)with, 63);
       }
     }
