@@ -461,7 +461,7 @@ pgemm_status pgemm_i8_workspace(int64_t M, int64_t N, int64_t K, int gated, int 
  *   of two that keeps them in its range.  An expert that a token does not
  *   choose has no part in its result, whatever its weights hold.  A logit that
  *   is NaN comes last.
- *   E at most 1024, top_k at most 32 and E, M below 32768, D at most 2^22, F at
+ *   E at most 1024, top_k at most 32 and E, M at most 32767, D at most 2^22, F at
  *   most 2^17.  Weights are read once for every 64 tokens that reach their expert.
  */
 pgemm_status pgemm_f16_moe(const uint16_t *x, const uint16_t *router, const uint16_t *w, const uint16_t *down, uint16_t *y,

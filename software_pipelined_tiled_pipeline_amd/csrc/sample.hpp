@@ -10,6 +10,15 @@
 // and not over tokens: a row is counted by value, and a value's share is its
 // count times one exponential.  Counts do not depend on the order of their
 // atomics, and all sums are in 64 bits.
+//
+// A workgroup has a row: the sums over a row's values need all its counts, and
+// joining those of several workgroups (128 KiB each) costs more than the rest.
+// Bound by a CU's own time: of 25 us for one row of 131072 logits in bf16 about 9
+// for reading and counting (vector instructions, two logits a dozen), 5 for the
+// blocks' sums and shares, 5 for one wave's search for the borders of what is
+// kept, 3 for finding the token's index; 256 rows of 50021 in f16, one a CU, 26 us.
+// (First reading a row for its maximum, then counting below it, with an
+// exponential a value, took 121 and 157 us.)
 #pragma once
 
 #include "fused_launch.hpp"
