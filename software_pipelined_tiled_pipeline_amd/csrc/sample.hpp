@@ -61,6 +61,7 @@ struct SampleShared {
   int64_t answer_n, below;
   int answer_key;
   uint32_t answer_in, found;
+  uint32_t lowest;  // logits of the type's lowest value
 };
 
 // e^d for d <= 0 in 64 bits: 2^(n/32) from a table times a polynomial of what
@@ -97,6 +98,13 @@ __device__ __forceinline__ double sample_value(int key) {
 template <typename T>
 constexpr int kLowestKey = std::is_same_v<T, _Float16> ? -0x7C00 : -0x7F80;
 
+// Masks are often that value instead of minus infinity: a vocabulary's worth of it
+// is counted in 32 bits, and not by atomics that all meet on one dword (131072 and
+// 50021 logits, all but ten: 275 and 60 us as other values).  The last of its block:
+template <typename T>
+constexpr int kLowestBlock = kPositive + (-kLowestKey<T> - 1) / 64;
+static_assert((-kLowestKey<_Float16> - 1) % 64 == 63 && (-kLowestKey<__bf16> - 1) % 64 == 63, "");
+
 struct SampleSettings {
   float u, top_p, min_p;
   int k;
@@ -110,6 +118,7 @@ struct Sampler {
   int top;                // the largest logit's key
   double largest, slope;  // its value; 1 / temperature
   int window;             // which one is counted
+  uint32_t lowest;        // logits of the type's lowest value, of a packed row
 
   // Eight logits from an index on; minus infinity past the row's end.
   __device__ __forceinline__ u32x4 eight(int base) const {
@@ -170,6 +179,7 @@ struct Sampler {
   __device__ __forceinline__ uint32_t count_at(int block, int i) const {
     const int of = packed && block < kPositive ? block ^ (kPositive - 1) : block;
     const uint32_t v = s.count[of * 32 + ((i ^ block) & 31)];
+    if (packed && block == kLowestBlock<T> && i == 63) return lowest;
     return packed ? v >> (((i >> 5) ^ (block < kPositive)) << 4) & 0xFFFFu : v;
   }
 
@@ -186,10 +196,10 @@ struct Sampler {
     window = 0;
     bins = 64;
     start = 0x7FFF;
-    if (tid == 0) s.found = 0;
+    if (tid == 0) s.found = s.lowest = 0;
     __syncthreads();
     constexpr uint32_t LOW = 0x10000u - (0x8000u + kLowestKey<T>);  // minus infinity's bits; above them, NaN with a sign
-    uint32_t taken = 0;
+    uint64_t aside = 0;  // how many are not counted in place, and of these, times 2^32, the lowest values
     auto count = [&](uint32_t two, bool both, bool lo, bool hi) {
       // dwords p / 64 * 32 + (p ^ p / 64) % 32; 16 for the second half
       const u16x2 p = __builtin_bit_cast(u16x2, two);
@@ -203,23 +213,30 @@ struct Sampler {
               u16x2 most = {0, 0}, least = {0xFFFF, 0xFFFF};
 #pragma unroll
               for (int d = 0; d < 4; ++d) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, +v[d]));
-              if (most[0] < LOW && most[1] < LOW) {
+              if (most[0] < LOW - 1 && most[1] < LOW - 1) {
 #pragma unroll
                 for (int d = 0; d < 4; ++d) count(v[d], true, true, true);
-                taken += 8;
                 return false;
               }
-              // nothing but minus infinity?
+              // all of them minus infinity, or the lowest value?
 #pragma unroll
               for (int d = 0; d < 4; ++d) least = __builtin_elementwise_min(least, __builtin_bit_cast(u16x2, +v[d]));
-              return most[0] != LOW || most[1] != LOW || least[0] != LOW || least[1] != LOW;
+              const uint32_t all = most[0];
+              if (most[1] != all || least[0] != all || least[1] != all || all > LOW) return true;
+              aside += all < LOW ? 8ull << 32 | 8 : 8;
+              return false;
             },
             [&](uint32_t two, int) {
               const uint32_t lo = two & 0xFFFFu, hi = two >> 16;
-              count(two, false, lo < LOW, hi < LOW);
-              taken += (lo < LOW) + (hi < LOW);
+              count(two, false, lo < LOW - 1, hi < LOW - 1);
+              aside += (lo >= LOW - 1) + (hi >= LOW - 1) + ((uint64_t)((lo == LOW - 1) + (hi == LOW - 1)) << 32);
               if (lo > LOW || hi > LOW) s.found = 1;
             });
+    uint32_t low = (uint32_t)(aside >> 32);
+    if (__any(low != 0)) {
+      low = wave_scan(low);
+      if (lane == 63) atomicAdd(&s.lowest, low);
+    }
     __syncthreads();
     if (tid == 0) {  // minus zero is zero
       constexpr int minus = kPositive * 32;
@@ -235,6 +252,9 @@ struct Sampler {
       const uint32_t c = mine[(i ^ tid) & 31];
       n += (c & 0xFFFFu) + (c >> 16);
     }
+    const uint32_t lost = (tid == 0 ? ((uint32_t)V + 7) & ~7u : 0u) - (uint32_t)aside - n;  // together nothing
+    lowest = (uint32_t)__builtin_amdgcn_readfirstlane((int)s.lowest);
+    if (tid == kLowestBlock<T>) n += lowest;
     const uint64_t here = __ballot(n != 0);
     if (lane == 0) s.first[wave] = here ? wave * 64 + __builtin_ctzll(here) : kSampleThreads;
     __syncthreads();
@@ -258,11 +278,13 @@ struct Sampler {
       const double r = sample_exp((sample_value<T>(key - 1) - sample_value<T>(key)) * slope, s.root);
       const int near = tid < kPositive ? 16 : 0;  // the first 32 values' counts
       double far = 0.0, r32 = r;
+      uint32_t last = tid == kLowestBlock<T> ? lowest : 0;  // more of the last value
 #pragma unroll 8
       for (int i = 31; i >= 0; --i) {
         const uint32_t v = mine[(i ^ tid) & 31], c = __builtin_rotateright32(v, near);
         m = __builtin_fma(m, r, (double)(c & 0xFFFFu));
-        far = __builtin_fma(far, r, (double)(c >> 16));
+        far = __builtin_fma(far, r, (double)((c >> 16) + last));
+        last = 0;
       }
 #pragma unroll
       for (int i = 0; i < 5; ++i) r32 *= r32;
@@ -276,9 +298,9 @@ struct Sampler {
         if (tid == g) m = of_g;
       }
     }
-    // A count that runs over takes 2^16 from itself and adds at most one elsewhere: the counts' sum is then too small,
+    // A 16-bit count that runs over takes 2^16 from itself and adds at most one elsewhere: the counts' sum is then too small,
     // modulo 2^32 too, since a row has fewer logits.
-    add_up(n, m, taken - n);
+    add_up(n, m, lost);
     if (V > 0xFFFF && (none || s.below != 0)) {
       packed = false;
       return find_top();
@@ -542,7 +564,7 @@ struct Sampler {
     };
     uint32_t ours = 0;
     auto count = [&](uint32_t two, int base) { ours += matches(two, base, 0) + matches(two, base, 1); };
-    each<8>(from, to, lane, 64,
+    each<4>(from, to, lane, 64,
             [&](const u32x4 &v) {
 #pragma unroll
               for (int d = 0; d < 4; ++d) count(v[d], from);
@@ -579,7 +601,7 @@ template <typename T>
 __device__ __attribute__((noinline)) void sample_wide(SampleShared &s, const uint16_t *logits, int V, int top, double slope,
                                                       SampleSettings set) {
   const int tid = threadIdx.x;
-  Sampler<T> row{s, logits, V, tid, tid & 63, tid >> 6, top, sample_value<T>(top), slope, -1, false, 0, 0};
+  Sampler<T> row{s, logits, V, tid, tid & 63, tid >> 6, top, sample_value<T>(top), slope, -1, 0, false, 0, 0};
   const auto f = row.choose(set, [&](auto what, int64_t want, double mass) { return row.find(what, want, mass); });
   if (tid == 0) {
     s.answer_key = f.key;
@@ -592,9 +614,13 @@ template <typename T>
 __global__ void __launch_bounds__(kSampleThreads) sample_kernel(SampleArgs a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   SampleShared &s = *reinterpret_cast<SampleShared *>(smem);
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  if (tid < 32) s.root[tid] = exp2((double)tid / 32.0);
+  if (threadIdx.x < 32) s.root[threadIdx.x] = exp2((double)threadIdx.x / 32.0);
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+    // What follows from these is worked out for every row: ahead of the loop, which most workgroups run through once, it
+    // would take more registers than there are.
+    int tid = threadIdx.x, V = a.V;
+    asm volatile("" : "+v"(tid), "+s"(V));
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     auto at = [&](int bit) { return a.shared & bit ? 0 : m; };
     const float u = a.u[m];
     const float t = a.temperature ? a.temperature[at(PGEMM_SAMPLE_TEMPERATURE)] : 1.0f;
@@ -602,7 +628,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(SampleArgs a) {
     const float top_p = a.top_p ? a.top_p[at(PGEMM_SAMPLE_TOP_P)] : 1.0f;
     const float min_p = a.min_p ? a.min_p[at(PGEMM_SAMPLE_MIN_P)] : 0.0f;
 
-    Sampler<T> row{s, a.logits + m * a.V, a.V, tid, lane, wave, 0, 0.0, 1.0, -1, false, 0, 0};
+    Sampler<T> row{s, a.logits + m * V, V, tid, lane, wave, 0, 0.0, 1.0, -1, 0, false, 0, 0};
     const bool first = t == 0.0f || top_p <= 0.0f || min_p > 1.0f || k == 1;  // nothing to choose
     row.slope = 1.0 / (double)t;
     bool good = t >= 0.0f && top_p == top_p && min_p == min_p && u == u;

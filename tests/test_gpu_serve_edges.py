@@ -193,6 +193,19 @@ def test_quant_of_infinities_and_nan(pg, fmt, K):
         assert torch.isnan(y).all(1).tolist() == [r % 2 == 0 for r in rows] and torch.isfinite(y[1::2]).all()
 
 
+def test_quant_offsets_past_32_bits(pg):
+    M, K = 70001, 65540
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(23)
+    for m in range(0, M, 5000):
+        x[m:m + 5000] = torch.randn(min(5000, M - m), K, generator=gen, device="cuda")
+    q, s = pg.pgemm_bf16_quant_i8(x)
+    some = [0, 1, 32767, 32768, 65535, 70000]
+    want = ref.quant(x[some])
+    assert torch.equal(s[some], want[1])
+    equal("q", q[some], want[0])
+
+
 @pytest.mark.parametrize("fmt", FMT)
 @pytest.mark.parametrize("M", [3, 20, 300])
 def test_i8_largest_sums(pg, fmt, M):
@@ -395,6 +408,27 @@ def test_sample_counts_past_16_bits(pg, fmt):
     k[::3] *= 2000
     for kw in ({}, dict(temperature=t, top_k=k, top_p=p, min_p=q), dict(top_p=p), dict(temperature=t.clamp(min=0.5), min_p=q)):
         equal("token", sampled(pg, fmt, z, u, **kw), ref.sample(z.to(TYPES[fmt]), u, **kw))
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("V", [300, 65601, 140001])
+def test_sample_masked_by_the_lowest_value(pg, fmt, V):
+    gen = torch.Generator().manual_seed(V)
+    M = 12
+    low = torch.finfo(TYPES[fmt]).min
+    z = torch.full((M, V), low)
+    for m in range(1, M):  # row 0 has nothing else
+        at = torch.randperm(V, generator=gen)[:2 ** m // 4 + 1]
+        z[m, at] = randn(gen, len(at), scale=low / -9 if m % 3 else 2.0)  # to half of the type's range, or ordinary logits
+    z[5, torch.randperm(V, generator=gen)[:V // 3]] = -math.inf
+    u = torch.rand(M, generator=gen)
+    u[3:6] = 1 - 2.0 ** -24
+    t, k, p, q = settings(gen, M)
+    k[::2] = V // 2 + 7
+    for T in (1.0, 0.01, -low / 30, -low * 100 if fmt == "f16" else math.inf, math.inf):
+        T = torch.full((M,), T)
+        for kw in ({}, dict(top_k=k), dict(top_p=p), dict(min_p=q), dict(top_k=k, top_p=p, min_p=q)):
+            equal(f"T {T[0]} {list(kw)}", sampled(pg, fmt, z, u, temperature=T, **kw), ref.sample(z.to(TYPES[fmt]), u, temperature=T, **kw))
 
 
 @pytest.mark.parametrize("fmt", FMT)
