@@ -13,10 +13,10 @@
 //
 // A workgroup has a row: the sums over a row's values need all its counts, and
 // joining those of several workgroups (128 KiB each) costs more than the rest.
-// Bound by a CU's own time: of 25 us for one row of 131072 logits in bf16 about 9
+// Bound by a CU's own time: of 24 us for one row of 131072 logits in bf16 about 9
 // for reading and counting (vector instructions, two logits a dozen), 5 for the
 // blocks' sums and shares, 5 for one wave's search for the borders of what is
-// kept, 3 for finding the token's index; 256 rows of 50021 in f16, one a CU, 26 us.
+// kept, 3 for finding the token's index; 256 rows of 50021 in f16, one a CU, 23 us.
 // (First reading a row for its maximum, then counting below it, with an
 // exponential a value, took 121 and 157 us.)
 #pragma once
@@ -99,8 +99,9 @@ template <typename T>
 constexpr int kLowestKey = std::is_same_v<T, _Float16> ? -0x7C00 : -0x7F80;
 
 // Masks are often that value instead of minus infinity: a vocabulary's worth of it
-// is counted in 32 bits, and not by atomics that all meet on one dword (131072 and
-// 50021 logits, all but ten: 275 and 60 us as other values).  The last of its block:
+// is counted in 32 bits, and not by atomics that all meet on one dword (rows of
+// 131072 and 50021, all but ten: 19 and 21 us, 275 and 60 as other values).  The last
+// of its block:
 template <typename T>
 constexpr int kLowestBlock = kPositive + (-kLowestKey<T> - 1) / 64;
 static_assert((-kLowestKey<_Float16> - 1) % 64 == 63 && (-kLowestKey<__bf16> - 1) % 64 == 63, "");
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(SampleArgs a) {
   if (threadIdx.x < 32) s.root[threadIdx.x] = exp2((double)threadIdx.x / 32.0);
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     // What follows from these is worked out for every row: ahead of the loop, which most workgroups run through once, it
-    // would take more registers than there are.
+    // would take more registers than there are (26.6 us with their spills, 21.8 without, 256 rows of 50021).
     int tid = threadIdx.x, V = a.V;
     asm volatile("" : "+v"(tid), "+s"(V));
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
