@@ -193,6 +193,15 @@ def test_quant_of_infinities_and_nan(pg, fmt, K):
         assert torch.isnan(y).all(1).tolist() == [r % 2 == 0 for r in rows] and torch.isfinite(y[1::2]).all()
 
 
+@pytest.mark.parametrize("M,K", [(3000001, 5), (300001, 24), (40001, 1100), (17001, 4100)])
+def test_quant_more_rows_than_a_launch_has_groups(pg, M, K):
+    x = torch.randn(M, K, generator=torch.Generator(device="cuda").manual_seed(K), device="cuda").half()
+    q, s = pg.pgemm_f16_quant_i8(x)
+    want = ref.quant(x)
+    assert torch.equal(s, want[1])
+    equal("q", q, want[0])
+
+
 def test_quant_offsets_past_32_bits(pg):
     M, K = 70001, 65540
     x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
@@ -514,6 +523,23 @@ def test_sample_offsets_past_32_bits(pg):
     got = pg.pgemm_bf16_sample(z, u, top_k=k)
     some = [0, 1, 16383, 16384, 16999]
     equal("token", got[some].cpu(), ref.sample(z[some].cpu(), u[some].cpu(), top_k=k.cpu()))
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_sample_more_rows_than_workgroups(pg, fmt):
+    # a workgroup's second row, after one of any kind (taken, refused, greedy): the same tokens as the first time
+    gen = torch.Generator().manual_seed(24)
+    n, V = 65536, 70
+    z, u = randn(gen, n, V, scale=2.0), torch.rand(n, generator=gen)
+    t = torch.rand(n, generator=gen) * 2
+    z[::7] = -math.inf
+    z[3::11, 5] = math.nan
+    t[::5] = 0
+    turn = torch.randperm(n, generator=gen)
+    got = sampled(pg, fmt, torch.cat([z, z[turn]]), torch.cat([u, u[turn]]), temperature=torch.cat([t, t[turn]]))
+    assert torch.equal(got[n:], got[:n][turn])
+    some = torch.cat([torch.arange(200), torch.arange(n - 200, n)])
+    equal("token", got[some], ref.sample(z[some].to(TYPES[fmt]), u[some], temperature=t[some]))
 
 
 # ------------------------------------------------------------ together
