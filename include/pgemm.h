@@ -456,9 +456,10 @@ pgemm_status pgemm_i8_workspace(int64_t M, int64_t N, int64_t K, int gated, int 
  *   int32 [M, top_k] and weights: fp32 [M, top_k], what was chosen and p, each
  *   may be NULL; act: a pgemm_act.
  *   The logits are sums in 64 bits, so that the choice does not depend on
- *   their order.  The products of the gated block are fp32; its values are
- *   rounded to the 16-bit type for the second product, in f16 after a power
- *   of two that keeps them in its range.  An expert that a token does not
+ *   their order.  The products of the gated block are fp32; its values go
+ *   into the second product as the sum of two numbers of the 16-bit type (off
+ *   by 2^-16 of them in bf16; in f16 by 2^-22, or 2^-39 of a choice's largest,
+ *   after a power of two that keeps them in range).  An expert that a token does not
  *   choose has no part in its result, whatever its weights hold.  A logit that
  *   is NaN comes last.
  *   E at most 1024, top_k at most 32 and E, M at most 32767, D at most 2^22, F at

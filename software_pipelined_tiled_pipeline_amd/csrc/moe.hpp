@@ -24,7 +24,7 @@ struct MoeArgs {
   int32_t *experts;    // [M][k]
   float *weights;      // [M][k]
   double *logits;      // [M][E]
-  char *h;             // [M k][F]: T, or fp32 where T is f16
+  char *h;             // [M k][F] fp32 where T is f16, else [M k][2][F]: the values in T, and their rests
   uint32_t *tops;      // [M k] largest |h|, f16 only
   float *products;     // [M k][D] second products, times the choices' weights
   int M, E, D, F, k, slots;
@@ -33,10 +33,16 @@ struct MoeArgs {
   bool normalize;
 };
 
-// The hidden values are multiplied again on the matrix units and rounded to T
-// for that.  binary16 ends at 65504, which h may pass where y does not: in f16
-// they are kept in fp32 with each choice's largest, and rounded after a power
-// of two that takes this into [2^14, 2^15).
+// The hidden values are multiplied again on the matrix units, as two numbers of
+// 16 bits: what they round to in T, and what that leaves, rounded (2^-16 of them
+// is lost in bf16, 2^-22 in f16; with the first alone results were off by half as
+// much again as by their own rounding).  Both are rows of the second products,
+// one after the other, and the sums of both are added at the end: eight tokens
+// are a block of 16 rows.  One token's products take as long as with one part
+// (16.5 us for 84 MB), since their rows were there.
+// binary16 ends at 65504, which h may pass where y does not: in f16 they are
+// kept in fp32 with each choice's largest, and split after a power of two that
+// takes this into [2^14, 2^15).
 template <typename T>
 constexpr bool kWideHidden = std::is_same_v<T, _Float16>;
 
@@ -204,12 +210,12 @@ __device__ __forceinline__ int moe_exponent(uint32_t top) {
 }
 
 // waves a SIMD holds by their registers
-constexpr int moe_per_simd(int mt, bool wide) { return (mt == 1 ? 4 : mt == 2 ? 3 : 2) - (wide ? 1 : 0); }
+constexpr int moe_per_simd(int mt) { return mt == 1 ? 4 : mt == 2 ? 3 : 2; }
 
 // The gated blocks and, DOWN, the second products.  A workgroup has an expert's 16
 // gate rows and the same 16 up rows, or 32 rows of its second matrix; its waves take blocks
-// of K in turn and join their sums in LDS.  More than 16 MT tokens of an expert take
-// another pass over these weights.  SHORT: rows of less than eight values.
+// of K in turn and join their sums in LDS.  More than 16 MT tokens of an expert (DOWN:
+// 8 MT) take another pass over these weights.  SHORT: rows of less than eight values.
 //
 // (Second products that a workgroup sums over all experts in LDS save the last
 // launch, but leave little LDS for weights on the way, and few workgroups: 49 us
@@ -221,7 +227,7 @@ constexpr int moe_per_simd(int mt, bool wide) { return (mt == 1 ? 4 : mt == 2 ? 
 // 450 MB, 5.1 TB/s, and 67 us for 225 MB, 3.3 TB/s, where weight rows start on odd
 // multiples of two bytes and the tokens' are fp32.
 template <typename T, int MT, int WAVES, bool DOWN, bool SHORT>
-__global__ void __launch_bounds__(WAVES * 64, moe_per_simd(MT, DOWN && kWideHidden<T>)) moe_rows_kernel(MoeArgs a) {
+__global__ void __launch_bounds__(WAVES * 64, moe_per_simd(SHORT ? 4 : MT)) moe_rows_kernel(MoeArgs a) {
   constexpr int NT = 2, VALS = MT * NT * 4;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   uint16_t *list = reinterpret_cast<uint16_t *>(smem);  // [64]
@@ -236,6 +242,7 @@ __global__ void __launch_bounds__(WAVES * 64, moe_per_simd(MT, DOWN && kWideHidd
   const int expert = a.by_choice ? __builtin_amdgcn_readfirstlane(experts[slot]) : slot;
   const int K = DOWN ? a.F : a.D, rows = DOWN ? a.D : a.F;  // of a weight row; of a matrix
   constexpr bool WIDE = DOWN && kWideHidden<T>;
+  constexpr int PARTS = DOWN ? 2 : 1;  // rows of a token
   using Stream = RowStream<Frag8<T>, MT, NT, WIDE ? Tokens::Wide : Tokens::Rows, T>;
   Stream job;
   job.init(lane, K, reinterpret_cast<char *>(sums) + wave * stream_bytes(MT));
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(WAVES * 64, moe_per_simd(MT, DOWN && kWideHidd
 #pragma unroll
     for (int i = 0; i < 4; ++i) job.wo[b][i] = block_row(row0, 4 * i + (lane >> 4), rows, pitch);
   }
-  job.x = DOWN ? a.h + (int64_t)t0 * a.k * a.F * (WIDE ? 4 : 2) : reinterpret_cast<const char *>(a.x + (int64_t)t0 * a.D);
+  job.x = DOWN ? a.h + (int64_t)t0 * a.k * a.F * 4 : reinterpret_cast<const char *>(a.x + (int64_t)t0 * a.D);
   const bool streams = !SHORT && wave < blocks;
   // weights are on the way while the expert's tokens are found (a slot of a choice has some, but for a second choice of
   // its expert)
@@ -272,18 +279,19 @@ __global__ void __launch_bounds__(WAVES * 64, moe_per_simd(MT, DOWN && kWideHidd
   __syncthreads();
   const int n = __builtin_amdgcn_readfirstlane(*found);
   if (n == 0) return;
+  auto choice_at = [&](int i) -> int { return list[i < n ? i : n - 1]; };
 
   const int c = lane & 15, q = lane >> 4;
   auto same = []() {};
-  for (int first = 0; first < n; first += 16 * MT) {
-    job.have = n - first;
+  for (int first = 0; first < n; first += 16 * MT / PARTS) {
+    job.have = (n - first) * (WIDE ? 1 : PARTS);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = first + 16 * m + 4 * r + (lane >> 4);
-        const int choice = list[i < n ? i : n - 1];
-        job.xo[m][r] = (uint32_t)(DOWN ? choice : choice / a.k) * (uint32_t)K * (WIDE ? 4u : 2u);
+      for (int r = 0; r < Stream::XL; ++r) {
+        const int row = 4 * (Stream::XL * m + r) + (lane >> 4), choice = choice_at(first + (WIDE ? row : row / PARTS));
+        job.xo[m][r] = WIDE ? (uint32_t)choice * (uint32_t)K * 4u
+                            : (uint32_t)(DOWN ? choice * PARTS + row % PARTS : choice / a.k) * (uint32_t)K * 2u;
         if constexpr (WIDE) job.scale[m][r] = ldexpf(1.0f, moe_exponent(a.tops[(int64_t)t0 * a.k + choice]));
       }
     job.clear();
@@ -308,20 +316,23 @@ __global__ void __launch_bounds__(WAVES * 64, moe_per_simd(MT, DOWN && kWideHidd
 #pragma unroll
         for (int r = 0; r < 4; ++r) sums[(wave * VALS + (m * NT + b) * 4 + r) * 64 + lane] = job.tot[m][b][r];
     __syncthreads();
-    constexpr int OB = DOWN ? NT : 1;
-    for (int i = wave; i < MT * OB * 4; i += WAVES) {
-      const int m = i / (OB * 4), b = i / 4 % OB, r = i % 4, place = first + 16 * m + 4 * q + r, col = n0 + 16 * b + c;
-      if (first + 16 * m + r >= n) continue;  // no token in any lane
-      auto joined = [&](int of) {
+    constexpr int OB = DOWN ? NT : 1, TOKENS = 4 / PARTS;  // of a lane's four sums
+    for (int i = wave; i < MT * OB * TOKENS; i += WAVES) {
+      const int m = i / (OB * TOKENS), b = i / TOKENS % OB, r = i % TOKENS, col = n0 + 16 * b + c;
+      const int place = first + (4 * m + q) * TOKENS + r;
+      if (first + 4 * m * TOKENS + r >= n) continue;  // no token in any lane
+      auto joined = [&](int of, int part) {
         float v = 0.0f;
 #pragma unroll
-        for (int u = 0; u < WAVES; ++u) v += sums[(u * VALS + (m * NT + of) * 4 + r) * 64 + lane];
+        for (int u = 0; u < WAVES; ++u) v += sums[(u * VALS + (m * NT + of) * 4 + r * PARTS + part) * 64 + lane];
         return v;
       };
       const bool in = place < n && col < rows;
-      const int64_t choice = (int64_t)t0 * a.k + list[place < n ? place : n - 1];
+      const int64_t choice = (int64_t)t0 * a.k + choice_at(place);
       if constexpr (DOWN) {
-        float v = joined(b);
+        float v = joined(b, 0);
+        const float rest = joined(b, 1);
+        if (fabsf(v) < INFINITY) v += rest;  // an infinite weight's product has the value's sign, and not the rest's
         if constexpr (WIDE) v = ldexpf(v, -moe_exponent(a.tops[choice]));
         v *= a.weights[choice];
         if (in && a.k == 1)
@@ -330,7 +341,7 @@ __global__ void __launch_bounds__(WAVES * 64, moe_per_simd(MT, DOWN && kWideHidd
           a.products[choice * a.D + col] = v;
         continue;
       }
-      const float h = activate(a.act, joined(0)) * joined(1);
+      const float h = activate(a.act, joined(0, 0)) * joined(1, 0);
       if constexpr (kWideHidden<T>) {
         if (in) reinterpret_cast<float *>(a.h)[choice * a.F + col] = h;
         // of the finite ones: the others end where the definition has them end
@@ -342,7 +353,11 @@ __global__ void __launch_bounds__(WAVES * 64, moe_per_simd(MT, DOWN && kWideHidd
         }
         if (c == 0 && place < n) atomicMax(a.tops + choice, top);
       } else {
-        if (in) reinterpret_cast<uint16_t *>(a.h)[choice * a.F + col] = __builtin_bit_cast(uint16_t, (T)h);
+        uint16_t *to = reinterpret_cast<uint16_t *>(a.h) + choice * 2 * a.F + col;
+        if (in) {
+          to[0] = __builtin_bit_cast(uint16_t, (T)h);
+          to[a.F] = __builtin_bit_cast(uint16_t, (T)rest_of<T>(h));
+        }
       }
     }
     __syncthreads();

@@ -22,12 +22,12 @@ pgemm_status launch_moe_rows_one(const MoeArgs &a, int64_t chunks, hipStream_t s
   return launched();
 }
 
-// Blocks of 16 tokens by how many an expert has on average; waves along K so
-// that all workgroups together give each CU about sixteen.
+// Blocks of 16 rows (DOWN: two of a token) by how many an expert has on average;
+// waves along K so that all workgroups together give each CU about sixteen.
 template <typename T, bool DOWN>
 pgemm_status launch_moe_rows(const MoeArgs &a, int64_t chunks, hipStream_t stream, int dev) {
   if ((DOWN ? a.F : a.D) < 8) return launch_moe_rows_one<T, 1, 8, DOWN, true>(a, chunks, stream, dev);
-  const int64_t mean = (a.M < kMoeChunk ? a.M : kMoeChunk) * a.k / a.E;
+  const int64_t mean = (a.M < kMoeChunk ? a.M : kMoeChunk) * a.k * (DOWN ? 2 : 1) / a.E;
   const bool many = (DOWN ? per(a.D, 32) : per(a.F, 16)) * a.slots * chunks > 512;
   if (mean > 24) return launch_moe_rows_one<T, 4, 4, DOWN, false>(a, chunks, stream, dev);
   if (mean > 8)

@@ -31,23 +31,33 @@ struct Int8Step {
 
 // Where the tokens are: in memory like the weights; in LDS already, in whole
 // blocks, where `xl` points at this lane's fragment (token l % 16, 16-byte piece
-// l / 16); or in memory in fp32, to be rounded to T after a factor of their row.
+// l / 16); or in memory in fp32, where eight of them are a block: a row's values
+// times its factor are rounded to T for row 2 i of the block, and what that leaves
+// for row 2 i + 1.
 enum class Tokens { Rows, Lds, Wide };
 
 constexpr int kBlockBytes = 4096;  // of 16 rows
+// What rounding to T leaves of a number; nothing of an infinite one or a NaN.
+template <typename T>
+__device__ __forceinline__ float rest_of(float v) {
+  const float r = v - (float)(T)v;
+  return fabsf(r) < INFINITY ? r : 0.0f;
+}
+
 // LDS of a wave: each block of tokens, and a block of weights
 constexpr int stream_bytes(int mt) { return (mt + 1) * kBlockBytes; }
 
 template <class F, int MT, int NT, Tokens X = Tokens::Rows, typename T = void>
 struct RowStream {
   static constexpr int XP = X == Tokens::Wide ? 2 : 1;  // 16-byte pieces of a token's share
+  static constexpr int XL = X == Tokens::Wide ? 2 : 4;  // loads of a block of tokens, four of them each
 
   // Where the tokens and each block of weight rows start, the same for the wave,
   // and this lane's rows (4 i + l / 16 of each block) from there, below 2^31 bytes.
   const char *x, *w[NT];
-  uint32_t xo[MT][4], wo[NT][4];
-  float scale[MT][4];  // Wide: of x's rows
-  // Tokens there are.  The rows of a block past them are neither loaded nor put
+  uint32_t xo[MT][XL], wo[NT][4];
+  float scale[MT][XL];  // Wide: of x's rows
+  // Rows of tokens there are.  The rows of a block past them are neither loaded nor put
   // into LDS: what they hold there reaches no token's sums.
   int have;
 
@@ -56,7 +66,7 @@ struct RowStream {
   char *put_at, *get_at;  // this lane's row in the wave's LDS, as it loads and as it multiplies
   int row, part;          // that row, and 16-byte piece
   f32x4 tot[MT][NT];
-  u32x4 xr[MT][4][XP], wr[NT][4];
+  u32x4 xr[MT][XL][XP], wr[NT][4];
   const char *xl;
 
   __device__ __forceinline__ void init(int lane, int units, char *lds) {
@@ -96,6 +106,13 @@ struct RowStream {
   __device__ __forceinline__ void put(int which, int i, u32x4 v) const {
     *reinterpret_cast<u32x4 *>(put_at + which * kBlockBytes + i * 1024 + ((piece ^ (4 * i + part)) * 16)) = v;
   }
+  // A row of fp32 tokens' two.
+  __device__ __forceinline__ void put_both(int which, int i, const u32x4 (&v)[2]) const {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      *reinterpret_cast<u32x4 *>(put_at + part * 256 + which * kBlockBytes + i * 2048 + r * 256 +
+                                 ((piece ^ (8 * i + 2 * part + r)) * 16)) = v[r];
+  }
   __device__ __forceinline__ u32x4 get(int which, int s) const {
     return *reinterpret_cast<const u32x4 *>(get_at + which * kBlockBytes + (((4 * s + part) ^ row) * 16));
   }
@@ -106,8 +123,8 @@ struct RowStream {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (16 * m + 4 * i >= have) break;
+      for (int i = 0; i < XL; ++i) {
+        if (4 * (XL * m + i) >= have) break;
         if constexpr (X == Tokens::Wide) {
           xr[m][i][0] = load_at<u32x4_any>(x, xo[m][i] + 4u * k);
           xr[m][i][1] = load_at<u32x4_any>(x, xo[m][i] + 4u * k + 16u);
@@ -126,19 +143,26 @@ struct RowStream {
     for (int b = 0; b < NT; ++b) load_w(b, kb);
   }
 
-  __device__ __forceinline__ u32x4 token_piece(int m, int i) const {
+  __device__ __forceinline__ void put_tokens(int m, int i, int kb) const {
     if constexpr (X == Tokens::Wide) {
-      u32x4 v;
+      u32x4 v[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const f32x4 f = __builtin_bit_cast(f32x4, xr[m][i][e]) * scale[m][i];
-        const u32x2 two = Mfma<T>::pack4(f[0], f[1], f[2], f[3]);
-        v[2 * e] = two[0];
-        v[2 * e + 1] = two[1];
+        f32x4 f = __builtin_bit_cast(f32x4, xr[m][i][e]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) f[x] *= scale[m][i];  // (times a vector of them, it is read from scratch memory)
+        const u32x2 first = Mfma<T>::pack4(f[0], f[1], f[2], f[3]);
+        const u32x2 rest = Mfma<T>::pack4(rest_of<T>(f[0]), rest_of<T>(f[1]), rest_of<T>(f[2]), rest_of<T>(f[3]));
+        v[0][2 * e] = first[0];
+        v[0][2 * e + 1] = first[1];
+        v[1][2 * e] = rest[0];
+        v[1][2 * e + 1] = rest[1];
       }
-      return v;
+      v[0] = in_place(v[0], kb);
+      v[1] = in_place(v[1], kb);
+      put_both(m, i, v);
     } else {
-      return xr[m][i][0];
+      put(m, i, in_place(xr[m][i][0], kb));
     }
   }
 
@@ -148,19 +172,22 @@ struct RowStream {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (piece == 0) {
-          if constexpr (X == Tokens::Wide) {
-            const float *from = reinterpret_cast<const float *>(x + xo[m][i]);
+      for (int i = 0; i < XL; ++i) {
+        u32x4 v[2] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+        if constexpr (X == Tokens::Wide) {
+          const float *from = reinterpret_cast<const float *>(x + xo[m][i]);
 #pragma unroll
-            for (int e = 0; e < 7; ++e)
-              if (e < K) v[e / 2] |= Mfma<T>::pack4(from[e] * scale[m][i], 0.0f, 0.0f, 0.0f)[0] << (16 * (e % 2));
-          } else {
-            v = load_tail(reinterpret_cast<const uint16_t *>(x + xo[m][i]), 0, K);
-          }
+          for (int e = 0; e < 7; ++e)
+            if (piece == 0 && e < K) {
+              const float f = from[e] * scale[m][i];
+              v[0][e / 2] |= Mfma<T>::pack4(f, 0.0f, 0.0f, 0.0f)[0] << (16 * (e % 2));
+              v[1][e / 2] |= Mfma<T>::pack4(rest_of<T>(f), 0.0f, 0.0f, 0.0f)[0] << (16 * (e % 2));
+            }
+          put_both(0, i, v);
+        } else {
+          if (piece == 0) v[0] = load_tail(reinterpret_cast<const uint16_t *>(x + xo[m][i]), 0, K);
+          put(0, i, v[0]);
         }
-        put(0, i, v);
       }
       xs[m] = get(0, 0);
     }
@@ -186,9 +213,9 @@ struct RowStream {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (16 * m + 4 * i >= have) break;
-          put(m, i, in_place(token_piece(m, i), kb));
+        for (int i = 0; i < XL; ++i) {
+          if (4 * (XL * m + i) >= have) break;
+          put_tokens(m, i, kb);
         }
     }
     if (MORE) {
