@@ -266,9 +266,8 @@ struct Sampler {
     const bool none = g == kSampleThreads;  // nothing, or a multiple of 2^16 of one value that left no carry
     if (s.found || (none && V <= 0xFFFF)) return false;
     const uint64_t held = none ? 1 : __ballot(count_at(g, lane) != 0);
-    const int j0 = (int)__builtin_ctzll(held);  // (if a count ran over, another key's: found below)
+    const int j0 = (int)__builtin_ctzll(held);  // (if a count ran over, another key's: found below; infinity's, a NaN's)
     top = key_at(g, j0);
-    if (!none && top > -kLowestKey<T>) return false;  // a NaN
     largest = sample_value<T>(top);
 
     // The shares of a block's values, equally far apart since binades begin at
@@ -306,7 +305,7 @@ struct Sampler {
       packed = false;
       return find_top();
     }
-    return true;
+    return top <= -kLowestKey<T>;  // else a NaN
   }
 
   // The largest logit by reading the row; false as count_all.
