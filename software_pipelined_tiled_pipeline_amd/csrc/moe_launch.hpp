@@ -10,7 +10,7 @@ namespace launch_detail {
 template <typename T, int MT, int WAVES, bool DOWN, bool SHORT>
 pgemm_status launch_moe_rows_one(const MoeArgs &a, int64_t chunks, hipStream_t stream, int dev) {
   static std::atomic<uint64_t> lds_set{0};
-  constexpr int LDS = 144 + WAVES * stream_bytes(MT);
+  constexpr int LDS = WAVES * stream_bytes(MT);
   static_assert(stream_bytes(MT) >= MT * 2048 && LDS <= 160 * 1024, "the sums take the blocks' place");
   auto kern = moe_rows_kernel<T, MT, WAVES, DOWN, SHORT>;
   if (LDS > 65536) {
@@ -24,6 +24,9 @@ pgemm_status launch_moe_rows_one(const MoeArgs &a, int64_t chunks, hipStream_t s
 
 // Blocks of 16 rows (DOWN: two of a token) by how many an expert has on average;
 // waves along K so that all workgroups together give each CU about sixteen.
+// Second products, the whole layer's time: 64 tokens' two of 8 experts of
+// 4096 x 1280 in bf16 75 us in four blocks, 77 in two; their eight of 64 404 us in
+// f16 in two blocks, 412 in one.
 template <typename T, bool DOWN>
 pgemm_status launch_moe_rows(const MoeArgs &a, int64_t chunks, hipStream_t stream, int dev) {
   if ((DOWN ? a.F : a.D) < 8) return launch_moe_rows_one<T, 1, 8, DOWN, true>(a, chunks, stream, dev);
