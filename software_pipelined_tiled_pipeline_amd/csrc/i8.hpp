@@ -276,14 +276,13 @@ __global__ void __launch_bounds__(WAVES * 64) i8_few_kernel(I8Args a) {
       job.load_x(kb);
     }
   }
-  auto same = []() {};
   if (wave < blocks) {
     for (int i = wave + WAVES; i < blocks; i += WAVES) {
       const int next = block(i);
-      job.template block<true>(kb, next, same);
+      job.template block<true>(kb, next);
       kb = next;
     }
-    job.template block<false>(kb, kb, same);
+    job.template block<false>(kb, kb);
   }
   __syncthreads();
 #pragma unroll

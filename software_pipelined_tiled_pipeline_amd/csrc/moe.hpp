@@ -281,7 +281,6 @@ __global__ void __launch_bounds__(WAVES * 64, moe_per_simd(SHORT ? 4 : MT)) moe_
   auto choice_at = [&](int i) { return __shfl(listed, i < n ? i : n - 1); };
 
   const int c = lane & 15, q = lane >> 4;
-  auto same = []() {};
   for (int first = 0; first < n; first += 16 * MT / PARTS) {
     job.have = (n - first) * (WIDE ? 1 : PARTS);
 #pragma unroll
@@ -302,10 +301,10 @@ __global__ void __launch_bounds__(WAVES * 64, moe_per_simd(SHORT ? 4 : MT)) moe_
       job.load_x(kb);
       for (int i = wave + WAVES; i < blocks; i += WAVES) {
         const int next = block(i);
-        job.template block<true>(kb, next, same);
+        job.template block<true>(kb, next);
         kb = next;
       }
-      job.template block<false>(kb, kb, same);
+      job.template block<false>(kb, kb);
     }
     __syncthreads();
 #pragma unroll

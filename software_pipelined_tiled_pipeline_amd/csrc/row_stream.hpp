@@ -10,9 +10,8 @@
 // lanes to 64 bytes of a row, and the lanes changed by ds_bpermute as in
 // skinny.hpp, experts of 2050 x 1001 values took 109 and 84 us instead of 88 and
 // 76 for their two products, where they are reached by 37 tokens four times each.)  The next block's
-// loads are on the way while this one is multiplied, also where the next block
-// belongs to other rows.
-//   lane l, register r of an accumulator: token 4 (l / 16) + r, weight row l % 16.
+// loads are on the way while this one is multiplied.
+//   lane l, register r of an accumulator: row 4 (l / 16) + r of the tokens, weight row l % 16.
 #pragma once
 
 #include "skinny.hpp"
@@ -205,10 +204,9 @@ struct RowStream {
     }
   }
 
-  // Block kb, while block next loads (rows of eight units and more); `move`
-  // sets the rows that it is of, if they are others.
-  template <bool MORE, typename Move>
-  __device__ __forceinline__ void block(int kb, int next, Move &&move) {
+  // Block kb, while block next loads (rows of eight units and more).
+  template <bool MORE>
+  __device__ __forceinline__ void block(int kb, int next) {
     if constexpr (X != Tokens::Lds) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -218,10 +216,7 @@ struct RowStream {
           put_tokens(m, i, kb);
         }
     }
-    if (MORE) {
-      move();
-      load_x(next);
-    }
+    if (MORE) load_x(next);
 #pragma unroll
     for (int b = 0; b < NT; ++b) {
 #pragma unroll
