@@ -202,6 +202,9 @@ def _make(fmt, dtype_name):
             if t is not None:
                 return t
         torch = fused.torch
+        for key, t in (("u", u), *zip(SETTINGS, (temperature, top_k, top_p, min_p))):
+            if not isinstance(t, torch.Tensor) and (t is not None or key == "u"):
+                raise ValueError(f"{key} must be a tensor on the logits' device, not {t!r}")
         M, V, dev = _first("logits", logits, getattr(torch, dtype_name))
         _want("u", u, torch.float32, (M,), dev)
         shared, pointers = 0, []
