@@ -22,22 +22,16 @@ pgemm_status launch_moe_rows_one(const MoeArgs &a, int64_t chunks, hipStream_t s
   return launched();
 }
 
-// Blocks of 16 rows (DOWN: two of a token) by how many an expert has on average;
-// waves along K so that all workgroups together give each CU about sixteen.
-// Second products, the whole layer's time: 64 tokens' two of 8 experts of
-// 4096 x 1280 in bf16 75 us in four blocks, 77 in two; their eight of 64 404 us in
-// f16 in two blocks, 412 in one.
 template <typename T, bool DOWN>
 pgemm_status launch_moe_rows(const MoeArgs &a, int64_t chunks, hipStream_t stream, int dev) {
   if ((DOWN ? a.F : a.D) < 8) return launch_moe_rows_one<T, 1, 8, DOWN, true>(a, chunks, stream, dev);
-  const int64_t mean = (a.M < kMoeChunk ? a.M : kMoeChunk) * a.k * (DOWN ? 2 : 1) / a.E;
-  const bool many = (DOWN ? per(a.D, 32) : per(a.F, 16)) * a.slots * chunks > 512;
-  if (mean > 24) return launch_moe_rows_one<T, 4, 4, DOWN, false>(a, chunks, stream, dev);
-  if (mean > 8)
-    return many ? launch_moe_rows_one<T, 2, 4, DOWN, false>(a, chunks, stream, dev)
-                : launch_moe_rows_one<T, 2, 8, DOWN, false>(a, chunks, stream, dev);
-  return many ? launch_moe_rows_one<T, 1, 4, DOWN, false>(a, chunks, stream, dev)
-              : launch_moe_rows_one<T, 1, 8, DOWN, false>(a, chunks, stream, dev);
+  const MoeCut cut = moe_cut(a.M, a.E, a.D, a.F, a.k, DOWN);
+  if (cut.blocks == 4) return launch_moe_rows_one<T, 4, 4, DOWN, false>(a, chunks, stream, dev);
+  if (cut.blocks == 2)
+    return cut.waves == 4 ? launch_moe_rows_one<T, 2, 4, DOWN, false>(a, chunks, stream, dev)
+                          : launch_moe_rows_one<T, 2, 8, DOWN, false>(a, chunks, stream, dev);
+  return cut.waves == 4 ? launch_moe_rows_one<T, 1, 4, DOWN, false>(a, chunks, stream, dev)
+                        : launch_moe_rows_one<T, 1, 8, DOWN, false>(a, chunks, stream, dev);
 }
 
 template <typename T>
