@@ -487,7 +487,8 @@ pgemm_status pgemm_moe_workspace(int64_t M, int64_t E, int64_t D, int64_t F, int
  *   temperature, top_p, min_p: fp32, top_k: int32; [M] values, or one for all
  *   rows where `shared` has its bit, or NULL (temperature 1, the others off);
  *   4-byte aligned, as u.  token: int64 [M].
- *   Shares and sums are in 64 bits.  Minus infinity is never taken.  A row
+ *   Shares and sums are in 64 bits, running sums off by at most 2^-45.  Minus
+ *   infinity is never taken.  A row
  *   that has nothing else, or a NaN in its logits, settings or u, or a
  *   temperature below 0, gets -1.  V at most 2^30.
  */

@@ -72,7 +72,8 @@ __device__ __forceinline__ double sample_exp(double d, const double *root) {
   const double n = __builtin_rint(d * 46.166241308446828384);         // 32 / ln 2
   double r = __builtin_fma(n, -0x1.62e42fefp-6, d);                   // ln 2 / 32: its first 33 bits,
   r = __builtin_fma(n, -0x1.473de6af278edp-39, r);                    // and the rest
-  double p = 1.0 / 120.0;  // up to r^5: 2^-48 of the result
+  double p = 1.0 / 720.0;  // up to r^6: 2^-58 of the result (to r^5, 2^-49, which a block's sum takes to the 63rd power)
+  p = __builtin_fma(p, r, 1.0 / 120.0);
   p = __builtin_fma(p, r, 1.0 / 24.0);
   p = __builtin_fma(p, r, 1.0 / 6.0);
   p = __builtin_fma(p, r, 0.5);

@@ -1,8 +1,10 @@
 """Sampling from rows with more logits of one value than 16 bits count, where
-the value is an infinity: its count's neighbour is a NaN's."""
+the value is an infinity: its count's neighbour is a NaN's; and at a border that
+the last bits of the shares' sums decide."""
 import math
 import os
 import sys
+from decimal import Decimal, localcontext
 
 import pytest
 
@@ -43,3 +45,19 @@ def test_nan_among_many_equal_logits(pg, fmt, where, value):
     z[1, where] = -math.nan
     z[2] = math.nan
     assert sampled(pg, fmt, z, torch.full((3,), 0.4)).tolist() == [-1, -1, -1]
+
+
+@pytest.mark.parametrize("fmt,first,temperature", [("bf16", 1 + 127 / 128, "0x1.828e4cp-1"), ("f16", 1 + 127 / 1024, "0x1.828e4cp-4")])
+def test_a_border_between_two_values(pg, fmt, first, temperature):
+    # 15014 logits of the largest value, and 55877 of 1, the last of the 64 values that are summed as powers of one
+    # exponential: half of all shares is more than the first ones have, by 2^-43.6 of it.  The 63rd power of an exponential
+    # that is off by 2^-52, and 64 roundings of 2^-53, are 2^-45.4
+    a, b, T = 15014, 55877, float.fromhex(temperature)
+    with localcontext() as c:
+        c.prec = 50
+        over = Decimal(b) * ((Decimal(1) - Decimal(first)) / Decimal(T)).exp() / a - 1
+        assert Decimal(2) ** Decimal("-43.7") < over < Decimal(2) ** Decimal("-43.6")
+    z = torch.cat([torch.full((a,), first), torch.full((b,), 1.0)]).repeat(2, 1)
+    z[1] = z[1].flip(0)
+    got = sampled(pg, fmt, z, torch.tensor([0.5, 0.5]), temperature=torch.tensor([T, T]))
+    assert got.tolist() == [a, 0]
