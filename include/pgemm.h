@@ -455,8 +455,8 @@ pgemm_status pgemm_i8_workspace(int64_t M, int64_t N, int64_t K, int gated, int 
  *   F gate rows and then its F up rows; down: [E, D, F]; y: [M, D]; experts:
  *   int32 [M, top_k] and weights: fp32 [M, top_k], what was chosen and p, each
  *   may be NULL; act: a pgemm_act.
- *   The logits are sums in 64 bits, so that the choice does not depend on
- *   their order.  The products of the gated block are fp32; its values go
+ *   The logits are sums in 64 bits, whose order moves them by some 2^-53 of
+ *   their terms; equal router rows have equal logits.  The products of the gated block are fp32; its values go
  *   into the second product as the sum of two numbers of the 16-bit type (off
  *   by 2^-16 of them in bf16; in f16 by 2^-22, or 2^-39 of a choice's largest,
  *   after a power of two that keeps them in range).  An expert that a token does not

@@ -48,8 +48,9 @@ constexpr bool kWideHidden = std::is_same_v<T, _Float16>;
 
 // ------------------------------------------------------------ the choice ---
 
-// Logits in 64 bits: which experts a token gets must not depend on the order
-// of the sum.  A workgroup has one expert and up to TB tokens, a thread eight
+// Logits in 64 bits, so that which experts a token gets depends on the order of
+// the sum only where logits are some 2^-53 of their terms apart; equal router rows
+// have equal logits.  A workgroup has one expert and up to TB tokens, a thread eight
 // values of K at a time, two loads ahead.
 template <typename T, int TB>
 __global__ void __launch_bounds__(256) moe_logits_kernel(MoeArgs a) {
@@ -223,8 +224,8 @@ constexpr int moe_per_simd(int mt) { return mt == 1 ? 4 : mt == 2 ? 3 : 2; }
 // bf16, 41 instead of 24 and 5 for 64 tokens' two of 8 of 4096 x 1280.)
 //
 // One token's eight choices of experts of 4096 x 1280: 31.5 us for 168 MB, 5.3 TB/s, and
-// 17 us for 84 MB, 4.9 TB/s.  37 tokens' four of 60 of 2050 x 1001 in f16: 88.5 us for
-// 450 MB, 5.1 TB/s, and 67 us for 225 MB, 3.3 TB/s, where weight rows start on odd
+// 16.5 us for 84 MB, 5.1 TB/s.  37 tokens' four of 60 of 2050 x 1001 in f16: 88 us for
+// 450 MB, 5.1 TB/s, and 51 us for 225 MB, 4.4 TB/s, where weight rows start on odd
 // multiples of two bytes and the tokens' are fp32.
 template <typename T, int MT, int WAVES, bool DOWN, bool SHORT>
 __global__ void __launch_bounds__(WAVES * 64, moe_per_simd(SHORT ? 4 : MT)) moe_rows_kernel(MoeArgs a) {

@@ -8,9 +8,9 @@
 // that start on no cache line cost few lines twice; the block goes through 4 KiB
 // of LDS of the wave's own to where the MFMAs want it, row l % 16.  (With four
 // lanes to 64 bytes of a row, and the lanes changed by ds_bpermute as in
-// skinny.hpp, experts of 2050 x 1001 values took 109 and 84 us instead of 88 and
-// 76 for their two products, where they are reached by 37 tokens four times each.)  The next block's
-// loads are on the way while this one is multiplied.
+// skinny.hpp, the gated blocks of 60 experts of 2050 x 1001 values took 109 us
+// instead of 88 for 37 tokens' four choices.)  The next block's loads are on the way
+// while this one is multiplied.
 //   lane l, register r of an accumulator: row 4 (l / 16) + r of the tokens, weight row l % 16.
 #pragma once
 

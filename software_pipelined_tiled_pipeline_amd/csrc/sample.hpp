@@ -11,8 +11,9 @@
 // count times one exponential.  Counts do not depend on the order of their
 // atomics, and all sums are in 64 bits.
 //
-// A workgroup has a row: the sums over a row's values need all its counts, and
-// joining those of several workgroups (128 KiB each) costs more than the rest.
+// A workgroup has a row.  (Several could count one, since the blocks' counts and
+// sums of shares below are linear in the counts, and would join 12 KiB each; values
+// are needed one by one only where a border falls.)
 // Bound by a CU's own time: of 24 us for one row of 131072 logits in bf16 about 9
 // for reading and counting (vector instructions, two logits a dozen), 5 for the
 // blocks' sums and shares, 5 for one wave's search for the borders of what is
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(SampleArgs a) {
   if (threadIdx.x < 32) s.root[threadIdx.x] = exp2((double)threadIdx.x / 32.0);
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     // What follows from these is worked out for every row: ahead of the loop, which most workgroups run through once, it
-    // would take more registers than there are (26.6 us with their spills, 21.8 without, 256 rows of 50021).
+    // would take more vector registers than there are (26.6 us with their spills, 21.8 without, 256 rows of 50021).
     int tid = threadIdx.x, V = a.V;
     asm volatile("" : "+v"(tid), "+s"(V));
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);

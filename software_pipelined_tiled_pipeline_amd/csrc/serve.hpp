@@ -11,10 +11,13 @@ namespace pgemm {
 constexpr int64_t kI8MaxK = ((int64_t)1 << 17) - 16;
 
 // An 8-bit product of up to 256 tokens by the kernel for few of them, or in
-// tiles, whichever takes less: microseconds, by what a workgroup's 256 bytes of K
-// were measured to take with 16, 32 or 64 tokens, where at least half of the CUs
-// have one, and by plan_tiles, or the weights' way from memory where that is
-// longer.  Measured, tiles and few tokens, for tokens x columns x K:
+// tiles, whichever is expected to take less: microseconds, by what a workgroup's 256
+// bytes of K were measured to take with 16, 32 or 64 tokens, where at least half of
+// the CUs have one, and by plan_tiles (whose times are those of 16-bit products of as
+// many bytes), or the weights' way from memory where that is longer.  The first is
+// off by a fifth where the last round of workgroups is a short one: of the sizes here
+// it takes 64 x 12288 x 4096 and 64 x 8192 x 8192 the slower way.
+// Measured, tiles and few tokens, for tokens x columns x K:
 //   8 x 4096 x 4096   10.1  6.8     64 x 12288 x 4096  20.5 22.5     128 x 4096 x 4096   15.7 10.4
 //   8 x 8192 x 8192   17.5 14.1     64 x 8192 x 8192   25.1 21.1     128 x 8192 x 8192   29.8 36.9
 //   8 x 28672 x 4096  29.4 23.1     64 x 28672 x 4096  30.4 40.0     128 x 28672 x 4096  31.9 64.4
